@@ -149,11 +149,14 @@ def _quantize(v):
 
 
 def _pack(q, code):
-    """Values and scale codes to bytes: two codes a byte, the even column's in the low half."""
+    """Values and scale codes to bytes: two codes a byte, the even column's in the low half; rows filled with zeros to whole
+    128 columns of codes (64 bytes) and whole 512 columns of scales (16 bytes)."""
     a = q.abs()
     c = torch.where(a < 2, a * 2, torch.where(a < 4, a + 2, a / 2 + 4)).to(torch.uint8) | (torch.signbit(q).to(torch.uint8) << 3)
     c = c.view(c.shape[0], -1, 2)
-    return (c[:, :, 0] | (c[:, :, 1] << 4)).contiguous(), code.to(torch.uint8)
+    c = c[:, :, 0] | (c[:, :, 1] << 4)
+    pad = torch.nn.functional.pad
+    return pad(c, (0, -c.shape[1] % 64)).contiguous(), pad(code.to(torch.uint8), (0, -code.shape[1] % 16)).contiguous()
 
 
 def _unpack(codes):
@@ -166,7 +169,7 @@ def _unpack(codes):
 
 def _scaled(q, code, cols):
     """Values times their scales, fp32 [rows, cols]."""
-    code = code.to(torch.int32)[:, :, None]
+    code = code[:, :q.shape[1], None].to(torch.int32)
     s = torch.where(code == 0, 1 << 22, code << 23).view(torch.float32)
     s = torch.where(code == 255, math.nan, s)
     return (q * s).view(q.shape[0], -1)[:, :cols]
@@ -219,7 +222,7 @@ def run(s):
         return list(tw.add_rms_norm_bwd(s["d_out"], s["residual"], s["rstd"], s["weight"], d_residual=s["d_residual"]))
     if s["op"] == "mx4_round":
         codes, scales = tw.quantize_mx4(s["value"])
-        return [tw.dequantize_mx4(codes, scales, s["cols"], dtype=s["value"].dtype), scales]
+        return [tw.dequantize_mx4(codes, scales, s["cols"], dtype=s["value"].dtype), scales[:, :-(-s["cols"] // 32)]]
     return [tw.linear_mx4(s["value"], s["codes"], s["scales"], out=s["out"])]
 
 
@@ -297,5 +300,5 @@ def exact(case, seed):
     x, _ = _exact_mx4(s["value"].double())
     c = torch.stack((s["codes"] & 15, s["codes"] >> 4), -1).flatten(1)[:, :case["cols"]].long()
     w = torch.tensor(_LEVELS + tuple(-v for v in _LEVELS), dtype=torch.float64, device=c.device)[c]
-    w = w * _power(s["scales"].long() - 127).repeat_interleave(32, 1)[:, :case["cols"]]
+    w *= _power(s["scales"].long() - 127).repeat_interleave(32, 1)[:, :case["cols"]]
     return [x @ w.T]
