@@ -149,3 +149,86 @@ class TwellGatedFFN(torch.nn.Module):
             t = t.reshape(-1)
         y = twell_ffn(x2, self.w_gate_t, self.w_up_t, self.w_down, t, self.l1_lambda, self.cfg)
         return y.reshape(*lead, y.shape[-1])
+
+
+class AddRmsNormFunction(torch.autograd.Function):
+    """r' = residual + delta and out = the RMS norm of r' times weight, through
+    libtwell's kernels both ways. Inputs are [rows, cols]; returns (r', out),
+    or out alone where delta is None (r' is then the residual itself)."""
+
+    @staticmethod
+    def forward(ctx, residual, delta, weight, eps: float, out_dtype):
+        train = any(ctx.needs_input_grad[:3])
+        residual, weight = residual.contiguous(), weight.contiguous()
+        if delta is not None:
+            delta = delta.contiguous()
+        got = tw.alloc_norm(residual, out_dtype, rstd=train)
+        if delta is None:
+            got = got._replace(residual=None)
+        tw.add_rms_norm(residual, weight, delta=delta, eps=eps, out=got)
+        ctx.set_materialize_grads(False)
+        if train:
+            ctx.save_for_backward(residual if delta is None else got.residual, got.rstd, weight)
+        ctx.delta_dtype = None if delta is None else delta.dtype
+        return got.out if delta is None else (got.residual, got.out)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *grads):
+        d_residual, d_out = grads if ctx.delta_dtype is not None else (None, grads[0])
+        residual, rstd, weight = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dw = None
+        if d_out is None:  # only the stream was used
+            dr = d_residual
+        else:
+            if d_out.dtype not in (torch.bfloat16, torch.float32):
+                d_out = d_out.float()
+            d_residual = None if d_residual is None else d_residual.contiguous()
+            dr, dw = tw.add_rms_norm_bwd(d_out.contiguous(), residual, rstd, weight, d_residual=d_residual)
+            dw = dw.to(weight.dtype)
+        return (dr if need[0] else None, dr.to(ctx.delta_dtype) if dr is not None and need[1] else None,
+                dw if need[2] else None, None, None)
+
+
+def add_rms_norm(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None):
+    """Functional form for any leading dimensions: (residual + delta, its RMS
+    norm times weight). Without delta the residual comes back as it is."""
+    shape = residual.shape
+    r2 = residual.reshape(-1, shape[-1])
+    if delta is None:
+        return residual, AddRmsNormFunction.apply(r2, None, weight, eps, out_dtype).reshape(shape)
+    if delta.shape != shape:
+        raise ValueError("delta must have the shape of the residual")
+    r, out = AddRmsNormFunction.apply(r2, delta.reshape(-1, shape[-1]), weight, eps, out_dtype)
+    return r.reshape(shape), out.reshape(shape)
+
+
+class TwellRMSNorm(torch.nn.Module):
+    """RMS norm of a residual stream with the addition in front of it:
+    forward(residual, delta=None) returns (residual + delta, norm)."""
+
+    def __init__(self, d_model: int, eps: float = 1e-6, dtype=torch.bfloat16, out_dtype=None, device="cuda"):
+        super().__init__()
+        self.eps, self.out_dtype = float(eps), out_dtype
+        self.weight = torch.nn.Parameter(torch.ones(d_model, dtype=dtype, device=device))
+
+    def forward(self, residual, delta=None):
+        return add_rms_norm(residual, self.weight, delta, self.eps, self.out_dtype)
+
+
+class TwellBlock(torch.nn.Module):
+    """The feed-forward half of a transformer layer: TwellRMSNorm in front of
+    TwellGatedFFN. forward(residual, delta=None, t=None) adds delta (what the
+    layer's attention put out, or the block before) to the stream and returns
+    (stream, y) with y in fp32, to be added by the next norm."""
+
+    def __init__(self, d_model: int, d_ff: int, l1_lambda: float = 0.0, cfg: TwellConfig = TwellConfig(),
+                 eps: float = 1e-6, dtype=torch.bfloat16, device="cuda"):
+        super().__init__()
+        self.norm = TwellRMSNorm(d_model, eps, dtype, out_dtype=dtype, device=device)
+        self.ffn = TwellGatedFFN(d_model, d_ff, l1_lambda, cfg, dtype, device)
+
+    def forward(self, residual, delta=None, t=None):
+        residual, x = self.norm(residual, delta)
+        return residual, self.ffn(x, t)

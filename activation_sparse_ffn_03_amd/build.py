@@ -15,6 +15,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_OPS = os.path.join(PKG, "csrc_ops")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtwell.so")
@@ -28,6 +29,8 @@ HIP_FLAGS = [
 ]
 SOURCES = ["twell_host.cpp", "twell_api.hip", "trace.hip", "side_stream.hip", "scan.hip", "gate_pack.hip",
            "quant.hip", "fused_fwd.hip", "up_blocked.hip", "route.hip", "bwd.hip", "noalloc.hip", "dense_rows.hip", "bwd_blocked.hip", "bwd_dense.hip"]
+# operators around the block
+OPS_SOURCES = ["ops_api.hip", "norm.hip", "norm_bwd.hip"]
 
 
 def _hipcc() -> str:
@@ -38,10 +41,11 @@ def _hipcc() -> str:
 
 
 def _compile(src: str, verbose: bool) -> str:
+    path = os.path.join(CSRC_OPS if src in OPS_SOURCES else CSRC, src)
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [_hipcc(), *HIP_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [_hipcc(), *HIP_FLAGS, "-c", path, "-o", obj]
     if src.endswith(".cpp"):
-        cmd = [_hipcc(), "-x", "hip", *HIP_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+        cmd = [_hipcc(), "-x", "hip", *HIP_FLAGS, "-c", path, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     out = "\n".join(line for line in (r.stdout + r.stderr).splitlines()
                     if "packed-fp32-ops" not in line)
@@ -55,9 +59,10 @@ def _compile(src: str, verbose: bool) -> str:
 def build(verbose: bool = False) -> str:
     """Compile every source for gfx950 and link libtwell.so; returns its path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    jobs = min(len(SOURCES), max(1, min(16, os.cpu_count() or 1)))
+    sources = SOURCES + OPS_SOURCES
+    jobs = min(len(sources), max(1, min(16, os.cpu_count() or 1)))
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        objs = list(ex.map(lambda s: _compile(s, verbose), sources))
     tmp = LIB + ".tmp"
     r = subprocess.run([_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs],
                        capture_output=True, text=True)

@@ -1,0 +1,209 @@
+// Root-mean-square norm with the residual's addition and an E4M3 output.
+//
+//   r'    = residual + delta              (fp32 sum, rounded to the stream's type as it is stored)
+//   rho   = 1 / sqrt(mean(r'^2) + eps)    (fp32)
+//   n     = r' * rho * w                  (fp32)
+//   out   = n in bf16 or fp32
+//   scale = max|n| / 448 (1 when that is not > 0), q = E4M3(n / scale)
+//
+// The norm is that of the residual as stored, so that the backward, which
+// reads the stored residual, differentiates exactly what was computed, and so
+// that adding first and norming later give the same. The codes come from the
+// fp32 n and not from the rounded out: one rounding, and for an fp32 out they
+// are bit for bit those of quantising it. The sum of squares is held in fp32
+// (rows with elements above 1.8e19 overflow it: their norm is 0).
+//
+// Bound by memory: the stream and the addition are read once, the new stream,
+// out and the codes written once; the row stays in registers between its three
+// passes (sum of squares, largest magnitude, encoding).
+#include "norm_device.h"
+#include "ops_kernels.h"
+#include "../csrc/twell_trace.h"
+
+namespace twell {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Codes of 8 quotients n / sc. With FAST the row's largest magnitude is finite
+// and its scale normal, so that every quotient is at most 448.001 and the
+// hardware conversion (nearest, ties to even) is right as it stands. Otherwise
+// quotients are held to +-448 first and NaN gets the code 0x7F.
+template <bool FAST>
+__device__ __forceinline__ u32x2_t encode8(const float (&n)[8], float sc) {
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] = n[k] / sc;
+    if constexpr (!FAST) v[k] = v[k] > 448.f ? 448.f : v[k] < -448.f ? -448.f : v[k];
+  }
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
+  u32x2_t r = {(uint32_t)lo, (uint32_t)hi};
+  if constexpr (!FAST) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int s = 8 * (k & 3);
+      if (v[k] != v[k]) r[k >> 2] = (r[k >> 2] & ~(0xFFu << s)) | (0x7Fu << s);
+    }
+  }
+  return r;
+}
+
+// 448 * 2^-126: from here the scale is a normal number.
+constexpr uint32_t kNormalScaleBits = 0x04E00000u;
+
+// TR: the stream's type; TD: the addition's (void: none). WPR waves a row, C
+// chunks of 8 elements a thread. WPR = 1: four rows a workgroup, no barrier.
+template <typename TR, typename TD, int WPR, int C, bool TAIL>
+__global__ __launch_bounds__(kThreads) void add_rms_norm_kernel(NormArgs a) {
+  constexpr int T = 64 * WPR;
+  constexpr bool ADD = !std::is_void_v<TD>;
+  using TDs = std::conditional_t<ADD, TD, TR>;
+  const int wave = threadIdx.x >> 6;
+  const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
+  if (row >= a.rows) return;  // whole waves, and with WPR > 1 whole workgroups
+  const int t = WPR == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+  const int cols = a.cols;
+  const int64_t off = row * cols;
+
+  Raw8<TR> rr[C];
+  Raw8<TDs> rd[ADD ? C : 1];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    rr[c].template load<TAIL>(static_cast<const TR*>(a.residual) + off, t + T * c, cols);
+    if constexpr (ADD) rd[c].template load<TAIL>(static_cast<const TD*>(a.delta) + off, t + T * c, cols);
+  }
+  float w[C][8];
+  load_weight<T, C, TAIL>(a.w, a.w_bf16, t, cols, w);
+
+  float x[C][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[c][k] = rr[c].get(k);
+      if constexpr (ADD) x[c][k] += rd[c].get(k);
+    }
+    if constexpr (ADD && std::is_same_v<TR, uint16_t>) {
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        const uint32_t p = pack_bf16(x[c][k], x[c][k + 1]);
+        x[c][k] = bf16lo_to_f32(p);
+        x[c][k + 1] = bf16hi_to_f32(p);
+      }
+    }
+    if (a.residual_out != nullptr)
+      store8<TAIL>(static_cast<TR*>(a.residual_out) + off, t + T * c, cols, x[c]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = fmaf(x[c][k], x[c][k], ss);
+  }
+  __shared__ float red_sum[WPR];
+  __shared__ uint32_t red_max[WPR];
+  ss = wave_sum_dpp(ss);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) red_sum[wave] = ss;
+    lds_barrier();
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < WPR; ++i) ss += red_sum[i];
+  }
+  const float rho = 1.0f / sqrtf(ss / (float)cols + a.eps);
+  if (a.rstd != nullptr && t == 0) a.rstd[row] = rho;
+
+  uint32_t mb = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[c][k] = x[c][k] * rho * w[c][k];
+      mb = max(mb, __float_as_uint(x[c][k]) & 0x7FFFFFFFu);
+    }
+  if (a.out != nullptr) {
+    if (a.out_bf16) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) store8<TAIL>(static_cast<uint16_t*>(a.out) + off, t + T * c, cols, x[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c) store8<TAIL>(static_cast<float*>(a.out) + off, t + T * c, cols, x[c]);
+    }
+  }
+  if (a.q == nullptr) return;
+
+  // Elements past the row's end hold 0 * rho * 0: 0, or NaN in a row whose rho
+  // is not finite, which cannot be (eps > 0) unless the row itself holds NaN.
+  mb = wave_max_bits(mb);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) red_max[wave] = mb;
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < WPR; ++i) mb = max(mb, red_max[i]);
+  }
+  float sc = __uint_as_float(mb) / 448.0f;
+  sc = sc > 0.f ? sc : 1.0f;  // NaN fails the test
+  if (t == 0) a.q_scale[row] = sc;
+  uint8_t* qrow = a.q + off;
+  auto encode = [&](auto fast) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int i = t + T * c;
+      const u32x2_t v = encode8<decltype(fast)::value>(x[c], sc);
+      if constexpr (!TAIL) {
+        if (8 * i < cols) *reinterpret_cast<u32x2_t*>(qrow + 8 * i) = v;
+      } else if (8 * i + 8 <= cols) {
+        *reinterpret_cast<u32x2_a1_t*>(qrow + 8 * i) = v;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 7; ++k)
+          if (8 * i + k < cols) qrow[8 * i + k] = (uint8_t)(v[k >> 2] >> (8 * (k & 3)));
+      }
+    }
+  };
+  if (mb < 0x7F800000u && mb >= kNormalScaleBits)
+    encode(std::true_type{});
+  else
+    encode(std::false_type{});
+}
+
+template <typename TR, typename TD, int WPR, int C>
+hipError_t launch_cfg(const NormArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(WPR == 1 ? (a.rows + 3) / 4 : a.rows));
+  if (a.cols % 8 == 0)
+    TWELL_LAUNCH("add_rms_norm", (add_rms_norm_kernel<TR, TD, WPR, C, false>), grid, kThreads, 0, s, a);
+  else
+    TWELL_LAUNCH("add_rms_norm", (add_rms_norm_kernel<TR, TD, WPR, C, true>), grid, kThreads, 0, s, a);
+  return hipGetLastError();
+}
+
+// Rows below which a row gets a whole workgroup instead of one wave.
+constexpr int64_t kWaveRows = 1024;
+
+template <typename TR, typename TD>
+hipError_t launch_typed(const NormArgs& a, hipStream_t s) {
+  if (a.cols <= 512) return launch_cfg<TR, TD, 1, 1>(a, s);
+  if (a.cols <= 4096 && a.rows >= kWaveRows) {
+    if (a.cols <= 1024) return launch_cfg<TR, TD, 1, 2>(a, s);
+    if (a.cols <= 2048) return launch_cfg<TR, TD, 1, 4>(a, s);
+    return launch_cfg<TR, TD, 1, 8>(a, s);
+  }
+  if (a.cols <= 2048) return launch_cfg<TR, TD, 4, 1>(a, s);
+  if (a.cols <= 4096) return launch_cfg<TR, TD, 4, 2>(a, s);
+  if (a.cols <= 8192) return launch_cfg<TR, TD, 4, 4>(a, s);
+  return launch_cfg<TR, TD, 4, 8>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_add_rms_norm(const NormArgs& a, hipStream_t s) {
+  if (a.res_bf16) {
+    if (a.delta == nullptr) return launch_typed<uint16_t, void>(a, s);
+    return a.delta_bf16 ? launch_typed<uint16_t, uint16_t>(a, s) : launch_typed<uint16_t, float>(a, s);
+  }
+  if (a.delta == nullptr) return launch_typed<float, void>(a, s);
+  return a.delta_bf16 ? launch_typed<float, uint16_t>(a, s) : launch_typed<float, float>(a, s);
+}
+
+}  // namespace twell

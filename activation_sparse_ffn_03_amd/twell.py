@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -30,7 +30,8 @@ _STATUS = {0: "TWELL_OK", 1: "TWELL_ERR_INVALID_ARG", 2: "TWELL_ERR_UNSUPPORTED"
 EXPORTS = ("twell_status_str", "twell_last_error", "twell_n_tiles", "twell_query_sizes", "twell_gate_pack",
            "twell_gate_pack_ws", "twell_pack_preact", "twell_quantize_e4m3", "twell_gate_pack_fp8",
            "twell_gate_pack_fp8_ws", "twell_ffn_fwd", "twell_ffn_forward", "twell_ffn_forward_fp8",
-           "twell_ffn_forward_noalloc", "twell_route_hybrid", "twell_ffn_bwd", "twell_trace_start",
+           "twell_ffn_forward_noalloc", "twell_route_hybrid", "twell_ffn_bwd", "twell_add_rms_norm",
+           "twell_add_rms_norm_bwd_ws", "twell_add_rms_norm_bwd", "twell_trace_start",
            "twell_trace_stop", "twell_trace_count", "twell_trace_dropped", "twell_trace_get")
 
 # Bytes of the library's static scratch used by twell_ffn_forward_noalloc.
@@ -113,6 +114,15 @@ def lib() -> ctypes.CDLL:
         L.twell_route_hybrid.argtypes = [pd, ctypes.c_int, pp, vp, ph, vp]
         L.twell_ffn_bwd.restype = ctypes.c_int
         L.twell_ffn_bwd.argtypes = [pd, ctypes.c_int, ph, vp, vp, vp, vp, vp, f32, vp, vp, vp, vp, vp, sz, vp]
+        i64 = ctypes.c_int64
+        L.twell_add_rms_norm.restype = ctypes.c_int
+        L.twell_add_rms_norm.argtypes = [i64, i32, ctypes.c_int, vp, ctypes.c_int, vp, ctypes.c_int, vp, f32, vp,
+                                         ctypes.c_int, vp, vp, vp, vp, vp]
+        L.twell_add_rms_norm_bwd_ws.restype = ctypes.c_int
+        L.twell_add_rms_norm_bwd_ws.argtypes = [i64, i32, ctypes.POINTER(sz)]
+        L.twell_add_rms_norm_bwd.restype = ctypes.c_int
+        L.twell_add_rms_norm_bwd.argtypes = [i64, i32, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp, ctypes.c_int, vp,
+                                             vp, vp, vp, sz, vp]
         L.twell_trace_start.restype = ctypes.c_int
         L.twell_trace_start.argtypes = [i32]
         L.twell_trace_stop.restype = ctypes.c_int
@@ -341,6 +351,119 @@ def ffn_bwd(dims: Dims, dtype: int, hyb: TwellHybrid, x, dy, w_gate_t, w_up_t, w
     _check(lib().twell_ffn_bwd(ctypes.byref(dims), int(dtype), ctypes.byref(h), _ptr(x), _ptr(dy), _ptr(w_gate_t),
                                _ptr(w_up_t), _ptr(w_down), ctypes.c_float(l1_lambda), _ptr(dx), _ptr(dw_gate_t),
                                _ptr(dw_up_t), _ptr(dw_down), _ptr(ws), nbytes, _stream(stream)), "twell_ffn_bwd")
+
+
+# ---------------------------------------------------------------- operators around the block
+
+_CODES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _code(t: torch.Tensor, what: str) -> int:
+    c = _CODES.get(t.dtype)
+    if c is None:
+        raise TypeError(f"{what} must be bfloat16 or float32, got {t.dtype}")
+    return c
+
+
+def _addr(t: Optional[torch.Tensor], what: str, shape, dtype=None):
+    """Device address of a contiguous tensor of the given shape (and dtype), None for None or an empty tensor."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on the GPU")
+    return t.data_ptr() or None
+
+
+class NormOut(NamedTuple):
+    """What add_rms_norm puts out; fields that were not asked for are None."""
+    residual: Optional[torch.Tensor]  # [rows, cols] r', dtype of the residual
+    out: Optional[torch.Tensor]       # [rows, cols] the norm
+    codes: Optional[torch.Tensor]     # [rows, cols] uint8 E4M3 codes of the norm
+    scale: Optional[torch.Tensor]     # [rows] fp32 scales of the codes
+    rstd: Optional[torch.Tensor]      # [rows] fp32, for the backward
+
+
+def alloc_norm(residual: torch.Tensor, out_dtype=None, codes: bool = False, rstd: bool = False) -> NormOut:
+    """Output buffers of add_rms_norm for a [rows, cols] residual."""
+    e = dict(device=residual.device)
+    rows = residual.shape[0]
+    return NormOut(torch.empty_like(residual), torch.empty(residual.shape, dtype=out_dtype or residual.dtype, **e),
+                   torch.empty(residual.shape, dtype=torch.uint8, **e) if codes else None,
+                   torch.empty(rows, dtype=torch.float32, **e) if codes else None,
+                   torch.empty(rows, dtype=torch.float32, **e) if rstd else None)
+
+
+def add_rms_norm(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None, codes: bool = False,
+                 rstd: bool = False, out=None, stream=None) -> NormOut:
+    """r' = residual + delta and its RMS norm times weight (twell_add_rms_norm).
+
+    residual [rows, cols], delta the same shape or None, weight [cols], each
+    bf16 or fp32. Without `out` the new residual and the norm (out_dtype,
+    default that of the residual) are returned, with codes=True also its E4M3
+    codes and row scales, as gate_pack_fp8 takes them, and with rstd=True what
+    add_rms_norm_bwd needs. `out`, a NormOut or five tensors in its order, each
+    None where it is not wanted, says what to write and where; out.residual may
+    be `residual` itself."""
+    if residual.dim() != 2:
+        raise ValueError("residual must be [rows, cols]")
+    shape = residual.shape
+    rows, cols = shape
+    rc = _code(residual, "residual")
+    if out is None:
+        out = alloc_norm(residual, out_dtype, codes, rstd)
+    elif not isinstance(out, NormOut):
+        out = NormOut(*out)
+    if (out.codes is None) != (out.scale is None):
+        raise ValueError("codes and scale go together")
+    row = shape[:1]
+    _check(lib().twell_add_rms_norm(
+        rows, cols, rc, _addr(residual, "residual", shape), BF16 if delta is None else _code(delta, "delta"),
+        _addr(delta, "delta", shape), _code(weight, "weight"), _addr(weight, "weight", shape[1:]), eps,
+        _addr(out.residual, "out.residual", shape, residual.dtype), F32 if out.out is None else _code(out.out, "out.out"),
+        _addr(out.out, "out.out", shape), _addr(out.codes, "out.codes", shape, torch.uint8),
+        _addr(out.scale, "out.scale", row, torch.float32), _addr(out.rstd, "out.rstd", row, torch.float32),
+        _stream(stream)), "twell_add_rms_norm")
+    return out
+
+
+def add_rms_norm_bwd_ws(rows: int, cols: int) -> int:
+    """Workspace bytes of add_rms_norm_bwd."""
+    n = ctypes.c_size_t()
+    _check(lib().twell_add_rms_norm_bwd_ws(rows, cols, ctypes.byref(n)), "twell_add_rms_norm_bwd_ws")
+    return n.value
+
+
+def add_rms_norm_bwd(d_out, residual, rstd, weight, d_residual=None, out=None, ws=None, stream=None):
+    """Gradients of add_rms_norm (twell_add_rms_norm_bwd): (dr, dw), dr that of
+    the residual and of delta alike in the residual's dtype, dw fp32. residual
+    and rstd are what the forward put out, d_out and d_residual the gradients
+    of its norm and of its new residual (None: nothing else reads that).
+    Written into `out`, a (dr, dw) pair, when given; ws (bytes of
+    add_rms_norm_bwd_ws) is allocated here when not."""
+    if residual.dim() != 2:
+        raise ValueError("residual must be [rows, cols]")
+    shape = residual.shape
+    rows, cols = shape
+    gc, rc, wc = _code(d_out, "d_out"), _code(residual, "residual"), _code(weight, "weight")
+    if out is None:
+        dr, dw = torch.empty_like(residual), torch.empty(cols, dtype=torch.float32, device=residual.device)
+    else:
+        dr, dw = out
+    args = (rows, cols, gc, _addr(d_out, "d_out", shape), rc, _addr(d_residual, "d_residual", shape, residual.dtype),
+            _addr(residual, "residual", shape), _addr(rstd, "rstd", shape[:1], torch.float32), wc,
+            _addr(weight, "weight", shape[1:]), _addr(dr, "dr", shape, residual.dtype),
+            _addr(dw, "dw", shape[1:], torch.float32))
+    if ws is None:
+        ws = torch.empty(add_rms_norm_bwd_ws(rows, cols), dtype=torch.uint8, device=residual.device)
+    _check(lib().twell_add_rms_norm_bwd(*args, ws.data_ptr() or None, ws.numel() * ws.element_size(), _stream(stream)),
+           "twell_add_rms_norm_bwd")
+    return dr, dw
 
 
 def trace_start(capacity: int = 4096) -> None:

@@ -330,6 +330,51 @@ twell_status twell_ffn_bwd(const twell_dims* dims, twell_dtype dtype, const twel
                            size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Operators around the block
+ * ------------------------------------------------------------------------- */
+
+/* Root-mean-square norm in front of the block, with the addition of what the
+ * previous layer put out (for example this block's y) to the residual stream,
+ * and E4M3 codes of the normed rows for the FP8 gate:
+ *   r'      = residual + delta, summed in fp32 and rounded to res_dtype
+ *   rho     = 1 / sqrt(mean_k(r'[i,k]^2) + eps), fp32
+ *   n[i,k]  = r'[i,k] * rho[i] * weight[k], fp32
+ *   residual_out = r',  out = n rounded to out_dtype,  rstd = rho
+ *   q_scale[i]   = max_k |n[i,k]| / 448 (1 for an all-zero row and for one
+ *                  holding NaN; inf in a row gives scale inf),
+ *   q[i,k]       = E4M3(n[i,k] / q_scale[i]), the rounding and the special
+ *                  values of twell_quantize_e4m3.
+ * The norm is that of r' as stored. The codes come from the fp32 n, so they
+ * are those of twell_quantize_e4m3 on an fp32 out. A row whose fp32 sum of
+ * squares overflows (elements above about 1.8e19) has rho = 0.
+ * residual [rows][cols] res_dtype; delta [rows][cols] delta_dtype or NULL (then
+ * r' = residual); weight [cols] weight_dtype; eps > 0. residual_out, out, q
+ * (with q_scale [rows]) and rstd [rows] may each be NULL, not all of them.
+ * residual_out may be `residual` itself (the stream updated in place); no other
+ * output may overlap an input. Any cols from 1 to 16384; rows == 0 is a no-op. */
+twell_status twell_add_rms_norm(int64_t rows, int32_t cols, twell_dtype res_dtype, const void* residual,
+                                twell_dtype delta_dtype, const void* delta, twell_dtype weight_dtype,
+                                const void* weight, float eps, void* residual_out, twell_dtype out_dtype, void* out,
+                                uint8_t* q, float* q_scale, float* rstd, void* stream);
+
+/* Workspace bytes of twell_add_rms_norm_bwd (host-only query; may be 0). */
+twell_status twell_add_rms_norm_bwd_ws(int64_t rows, int32_t cols, size_t* ws_bytes);
+
+/* Backward of twell_add_rms_norm, from the residual it stored (r') and its
+ * rstd. With xh = r' * rho and u = d_out * weight:
+ *   dr = d_residual + rho * (u - xh * mean_k(u * xh))
+ *   dw = sum_i d_out[i] * xh[i]
+ * dr is the gradient of the residual and of delta alike (res_dtype); dw is
+ * fp32, summed in a fixed order. d_out [rows][cols] d_out_dtype; d_residual
+ * [rows][cols] res_dtype, the gradient of residual_out, or NULL when nothing
+ * else reads the stream. The codes have no gradient. Both outputs are fully
+ * overwritten (rows == 0: dw = 0). ws: at least the queried bytes. */
+twell_status twell_add_rms_norm_bwd(int64_t rows, int32_t cols, twell_dtype d_out_dtype, const void* d_out,
+                                    twell_dtype res_dtype, const void* d_residual, const void* residual,
+                                    const float* rstd, twell_dtype weight_dtype, const void* weight, void* dr,
+                                    float* dw, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Tracing (diagnostics). When started, every kernel launched by the calls
  * above is bracketed by two HIP events recorded on the call's stream, so the
  * device time of each kernel can be read back afterwards. Events are created
