@@ -30,7 +30,7 @@ HIP_FLAGS = [
 SOURCES = ["twell_host.cpp", "twell_api.hip", "trace.hip", "side_stream.hip", "scan.hip", "gate_pack.hip",
            "quant.hip", "fused_fwd.hip", "up_blocked.hip", "route.hip", "bwd.hip", "noalloc.hip", "dense_rows.hip", "bwd_blocked.hip", "bwd_dense.hip"]
 # operators around the block
-OPS_SOURCES = ["ops_api.hip", "norm.hip", "norm_bwd.hip"]
+OPS_SOURCES = ["ops_api.hip", "norm.hip", "norm_bwd.hip", "mx4_quant.hip", "mx4_product.hip"]
 
 
 def _hipcc() -> str:

@@ -1,7 +1,8 @@
-// Row access shared by the norm's forward and backward kernels.
+// Row access of the operators around the block.
 //
 // A row is dealt to its threads in chunks of 8 elements (16 bytes of bf16, 32
-// of fp32): thread t of T takes chunks t, t + T, ... TAIL is set when the row
+// of fp32): thread t of T takes chunks t, t + T, ...; elements behind the row's
+// end read as zeros and are not written. TAIL is set when the row
 // length is not a multiple of 8: rows then start at any element, so chunks are
 // read and written with element-aligned vector accesses (global memory takes
 // them at any alignment on gfx950), and the row's last, partial chunk one
@@ -43,6 +44,13 @@ struct Raw8<uint16_t> {
         if (8 * i + k < cols) v[k >> 1] |= (uint32_t)p[k] << (16 * (k & 1));
     }
   }
+  // bit pattern of the largest magnitude, as fp32
+  __device__ __forceinline__ uint32_t max_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m = max(m, max((v[k] & 0x7FFFu) << 16, v[k] & 0x7FFF0000u));
+    return m;
+  }
   __device__ __forceinline__ float get(int k) const { return k & 1 ? bf16hi_to_f32(v[k >> 1]) : bf16lo_to_f32(v[k >> 1]); }
 };
 
@@ -66,6 +74,12 @@ struct Raw8<float> {
       for (int k = 0; k < 7; ++k)
         if (8 * i + k < cols) v[k >> 2][k & 3] = __float_as_uint(p[k]);
     }
+  }
+  __device__ __forceinline__ uint32_t max_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, v[k >> 2][k & 3] & 0x7FFFFFFFu);
+    return m;
   }
   __device__ __forceinline__ float get(int k) const { return __uint_as_float(v[k >> 2][k & 3]); }
 };

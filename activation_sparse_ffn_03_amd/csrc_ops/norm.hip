@@ -16,7 +16,7 @@
 // Bound by memory: the stream and the addition are read once, the new stream,
 // out and the codes written once; the row stays in registers between its three
 // passes (sum of squares, largest magnitude, encoding).
-#include "norm_device.h"
+#include "chunk8.h"
 #include "ops_kernels.h"
 #include "../csrc/twell_trace.h"
 

@@ -8,7 +8,7 @@
 // run of consecutive rows, keeps its part of dw in registers (thread t owns the
 // same columns in every row) and leaves one partial row; a second launch adds
 // the partial rows in a fixed order, so dw does not change from run to run.
-#include "norm_device.h"
+#include "chunk8.h"
 #include "ops_kernels.h"
 #include "../csrc/twell_trace.h"
 

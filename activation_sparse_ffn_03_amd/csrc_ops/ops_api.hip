@@ -46,6 +46,44 @@ size_t norm_bwd_ws_bytes(int64_t rows, int32_t cols) {
   return g == 1 ? 0 : (size_t)g * cols * 4;
 }
 
+twell_status check_mx4_shape(int64_t rows, int32_t cols) {
+  if (rows < 0 || cols <= 0) return fail(TWELL_ERR_INVALID_ARG, "rows must be >= 0 and cols > 0");
+  if (rows > 0x7FFFFFFFll) return fail(TWELL_ERR_UNSUPPORTED, "rows above 2^31 - 1");
+  if (cols > twell::kMx4MaxCols) return fail(TWELL_ERR_UNSUPPORTED, "cols above 2^20");
+  if (rows * ((cols + 511) / 512) > (1ll << 34)) return fail(TWELL_ERR_UNSUPPORTED, "rows x cols above 2^43");
+  return TWELL_OK;
+}
+
+size_t mx4_codes(int64_t rows, int32_t cols) { return (size_t)rows * twell::mx4_code_bytes(cols); }
+size_t mx4_scales(int64_t rows, int32_t cols) { return (size_t)rows * twell::mx4_scale_bytes(cols); }
+
+// Shape, weights and output shared by the products.
+twell_status check_mx4_product(int64_t n, int32_t cols, int32_t units, const uint8_t* w_q, const uint8_t* w_scale,
+                               twell_dtype y_dtype, void* y, twell::Mx4ProductArgs* a) {
+  twell_status st = check_mx4_shape(n, cols);
+  if (st != TWELL_OK) return st;
+  if (units <= 0) return fail(TWELL_ERR_INVALID_ARG, "units must be > 0");
+  if (units > (1 << 24)) return fail(TWELL_ERR_UNSUPPORTED, "units above 2^24");
+  if (((n + 15) / 16) * ((units + 15) / 16) > 0x7FFFFFFFll)
+    return fail(TWELL_ERR_UNSUPPORTED, "more than 2^31 - 1 output tiles of 16 x 16");
+  if (bad_dtype(y_dtype)) return fail(TWELL_ERR_INVALID_ARG, "dtypes must be bf16 or fp32");
+  OPS_CHECK_PTR(w_q, mx4_codes(units, cols), "w_q");
+  OPS_CHECK_PTR(w_scale, mx4_scales(units, cols), "w_scale");
+  OPS_CHECK_PTR(y, (size_t)n * units * size_of(y_dtype), "y");
+  a->n = n;
+  a->cols = cols;
+  a->units = units;
+  a->w_q = w_q;
+  a->w_scale = w_scale;
+  a->y = y;
+  a->y_bf16 = y_dtype == TWELL_BF16;
+  return TWELL_OK;
+}
+
+size_t linear_ws_bytes(int64_t n, int32_t cols) {
+  return twell::mx4_product_quantises(n) ? 0 : mx4_codes(n, cols) + mx4_scales(n, cols);
+}
+
 }  // namespace
 
 extern "C" {
@@ -135,6 +173,94 @@ twell_status twell_add_rms_norm_bwd(int64_t rows, int32_t cols, twell_dtype d_ou
   a.part = static_cast<float*>(ws);
   ok();
   return hip_status(twell::launch_add_rms_norm_bwd(a, (hipStream_t)stream), "twell_add_rms_norm_bwd");
+}
+
+twell_status twell_mx4_sizes(int64_t rows, int32_t cols, size_t* q_bytes, size_t* scale_bytes) {
+  const twell_status st = check_mx4_shape(rows, cols);
+  if (st != TWELL_OK) return st;
+  if (q_bytes == nullptr || scale_bytes == nullptr) return fail(TWELL_ERR_INVALID_ARG, "q_bytes or scale_bytes is NULL");
+  *q_bytes = mx4_codes(rows, cols);
+  *scale_bytes = mx4_scales(rows, cols);
+  return ok();
+}
+
+twell_status twell_quantize_mx4(int64_t rows, int32_t cols, twell_dtype dtype, const void* in, uint8_t* q,
+                                uint8_t* scale, void* stream) {
+  const twell_status st = check_mx4_shape(rows, cols);
+  if (st != TWELL_OK) return st;
+  if (bad_dtype(dtype)) return fail(TWELL_ERR_INVALID_ARG, "dtypes must be bf16 or fp32");
+  OPS_CHECK_PTR(in, (size_t)rows * cols * size_of(dtype), "in");
+  OPS_CHECK_PTR(q, mx4_codes(rows, cols), "q");
+  OPS_CHECK_PTR(scale, mx4_scales(rows, cols), "scale");
+  ok();
+  if (rows == 0) return TWELL_OK;
+  return hip_status(twell::launch_quantize_mx4(in, dtype == TWELL_BF16, rows, cols, q, scale, (hipStream_t)stream),
+                    "twell_quantize_mx4");
+}
+
+twell_status twell_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t* q, const uint8_t* scale,
+                                  twell_dtype dtype, void* out, void* stream) {
+  const twell_status st = check_mx4_shape(rows, cols);
+  if (st != TWELL_OK) return st;
+  if (bad_dtype(dtype)) return fail(TWELL_ERR_INVALID_ARG, "dtypes must be bf16 or fp32");
+  OPS_CHECK_PTR(q, mx4_codes(rows, cols), "q");
+  OPS_CHECK_PTR(scale, mx4_scales(rows, cols), "scale");
+  OPS_CHECK_PTR(out, (size_t)rows * cols * size_of(dtype), "out");
+  ok();
+  if (rows == 0) return TWELL_OK;
+  return hip_status(twell::launch_dequantize_mx4(q, scale, rows, cols, dtype == TWELL_BF16, out, (hipStream_t)stream),
+                    "twell_dequantize_mx4");
+}
+
+twell_status twell_matmul_mx4(int64_t n, int32_t cols, int32_t units, const uint8_t* x_q, const uint8_t* x_scale,
+                              const uint8_t* w_q, const uint8_t* w_scale, twell_dtype y_dtype, void* y,
+                              void* stream) {
+  twell::Mx4ProductArgs a{};
+  const twell_status st = check_mx4_product(n, cols, units, w_q, w_scale, y_dtype, y, &a);
+  if (st != TWELL_OK) return st;
+  OPS_CHECK_PTR(x_q, mx4_codes(n, cols), "x_q");
+  OPS_CHECK_PTR(x_scale, mx4_scales(n, cols), "x_scale");
+  ok();
+  if (n == 0) return TWELL_OK;
+  a.x_q = x_q;
+  a.x_scale = x_scale;
+  return hip_status(twell::launch_mx4_product(a, (hipStream_t)stream), "twell_matmul_mx4");
+}
+
+twell_status twell_linear_mx4_ws(int64_t n, int32_t cols, size_t* ws_bytes) {
+  const twell_status st = check_mx4_shape(n, cols);
+  if (st != TWELL_OK) return st;
+  if (ws_bytes == nullptr) return fail(TWELL_ERR_INVALID_ARG, "ws_bytes is NULL");
+  *ws_bytes = linear_ws_bytes(n, cols);
+  return ok();
+}
+
+twell_status twell_linear_mx4(int64_t n, int32_t cols, int32_t units, twell_dtype x_dtype, const void* x,
+                              const uint8_t* w_q, const uint8_t* w_scale, twell_dtype y_dtype, void* y, void* ws,
+                              size_t ws_bytes, void* stream) {
+  twell::Mx4ProductArgs a{};
+  const twell_status st = check_mx4_product(n, cols, units, w_q, w_scale, y_dtype, y, &a);
+  if (st != TWELL_OK) return st;
+  if (bad_dtype(x_dtype)) return fail(TWELL_ERR_INVALID_ARG, "dtypes must be bf16 or fp32");
+  OPS_CHECK_PTR(x, (size_t)n * cols * size_of(x_dtype), "x");
+  const size_t need = linear_ws_bytes(n, cols);
+  if (ws_bytes < need) return fail(TWELL_ERR_WORKSPACE, "workspace smaller than twell_linear_mx4_ws says");
+  if (twell::bad_ptr(ws, need)) return fail(TWELL_ERR_WORKSPACE, "workspace is NULL or not 16-byte aligned");
+  ok();
+  if (n == 0) return TWELL_OK;
+  if (twell::mx4_product_quantises(n)) {
+    a.x = x;
+    a.x_bf16 = x_dtype == TWELL_BF16;
+  } else {
+    uint8_t* x_q = static_cast<uint8_t*>(ws);
+    uint8_t* x_scale = x_q + mx4_codes(n, cols);
+    const hipError_t e =
+        twell::launch_quantize_mx4(x, x_dtype == TWELL_BF16, n, cols, x_q, x_scale, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_status(e, "twell_linear_mx4");
+    a.x_q = x_q;
+    a.x_scale = x_scale;
+  }
+  return hip_status(twell::launch_mx4_product(a, (hipStream_t)stream), "twell_linear_mx4");
 }
 
 }  // extern "C"

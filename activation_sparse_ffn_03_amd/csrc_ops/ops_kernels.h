@@ -51,4 +51,34 @@ inline int norm_bwd_groups(int64_t rows, int cols) {
 }
 hipError_t launch_add_rms_norm_bwd(const NormBwdArgs& a, hipStream_t s);
 
+// MX4 rows: 64 bytes of codes for every 128 columns begun, 16 scale bytes for
+// every 512 begun.
+constexpr int kMx4MaxCols = 1 << 20;
+__host__ __device__ inline int mx4_code_bytes(int cols) { return (cols + 127) / 128 * 64; }
+__host__ __device__ inline int mx4_scale_bytes(int cols) { return (cols + 511) / 512 * 16; }
+hipError_t launch_quantize_mx4(const void* in, int is_bf16, int64_t rows, int cols, uint8_t* q, uint8_t* scale,
+                               hipStream_t s);
+hipError_t launch_dequantize_mx4(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols, int out_bf16,
+                                 void* out, hipStream_t s);
+
+// y[i][c] = sum over blocks b of 2^(xs + ws - 254) * sum_k xq wq. Either x_q
+// and x_scale hold x's MX4 rows, or x holds bf16 / fp32 rows that the kernel
+// quantises itself (mx4_product_quantises).
+struct Mx4ProductArgs {
+  int64_t n;
+  int cols, units;
+  const uint8_t* x_q;
+  const uint8_t* x_scale;
+  const void* x;  // null: x_q and x_scale
+  int x_bf16;
+  const uint8_t* w_q;
+  const uint8_t* w_scale;
+  void* y;  // [n][units]
+  int y_bf16;
+};
+// Tokens up to which the product quantises x in its registers.
+constexpr int kMx4FusedTokens = 16;
+inline bool mx4_product_quantises(int64_t n) { return n <= kMx4FusedTokens; }
+hipError_t launch_mx4_product(const Mx4ProductArgs& a, hipStream_t s);
+
 }  // namespace twell

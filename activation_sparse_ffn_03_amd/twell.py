@@ -31,7 +31,8 @@ EXPORTS = ("twell_status_str", "twell_last_error", "twell_n_tiles", "twell_query
            "twell_gate_pack_ws", "twell_pack_preact", "twell_quantize_e4m3", "twell_gate_pack_fp8",
            "twell_gate_pack_fp8_ws", "twell_ffn_fwd", "twell_ffn_forward", "twell_ffn_forward_fp8",
            "twell_ffn_forward_noalloc", "twell_route_hybrid", "twell_ffn_bwd", "twell_add_rms_norm",
-           "twell_add_rms_norm_bwd_ws", "twell_add_rms_norm_bwd", "twell_trace_start",
+           "twell_add_rms_norm_bwd_ws", "twell_add_rms_norm_bwd", "twell_mx4_sizes", "twell_quantize_mx4",
+           "twell_dequantize_mx4", "twell_matmul_mx4", "twell_linear_mx4_ws", "twell_linear_mx4", "twell_trace_start",
            "twell_trace_stop", "twell_trace_count", "twell_trace_dropped", "twell_trace_get")
 
 # Bytes of the library's static scratch used by twell_ffn_forward_noalloc.
@@ -114,15 +115,28 @@ def lib() -> ctypes.CDLL:
         L.twell_route_hybrid.argtypes = [pd, ctypes.c_int, pp, vp, ph, vp]
         L.twell_ffn_bwd.restype = ctypes.c_int
         L.twell_ffn_bwd.argtypes = [pd, ctypes.c_int, ph, vp, vp, vp, vp, vp, f32, vp, vp, vp, vp, vp, sz, vp]
-        i64 = ctypes.c_int64
+        i64, psz = ctypes.c_int64, ctypes.POINTER(sz)
         L.twell_add_rms_norm.restype = ctypes.c_int
         L.twell_add_rms_norm.argtypes = [i64, i32, ctypes.c_int, vp, ctypes.c_int, vp, ctypes.c_int, vp, f32, vp,
                                          ctypes.c_int, vp, vp, vp, vp, vp]
         L.twell_add_rms_norm_bwd_ws.restype = ctypes.c_int
-        L.twell_add_rms_norm_bwd_ws.argtypes = [i64, i32, ctypes.POINTER(sz)]
+        L.twell_add_rms_norm_bwd_ws.argtypes = [i64, i32, psz]
         L.twell_add_rms_norm_bwd.restype = ctypes.c_int
         L.twell_add_rms_norm_bwd.argtypes = [i64, i32, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp, ctypes.c_int, vp,
                                              vp, vp, vp, sz, vp]
+
+        L.twell_mx4_sizes.restype = ctypes.c_int
+        L.twell_mx4_sizes.argtypes = [i64, i32, psz, psz]
+        L.twell_quantize_mx4.restype = ctypes.c_int
+        L.twell_quantize_mx4.argtypes = [i64, i32, ctypes.c_int, vp, vp, vp, vp]
+        L.twell_dequantize_mx4.restype = ctypes.c_int
+        L.twell_dequantize_mx4.argtypes = [i64, i32, vp, vp, ctypes.c_int, vp, vp]
+        L.twell_matmul_mx4.restype = ctypes.c_int
+        L.twell_matmul_mx4.argtypes = [i64, i32, i32, vp, vp, vp, vp, ctypes.c_int, vp, vp]
+        L.twell_linear_mx4_ws.restype = ctypes.c_int
+        L.twell_linear_mx4_ws.argtypes = [i64, i32, psz]
+        L.twell_linear_mx4.restype = ctypes.c_int
+        L.twell_linear_mx4.argtypes = [i64, i32, i32, ctypes.c_int, vp, vp, vp, ctypes.c_int, vp, vp, sz, vp]
         L.twell_trace_start.restype = ctypes.c_int
         L.twell_trace_start.argtypes = [i32]
         L.twell_trace_stop.restype = ctypes.c_int
@@ -464,6 +478,88 @@ def add_rms_norm_bwd(d_out, residual, rstd, weight, d_residual=None, out=None, w
     _check(lib().twell_add_rms_norm_bwd(*args, ws.data_ptr() or None, ws.numel() * ws.element_size(), _stream(stream)),
            "twell_add_rms_norm_bwd")
     return dr, dw
+
+
+def mx4_shapes(rows: int, cols: int):
+    """Shapes of the uint8 code and scale tensors of `rows` MX4 rows of `cols` columns."""
+    return (rows, -(-cols // 128) * 64), (rows, -(-cols // 512) * 16)
+
+
+def alloc_mx4(rows: int, cols: int, device="cuda"):
+    """(codes, scales) buffers of `rows` MX4 rows of `cols` columns."""
+    q, s = mx4_shapes(rows, cols)
+    return torch.empty(q, dtype=torch.uint8, device=device), torch.empty(s, dtype=torch.uint8, device=device)
+
+
+def quantize_mx4(a, out=None, stream=None):
+    """MX4 rows of a [rows, cols] bf16 / fp32 tensor (twell_quantize_mx4):
+    (codes, scales) as uint8 tensors of mx4_shapes(rows, cols), written into
+    `out` when given. scales[:, :ceil(cols / 32)] are the blocks' E8M0 codes."""
+    if a.dim() != 2:
+        raise ValueError("quantize_mx4 takes a [rows, cols] tensor")
+    rows, cols = a.shape
+    dt = _code(a, "a")
+    src = _addr(a, "a", a.shape)
+    q, s = alloc_mx4(rows, cols, a.device) if out is None else out
+    qs, ss = mx4_shapes(rows, cols)
+    _check(lib().twell_quantize_mx4(rows, cols, dt, src, _addr(q, "codes", qs, torch.uint8),
+                                    _addr(s, "scales", ss, torch.uint8), _stream(stream)), "twell_quantize_mx4")
+    return q, s
+
+
+def dequantize_mx4(codes, scales, cols: int, dtype=torch.bfloat16, out=None, stream=None):
+    """The values MX4 rows stand for, [rows, cols] in bf16 or fp32 (twell_dequantize_mx4)."""
+    rows = codes.shape[0]
+    qs, ss = mx4_shapes(rows, cols)
+    q, s = _addr(codes, "codes", qs, torch.uint8), _addr(scales, "scales", ss, torch.uint8)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
+    _check(lib().twell_dequantize_mx4(rows, cols, q, s, _code(out, "out"), _addr(out, "out", (rows, cols)),
+                                      _stream(stream)), "twell_dequantize_mx4")
+    return out
+
+
+def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bfloat16, out=None, stream=None):
+    """x · w^T of MX4 rows with `cols` columns (twell_matmul_mx4): [rows of x,
+    rows of w] in bf16 or fp32, written into `out` when given."""
+    n, units = x_codes.shape[0], w_codes.shape[0]
+    (xq, xs), (wq, ws) = mx4_shapes(n, cols), mx4_shapes(units, cols)
+    args = (_addr(x_codes, "x_codes", xq, torch.uint8), _addr(x_scales, "x_scales", xs, torch.uint8),
+            _addr(w_codes, "w_codes", wq, torch.uint8), _addr(w_scales, "w_scales", ws, torch.uint8))
+    if out is None:
+        out = torch.empty((n, units), dtype=dtype, device=x_codes.device)
+    _check(lib().twell_matmul_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units)),
+                                  _stream(stream)), "twell_matmul_mx4")
+    return out
+
+
+def linear_mx4_ws(rows: int, cols: int) -> int:
+    """Workspace bytes of linear_mx4."""
+    n = ctypes.c_size_t()
+    _check(lib().twell_linear_mx4_ws(rows, cols, ctypes.byref(n)), "twell_linear_mx4_ws")
+    return n.value
+
+
+def linear_mx4(x, w_codes, w_scales, dtype=torch.bfloat16, out=None, ws=None, stream=None):
+    """x · w^T with MX4 weights, x [rows, cols] bf16 / fp32 quantised to MX4
+    within the call (twell_linear_mx4): [rows, units] in bf16 or fp32, written
+    into `out` when given; ws (bytes of linear_mx4_ws) is allocated here when
+    not."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    n, cols = x.shape
+    units = w_codes.shape[0]
+    wq, wsc = mx4_shapes(units, cols)
+    args = (_code(x, "x"), _addr(x, "x", x.shape), _addr(w_codes, "w_codes", wq, torch.uint8),
+            _addr(w_scales, "w_scales", wsc, torch.uint8))
+    if out is None:
+        out = torch.empty((n, units), dtype=dtype, device=x.device)
+    if ws is None:
+        ws = torch.empty(linear_mx4_ws(n, cols), dtype=torch.uint8, device=x.device)
+    _check(lib().twell_linear_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units)),
+                                  ws.data_ptr() or None, ws.numel() * ws.element_size(), _stream(stream)),
+           "twell_linear_mx4")
+    return out
 
 
 def trace_start(capacity: int = 4096) -> None:

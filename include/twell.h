@@ -374,6 +374,52 @@ twell_status twell_add_rms_norm_bwd(int64_t rows, int32_t cols, twell_dtype d_ou
                                     const float* rstd, twell_dtype weight_dtype, const void* weight, void* dr,
                                     float* dw, void* ws, size_t ws_bytes, void* stream);
 
+/* MX4: microscaled 4-bit floating point. 32 consecutive columns of a row form
+ * a block with one E8M0 scale:
+ *   code  = max(floor(log2 max_k |v[k]|) - 2, -127) + 127, the scale 2^(code - 127);
+ *           an all-zero block has code 0, a block with NaN or infinity has
+ *           code 255 (the scale is NaN) and zero elements,
+ *   q[k]  = E2M1(v[k] / scale): the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with
+ *           ties to the even code, magnitudes above 6 held to 6, and the sign.
+ * A row of cols columns takes 64 bytes of codes for every 128 columns begun
+ * (two codes a byte, the even column's in the low half) and 16 scale bytes for
+ * every 512 begun; both are filled with zeros behind the last column, and the
+ * products rely on it. Rows follow one another without gaps. Any cols from 1
+ * to 2^20. */
+
+/* Byte sizes of `rows` MX4 rows (host-only query). */
+twell_status twell_mx4_sizes(int64_t rows, int32_t cols, size_t* q_bytes, size_t* scale_bytes);
+
+/* in [rows][cols] bf16 or fp32 -> MX4 rows q and scale (filling included).
+ * rows == 0 is a no-op. */
+twell_status twell_quantize_mx4(int64_t rows, int32_t cols, twell_dtype dtype, const void* in, uint8_t* q,
+                                uint8_t* scale, void* stream);
+
+/* MX4 rows -> out [rows][cols] bf16 or fp32: the values the codes stand for,
+ * exactly (NaN where the scale code is 255). */
+twell_status twell_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t* q, const uint8_t* scale,
+                                  twell_dtype dtype, void* out, void* stream);
+
+/* y[i][c] = sum_k x[i,k] * w[c,k] for MX4 rows x ([n] rows of cols columns) and
+ * w ([units] rows): the products of a block's codes are exact, their sums and
+ * the scaled blocks' are held in fp32, y [n][units] is rounded once to
+ * y_dtype. NaN scales make their row or column of y NaN. n == 0 is a no-op. */
+twell_status twell_matmul_mx4(int64_t n, int32_t cols, int32_t units, const uint8_t* x_q, const uint8_t* x_scale,
+                              const uint8_t* w_q, const uint8_t* w_scale, twell_dtype y_dtype, void* y,
+                              void* stream);
+
+/* Workspace bytes of twell_linear_mx4 (host-only query): the MX4 rows of x, or
+ * 0 for small n, where the product quantises x as it reads it. */
+twell_status twell_linear_mx4_ws(int64_t n, int32_t cols, size_t* ws_bytes);
+
+/* twell_quantize_mx4 of x [n][cols] (bf16 or fp32) and twell_matmul_mx4 in one
+ * call: the gate's pre-activation for twell_pack_preact when w is the gate
+ * weight. A serving operator: it has no backward. ws: at least the queried
+ * bytes (NULL allowed when that is 0). */
+twell_status twell_linear_mx4(int64_t n, int32_t cols, int32_t units, twell_dtype x_dtype, const void* x,
+                              const uint8_t* w_q, const uint8_t* w_scale, twell_dtype y_dtype, void* y, void* ws,
+                              size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Tracing (diagnostics). When started, every kernel launched by the calls
  * above is bracketed by two HIP events recorded on the call's stream, so the

@@ -84,3 +84,67 @@ def test_binding_refuses_what_does_not_fit():
     with pytest.raises(ValueError, match="contiguous"):
         f(torch.zeros(64, 4).t(), "x", (4, 64))
     assert f(None, "x", (4, 64)) is None
+
+
+# ---------------------------------------------------------------- MX4
+
+def _sizes(rows, cols):
+    q, s = ctypes.c_size_t(), ctypes.c_size_t()
+    st = tw.lib().twell_mx4_sizes(rows, cols, ctypes.byref(q), ctypes.byref(s))
+    return st, q.value, s.value
+
+
+def test_mx4_sizes_and_shapes():
+    for rows, cols in ((1, 1), (3, 128), (3, 129), (7, 512), (7, 513), (11008, 4096), (0, 64)):
+        st, q, s = _sizes(rows, cols)
+        (r0, c0), (r1, c1) = tw.mx4_shapes(rows, cols)
+        assert st == 0 and (q, s) == (r0 * c0, r1 * c1)
+        assert 2 * c0 >= cols and 32 * c1 >= cols and c0 % 64 == 0 and c1 % 16 == 0
+    assert _sizes(-1, 64)[0] == 1 and _sizes(1, 0)[0] == 1 and _sizes(1, (1 << 20) + 1)[0] == 2
+    assert _sizes(1 << 31, 64)[0] == 2 and _sizes((1 << 31) - 1, 1 << 20)[0] == 2
+    assert tw.lib().twell_mx4_sizes(1, 64, None, None) == 1
+    assert tw.linear_mx4_ws(1, 4096) == 0
+    assert tw.linear_mx4_ws(1000, 1990) == 1000 * (1024 + 64)
+
+
+def test_mx4_refusals():
+    L = tw.lib()
+    q = lambda rows=4, cols=64, dt=0, a=FAKE, c=FAKE, s=FAKE: L.twell_quantize_mx4(rows, cols, dt, a, c, s, None)  # noqa: E731
+    assert q(rows=-1) == 1 and q(cols=0) == 1 and q(cols=1 << 21) == 2 and q(dt=4) == 1
+    assert q(a=None) == 1 and q(c=ODD) == 1 and q(s=None) == 1 and b"scale" in L.twell_last_error()
+    d = lambda rows=4, cols=64, c=FAKE, s=FAKE, dt=0, o=FAKE: L.twell_dequantize_mx4(rows, cols, c, s, dt, o, None)  # noqa: E731
+    assert d(rows=-1) == 1 and d(c=None) == 1 and d(s=ODD) == 1 and d(dt=2) == 1 and d(o=None) == 1
+    m = lambda n=4, k=64, u=8, a=FAKE, b=FAKE, c=FAKE, e=FAKE, dt=0, y=FAKE: L.twell_matmul_mx4(n, k, u, a, b, c, e, dt, y, None)  # noqa: E731
+    for kw in (dict(n=-1), dict(k=0), dict(u=0), dict(a=None), dict(b=ODD), dict(c=None), dict(e=None), dict(dt=3), dict(y=None)):
+        assert m(**kw) == 1, kw
+    assert m(u=(1 << 24) + 1) == 2 and m(n=(1 << 31) - 1, u=1 << 20) == 2
+    f = lambda n=64, k=64, u=8, xd=0, x=FAKE, c=FAKE, e=FAKE, dt=0, y=FAKE, ws=FAKE, b=64 * 80: L.twell_linear_mx4(  # noqa: E731
+        n, k, u, xd, x, c, e, dt, y, ws, b, None)
+    for kw in (dict(xd=9), dict(x=None), dict(x=ODD), dict(c=None), dict(y=ODD)):
+        assert f(**kw) == 1, kw
+    assert f(b=64 * 80 - 1) == 3 and f(ws=None) == 3 and f(ws=ODD) == 3
+
+
+def test_mx4_of_no_rows_needs_no_device():
+    L = tw.lib()
+    assert L.twell_quantize_mx4(0, 64, 0, None, None, None, None) == 0
+    assert L.twell_dequantize_mx4(0, 64, None, None, 0, None, None) == 0
+    assert L.twell_matmul_mx4(0, 64, 8, None, None, FAKE, FAKE, 0, None, None) == 0
+    assert L.twell_linear_mx4(0, 64, 8, 0, None, FAKE, FAKE, 0, None, None, 0, None) == 0
+
+
+def test_mx4_binding_refuses_what_does_not_fit():
+    x = torch.zeros(4, 64)
+    w = torch.zeros(8, 64, dtype=torch.uint8), torch.zeros(8, 16, dtype=torch.uint8)
+    for call in (lambda: tw.quantize_mx4(x), lambda: tw.linear_mx4(x, *w), lambda: tw.dequantize_mx4(*w, 64),
+                 lambda: tw.matmul_mx4(*w, *w, 64)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+    with pytest.raises(ValueError, match="rows, cols"):
+        tw.quantize_mx4(x[0])
+    with pytest.raises(TypeError, match="bfloat16"):
+        tw.quantize_mx4(x.half())
+    with pytest.raises(ValueError, match="rows, cols"):
+        tw.linear_mx4(x[0], *w)
+    with pytest.raises(ValueError, match="shape"):
+        tw.dequantize_mx4(*w, 200)
