@@ -30,11 +30,18 @@ __device__ __forceinline__ i32x8_t operand(const u32x4_t& v) {
   return i32x8_t{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
 }
 
-// acc += A . B^T with both operands E2M1 (format 4), the lowest byte of sa and
-// sb as scale codes.
+// acc += A . B^T with both operands E2M1 (format 4) and byte B of sa and sb as
+// scale codes: 16 x 128 by 128 x 16 ...
+template <int B = 0>
 __device__ __forceinline__ f32x4_t mfma(const u32x4_t& a, const u32x4_t& b, const f32x4_t& acc, uint32_t sa,
                                         uint32_t sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(a), operand(b), acc, 4, 4, 0, (int)sa, 0, (int)sb);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(a), operand(b), acc, 4, 4, B, (int)sa, B, (int)sb);
+}
+// ... and 32 x 64 by 64 x 32.
+template <int B = 0>
+__device__ __forceinline__ f32x16_t mfma(const u32x4_t& a, const u32x4_t& b, const f32x16_t& acc, uint32_t sa,
+                                         uint32_t sb) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(a), operand(b), acc, 4, 4, B, (int)sa, B, (int)sb);
 }
 
 // Four neighbouring units of one token. WHOLE: units is a multiple of 4, so
@@ -182,160 +189,358 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_product_direct(Mx4ProductArgs 
 
 // ---------------------------------------------------------------- tiled
 
-// BU units by BT tokens per workgroup of WU x WT waves, ST stages of 128
-// columns (64 bytes a row).
-template <int BU_, int BT_, int WU_, int WT_, int ST_, int OCC_>
+// A workgroup of WU x WT waves, each FU x FT fragments of 32 x 32: BU units by
+// BT tokens. A stage is 256 columns: 128 bytes of codes a row, a whole cache
+// line (an L2 channel serves one request a clock, of 64 bytes or of 128), and
+// 8 scale bytes a row, arranged beforehand. LDS holds two.
+template <int FU_, int FT_, int WU_, int WT_, int OCC_>
 struct TileCfg {
-  static constexpr int BU = BU_, BT = BT_, WU = WU_, WT = WT_, ST = ST_, OCC = OCC_;
+  static constexpr int FU = FU_, FT = FT_, WU = WU_, WT = WT_, OCC = OCC_;
   static constexpr int NW = WU * WT, NT = 64 * NW;
-  static constexpr int FU = BU / WU / 16, FT = BT / WT / 16;
-  static constexpr int ROWS = BU + BT;
-  static constexpr int STAGE = ROWS * 64;
-  static constexpr int GPW = ROWS / 16 / NW;  // 1 KB loads of a wave per stage
-  static constexpr int SPW = (ROWS / 64 + NW - 1) / NW;  // scale loads (64 rows, 16 bytes each) of a wave per four stages
-  static constexpr int SCALES = SPW * NW * 1024;  // one of two buffers
-  static constexpr int LDS = ST * STAGE + 2 * SCALES;
-  static_assert(BU % (16 * WU) == 0 && BT % (16 * WT) == 0, "whole fragments");
-  static_assert(ROWS % (16 * NW) == 0, "stage loads split evenly over the waves");
-  static_assert(ST >= 2 && ST <= 4, "ring depth");
-  static_assert(LDS <= 160 * 1024, "LDS of a compute unit");
+  static constexpr int BU = 32 * FU * WU, BT = 32 * FT * WT, ROWS = BU + BT;
+  static constexpr int CODES = ROWS * 128, STAGE = CODES + ROWS * 8;
+  // a wave's rows of 128 output bytes, of 32 or 16 tokens at a time; 16 bytes
+  // more a row keep both sides' accesses on different banks
+  static constexpr int TOK = OCC > 1 ? 16 : 32;
+  static constexpr int OUT = TOK * 144;
+  static constexpr int LDS = 2 * STAGE + NW * OUT;
+  static constexpr int UG = BU / 8 / NW, TG = BT / 8 / NW;  // 1 KB loads of 8 rows, of a wave and stage
+  static constexpr int SROWS = ROWS / 128;                  // 1 KB loads of 128 rows' scales, of all waves;
+  static constexpr int SG = (SROWS + NW - 1) / NW;          // of a wave: with fewer than waves some are made twice
+  static constexpr int LOADS = UG + TG + SG;
+  static constexpr int MIN_STORES = 2 * FU * FT;            // of a wave at a tile's end: 16-byte stores of bf16
+  static_assert(LOADS / 2 + MIN_STORES <= 63, "vmcnt");
+  static_assert(NW == 4, "the key of the LDS rows");
+  static_assert(BU % 128 == 0 && BT % 128 == 0 && (SROWS % NW == 0 || NW % SROWS == 0), "loads split evenly over the waves");
+  static_assert(OCC * LDS <= 160 * 1024, "LDS of a compute unit");
 };
 
-// XOR key of the 16-byte pieces of a 64-byte LDS row that keeps the fragment
-// reads (16 rows, one piece each per 16 lanes) free of bank conflicts.
-__device__ __forceinline__ int piece_key(int r) { return ((r >> 3) & 1) | ((((r >> 1) ^ (r >> 3)) & 1) << 1); }
+// 16 bytes per lane from base + off straight into LDS, lane l's at lds + 16 l.
+__device__ __forceinline__ void dma_16B(const uint8_t* base, uint32_t off, uint32_t lds) {
+  const uint32_t m = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(m) : "memory");
+}
+// vmcnt(M) if `many` (uniform) is not 0, else vmcnt(N). The branch is inside
+// the statement: one that the compiler sees would split the loop's body, and
+// it then moves matrix instructions across.
+template <int M, int N>
+__device__ __forceinline__ void wait_vmcnt_either(uint32_t many) {
+  asm volatile(
+      "s_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lfew%=\n\ts_waitcnt vmcnt(%1)\n\ts_branch .Lend%=\n.Lfew%=:\n\t"
+      "s_waitcnt vmcnt(%2)\n.Lend%=:" ::"s"(__builtin_amdgcn_readfirstlane(many)), "n"(M), "n"(N) : "memory", "scc");
+}
 
 // Workgroup -> tile: each XCD takes a contiguous run of tiles, walked in
-// groups of kGroup token blocks so that the tiles in flight share rows in L2.
-__device__ __forceinline__ void tile_of(int64_t L, int tb, int ub, int group, int& t, int& u) {
-  const int64_t per = (int64_t)group * ub;
-  const int first = (int)(L / per) * group;
-  const int g = min(tb - first, group);
+// groups of 4 token blocks so that the tiles in flight share rows in L2 (us for
+// 16384 x 4096 x 11008: 357 in groups of 2, 4 and 6, 364 of 8, 371 of 16).
+__device__ __forceinline__ void tile_of(int64_t L, int tb, int ub, int& t, int& u) {
+  constexpr int kGroup = 4;
+  const int64_t per = (int64_t)kGroup * ub;
+  const int first = (int)(L / per) * kGroup;
+  const int g = min(tb - first, kGroup);
   const int in = (int)(L % per);
   t = first + in % g;
   u = in / g;
 }
 
+// A wave's results to memory. Where rows of y are 16-byte aligned they go
+// through LDS, 32 tokens by 128 bytes at a time, so that each store writes
+// whole lines (8 tokens, 128 bytes each) instead of 32-byte pieces, each of
+// which is a request of its own to L2.
 template <class C>
+__device__ __forceinline__ void store_tile(const Mx4ProductArgs& a, const f32x16_t (&acc)[C::FU][C::FT], int64_t t0,
+                                           int u0, char* out) {
+  const int lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5;
+  const int esz = a.y_bf16 ? 2 : 4;
+  if (a.units * esz % 16 == 0 && u0 * esz % 16 == 0) {
+    char* y = static_cast<char*>(a.y) + (t0 * a.units + u0) * esz;
+    const int64_t pitch = (int64_t)a.units * esz;
+    const int64_t left = a.n - t0;  // tokens there are
+    constexpr int TOK = C::TOK;
+    // TOK tokens from tok0, bytes [at, at + 128) of the wave's units. A wave's
+    // LDS operations are done in their order; the statements around the reads
+    // keep the compiler to it, which sees no lane's write of what another reads.
+    auto flush = [&](int tok0, int at) {
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int r = 0; r < TOK / 8; ++r) {
+        const int tok = 8 * r + (lane >> 3);
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(out + tok * 144 + 16 * (lane & 7));
+        if (tok0 + tok < left) *reinterpret_cast<u32x4_t*>(y + (tok0 + tok) * pitch + at + 16 * (lane & 7)) = v;
+      }
+      asm volatile("" ::: "memory");
+    };
+#pragma unroll
+    for (int j = 0; j < C::FT; ++j)
+#pragma unroll
+      for (int h = 0; h < 32 / TOK; ++h) {  // lanes of TOK tokens write, all read
+        const bool mine = row / TOK == h;
+        char* line = out + row % TOK * 144;
+        if (a.y_bf16) {
+          static_assert(C::FU % 2 == 0, "64 units a line");
+#pragma unroll
+          for (int i = 0; i < C::FU; i += 2) {
+            if (mine) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const f32x16_t& v = acc[i + k][j];
+                  *reinterpret_cast<u32x2_t*>(line + 64 * k + 16 * q + 8 * half) =
+                      u32x2_t{pack_bf16(v[4 * q], v[4 * q + 1]), pack_bf16(v[4 * q + 2], v[4 * q + 3])};
+                }
+            }
+            flush(32 * j + TOK * h, 64 * i);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < C::FU; ++i) {
+            if (mine) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const f32x16_t& v = acc[i][j];
+                *reinterpret_cast<f32x4_t*>(line + 32 * q + 16 * half) =
+                    f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+              }
+            }
+            flush(32 * j + TOK * h, 128 * i);
+          }
+        }
+      }
+    return;
+  }
+  store_kind(a, [&](auto bf16, auto whole) {
+#pragma unroll
+    for (int j = 0; j < C::FT; ++j)
+#pragma unroll
+      for (int i = 0; i < C::FU; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          store_units<decltype(bf16)::value, decltype(whole)::value>(
+              a.y, t0 + 32 * j + row, a.n, u0 + 32 * i + 8 * q + 4 * half, a.units,
+              f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
+  });
+}
+
+// Needs at least BU units, BT tokens (without FEW) and two stages of columns. The last tile
+// of a row or column of tiles is moved back to end with the matrix: what it
+// shares with its neighbour is computed by both, to the same bits.
+// HALF: the last stage has only 128 columns. FEW: fewer than BT tokens, one
+// row of tiles; rows behind the last read the last one and are not stored.
+template <class C, bool HALF, bool FEW>
 __global__ __launch_bounds__(C::NT, C::OCC) void mx4_product_tiled(Mx4ProductArgs a, int tb, int ub) {
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
   constexpr int FU = C::FU, FT = C::FT;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wu = wave / C::WT, wt = wave % C::WT;
-  const int row = lane & 15, kb = lane >> 4;
-  int tt, tu;
-  tile_of(xcd_run_block(blockIdx.x, gridDim.x), tb, ub, 8, tt, tu);
-  const int64_t t0 = (int64_t)tt * C::BT;
-  const int u0 = tu * C::BU;
-  const int cbytes = mx4_code_bytes(a.cols), sbytes = mx4_scale_bytes(a.cols);
-  const int KT = cbytes / 64;
+  const int row = lane & 31, half = lane >> 5;
+  const int cbytes = mx4_code_bytes(a.cols);
+  const int KT = (cbytes + 127) / 128;
 
-  // Row r of a stage: unit u0 + r, then token t0 + r - BU; rows behind the
-  // last unit or token read row 0, their results are not stored.
-  auto code_row = [&](int r) {
-    if (r < C::BU) return a.w_q + (int64_t)(u0 + r < a.units ? u0 + r : 0) * cbytes;
-    const int64_t t = t0 + r - C::BU;
-    return a.x_q + (t < a.n ? t : 0) * cbytes;
-  };
-  auto scale_row = [&](int r) {
-    if (r < C::BU) return a.w_scale + (int64_t)(u0 + r < a.units ? u0 + r : 0) * sbytes;
-    const int64_t t = t0 + r - C::BU;
-    return a.x_scale + (t < a.n ? t : 0) * sbytes;
-  };
-  const uint8_t* src[C::GPW];
-  uint32_t dst[C::GPW];
-  const int rin = lane >> 2, pos = lane & 3;
+  // This workgroup's tiles: every n-th (n workgroups on the XCD) of its XCD's run.
+  const int64_t tiles = (int64_t)tb * ub;
+  const int xcd = blockIdx.x % 8;
+  const int64_t run = tiles / 8, extra = tiles % 8;
+  const int64_t end = (xcd + 1) * run + min((int64_t)xcd + 1, extra);
+  const int64_t stride = (gridDim.x + 7 - xcd) / 8;
+  int64_t L = xcd * run + min((int64_t)xcd, extra) + blockIdx.x / 8;
+  if (L >= end) return;
+
+  // LDS: 16-byte piece p of row r lies at piece p ^ key(r), key = (r ^ r >> 3)
+  // & 7 of r mod 32, so that eight consecutive rows' pieces (and sixteen's)
+  // fall into different banks. A load covers 8 rows, lane l piece l & 7 of row
+  // l >> 3; a wave's loads are 32 rows apart and share their keys.
+  const int key = (row ^ (row >> 3)) & 7;
+  const int lrow = 8 * wave + (lane >> 3);
+  const int lpiece = (lane & 7) ^ ((lane >> 3) ^ wave);
+  const uint32_t off = (uint32_t)(lrow * cbytes + 16 * lpiece);
+  // the last stage's second half does not exist: read the first half again
+  const uint32_t off_last = HALF ? (uint32_t)(lrow * cbytes + 16 * (lpiece & 3)) : off;
+  uint32_t few[FEW ? C::TG : 1];  // FEW: rows of the token loads, held to the last one
+  if constexpr (FEW) {
 #pragma unroll
-  for (int g = 0; g < C::GPW; ++g) {
-    const int r = (wave + C::NW * g) * 16 + rin;
-    src[g] = code_row(r) + ((pos ^ piece_key(r & 15)) << 4);
-    dst[g] = (uint32_t)((r - rin) * 64);
+    for (int g = 0; g < C::TG; ++g) few[g] = (uint32_t)(min(lrow + 32 * g, (int)a.n - 1) * cbytes);
   }
-  const uint8_t* ssrc[C::SPW];
-  uint32_t sdst[C::SPW];
-#pragma unroll
-  for (int g = 0; g < C::SPW; ++g) {
-    const int first = (wave + C::NW * g) * 64;
-    ssrc[g] = scale_row(min(first + lane, C::ROWS - 1));
-    sdst[g] = (uint32_t)(C::ST * C::STAGE + first * 16);
-  }
+  const uint32_t soff = 16u * lane;
   const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(smem));
-  auto issue = [&](int kt) {
-    if (kt % 4 == 0) {
+
+  struct Tile {
+    const uint8_t *wq, *xq, *sc[C::SG];  // first rows of codes, and of this wave's scale loads
+    int64_t t0;
+    int u0;
+  };
+  auto tile_at = [&](int64_t l) {
+    int t, u;
+    tile_of(l, tb, ub, t, u);
+    Tile r;
+    r.t0 = FEW ? 0 : min((int64_t)t * C::BT, a.n - C::BT);
+    r.u0 = min(u * C::BU, a.units - C::BU);
+    r.wq = a.w_q + (int64_t)r.u0 * cbytes;
+    r.xq = a.x_q + r.t0 * cbytes;
 #pragma unroll
-      for (int g = 0; g < C::SPW; ++g)
-        dma_16B(ssrc[g] + 4 * kt, lds0 + sdst[g] + (uint32_t)((kt / 4 % 2) * C::SCALES));
+    for (int g = 0; g < C::SG; ++g) {
+      const int first = (wave + 4 * g) % C::SROWS * 128;
+      r.sc[g] = first < C::BU ? a.w_arr + (int64_t)(r.u0 + first) * 8 : a.x_arr + (r.t0 + first - C::BU) * 8;
     }
-    const uint32_t sb = lds0 + (uint32_t)((kt % C::ST) * C::STAGE);
+    return r;
+  };
+  int64_t sstep[C::SG];  // bytes from one stage's scales to the next's
 #pragma unroll
-    for (int g = 0; g < C::GPW; ++g) dma_16B(src[g] + (size_t)kt * 64, sb + dst[g]);
+  for (int g = 0; g < C::SG; ++g) sstep[g] = 8 * ((wave + 4 * g) % C::SROWS * 128 < C::BU ? (int64_t)a.units : mx4_arranged_rows(a.n));
+  struct Stage {
+    const uint8_t *wq, *xq, *sc[C::SG];
+    uint32_t off;
+  };
+  auto stage_at = [&](const Tile& c, const Tile& n, int kt) {  // past c's last: of n
+    const bool in = kt < KT;
+    const int k = in ? kt : kt - KT;
+    Stage r;
+    r.wq = (in ? c.wq : n.wq) + 128 * k;
+    r.xq = (in ? c.xq : n.xq) + 128 * k;
+#pragma unroll
+    for (int g = 0; g < C::SG; ++g) r.sc[g] = (in ? c.sc[g] : n.sc[g]) + k * sstep[g];
+    r.off = HALF && k == KT - 1 ? off_last : off;
+    return r;
+  };
+  auto issue = [&](const Stage& t, uint32_t buf, int g) {
+    const uint32_t at = lds0 + buf * C::STAGE;
+    if (g < C::UG)
+      dma_16B(t.wq + (int64_t)(32 * g) * cbytes, t.off, at + (wave + 4 * g) * 1024);
+    else if (FEW && g < C::UG + C::TG)
+      dma_16B(t.xq, few[g - C::UG] + (t.off - (uint32_t)(lrow * cbytes)), at + C::BU * 128 + (wave + 4 * (g - C::UG)) * 1024);
+    else if (g < C::UG + C::TG)
+      dma_16B(t.xq + (int64_t)(32 * (g - C::UG)) * cbytes, t.off, at + C::BU * 128 + (wave + 4 * (g - C::UG)) * 1024);
+    else
+      dma_16B(t.sc[g - C::UG - C::TG], soff, at + C::CODES + (wave + 4 * (g - C::UG - C::TG)) % C::SROWS * 1024);
   };
 
-  f32x4_t acc[FU][FT];
-#pragma unroll
-  for (int i = 0; i < FU; ++i)
-#pragma unroll
-    for (int j = 0; j < FT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-#pragma unroll
-  for (int st = 0; st < C::ST - 1; ++st)
-    if (st < KT) issue(st);
-
+  f32x16_t acc[FU][FT];
+  u32x4_t av[4][FU], bv[4][FT];  // operands of a stage's four steps
   uint32_t sa[FU], sb[FT];
-  // byte kb of each word of a row's 16 scale bytes: its block kb in the four
-  // stages they cover
-  const uint32_t pick = (uint32_t)kb | ((uint32_t)(kb + 4) << 8);
-  auto scales_of = [&](int r, int buf) {
-    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(smem + C::ST * C::STAGE + buf * C::SCALES + r * 16);
-    const uint32_t lo = __builtin_amdgcn_perm(v[1], v[0], pick), hi = __builtin_amdgcn_perm(v[3], v[2], pick);
-    return (lo & 0xFFFFu) | (hi << 16);
+  int piece[4];
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) piece[ks] = row * 128 + ((2 * ks + half) ^ key) * 16;
+  auto read_a = [&](int i, int ks, uint32_t buf) {
+    return *reinterpret_cast<const u32x4_t*>(smem + buf * C::STAGE + (wu * FU + i) * 4096 + piece[ks]);
   };
-  const int at = (kb ^ piece_key(row)) << 4;
-  for (int kt = 0; kt < KT; ++kt) {
-    // Stage kt is complete for this wave once only the later stages' loads are
-    // pending (scale loads among them make the wait stricter, never looser);
-    // the barrier extends that to every wave, and says that every wave is done
-    // with the stage refilled below.
-    const int later = min(C::ST - 2, KT - 1 - kt);
-    if (later >= 2) wait_vmcnt<2 * C::GPW>();
-    else if (later == 1) wait_vmcnt<C::GPW>();
-    else wait_vmcnt<0>();
-    lds_barrier();
-    if (kt + C::ST - 1 < KT) issue(kt + C::ST - 1);
-    const char* A = smem + (kt % C::ST) * C::STAGE;
-    if (kt % 4 == 0) {
-      const int buf = kt / 4 % 2;
+  auto read_b = [&](int j, int ks, uint32_t buf) {
+    return *reinterpret_cast<const u32x4_t*>(smem + buf * C::STAGE + C::BU * 128 + (wt * FT + j) * 4096 + piece[ks]);
+  };
+  // a row's scale codes of the steps' blocks `half`, step 0's lowest
+  auto read_scale = [&](int r, uint32_t buf) {
+    return *reinterpret_cast<const uint32_t*>(smem + buf * C::STAGE + C::CODES + r * 8 + 4 * half);
+  };
+
+  // Loads run two stages ahead, into the next tile at a tile's end; behind the
+  // last tile they read it again, unused.
+  Tile cur = tile_at(L);
+  {
+    const Stage s0 = stage_at(cur, cur, 0), s1 = stage_at(cur, cur, 1);
 #pragma unroll
-      for (int i = 0; i < FU; ++i) sa[i] = scales_of((wu * FU + i) * 16 + row, buf);
+    for (int g = 0; g < C::LOADS; ++g) issue(s0, 0, g);
 #pragma unroll
-      for (int j = 0; j < FT; ++j) sb[j] = scales_of(C::BU + (wt * FT + j) * 16 + row, buf);
-    } else {
+    for (int g = 0; g < C::LOADS; ++g) issue(s1, 1, g);
+  }
+  wait_vmcnt<C::LOADS>();
+  lds_barrier();
 #pragma unroll
-      for (int i = 0; i < FU; ++i) sa[i] >>= 8;
+  for (int i = 0; i < FU; ++i) {
+    av[0][i] = read_a(i, 0, 0);
+    sa[i] = read_scale((wu * FU + i) * 32 + row, 0);
+  }
 #pragma unroll
-      for (int j = 0; j < FT; ++j) sb[j] >>= 8;
-    }
-    u32x4_t av[FU], bv[FT];
-#pragma unroll
-    for (int i = 0; i < FU; ++i) av[i] = *reinterpret_cast<const u32x4_t*>(A + ((wu * FU + i) * 16 + row) * 64 + at);
-#pragma unroll
-    for (int j = 0; j < FT; ++j)
-      bv[j] = *reinterpret_cast<const u32x4_t*>(A + (C::BU + (wt * FT + j) * 16 + row) * 64 + at);
+  for (int j = 0; j < FT; ++j) {
+    bv[0][j] = read_b(j, 0, 0);
+    sb[j] = read_scale(C::BU + (wt * FT + j) * 32 + row, 0);
+  }
+
+  uint32_t buf = 0, stores = 0;  // stores: the tile before has left some behind
+  for (;;) {
+    const bool more = L + stride < end;
+    const Tile next = more ? tile_at(L + stride) : cur;
 #pragma unroll
     for (int i = 0; i < FU; ++i)
 #pragma unroll
-      for (int j = 0; j < FT; ++j) acc[i][j] = mfma(av[i], bv[j], acc[i][j], sa[i], sb[j]);
-  }
+      for (int j = 0; j < FT; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
 
-  auto put = [&](auto bf16, auto whole) {
+    for (int kt = 0; kt < KT; ++kt) {
+      // Four steps of 64 columns. All operands of the stage are in registers
+      // when the second step ends, so that its LDS can be filled again during
+      // the third and fourth; the next stage's first operands are read in the
+      // fourth. Loads are spread over two steps: a wave that issues them at
+      // once waits for the address unit and keeps its matrix core waiting.
+      const Stage ahead = stage_at(cur, next, kt + 2);
+      const uint32_t live = HALF && kt == KT - 1 ? 0u : ~0u;  // of the last two steps
+      uint32_t na[FU], nb[FT];
+      constexpr int OPS = FU + FT, M = FU * FT;  // operands and matrix instructions of a step
+      // read r of the 3 OPS behind the first step's operands
+      auto read = [&](int r) {
+        const int ks = 1 + r / OPS, k = r % OPS;
+        if (k < FU) {
+          av[ks][k] = read_a(k, ks, buf);
+          if (HALF && ks >= 2) av[ks][k] &= live;
+        } else {
+          bv[ks][k - FU] = read_b(k - FU, ks, buf);
+        }
+      };
+      auto read_next = [&](int r) {
+        if (r < FU) av[0][r] = read_a(r, 0, buf ^ 1);
+        else if (r < OPS) bv[0][r - FU] = read_b(r - FU, 0, buf ^ 1);
+        else if (r < OPS + FU) na[r - OPS] = read_scale((wu * FU + r - OPS) * 32 + row, buf ^ 1);
+        else nb[r - OPS - FU] = read_scale(C::BU + (wt * FT + r - OPS - FU) * 32 + row, buf ^ 1);
+      };
+      // Operation k of n that are dealt to slots [0, m): those of slot s.
+      auto first_of = [](int s, int n, int m) { return s >= m ? n : s * n / m; };
+      auto step = [&](auto KS) {
+        constexpr int ks = decltype(KS)::value;
 #pragma unroll
-    for (int j = 0; j < FT; ++j)
+        for (int s = 0; s < M; ++s) {
+          const int i = s / FT, j = s % FT;
+          acc[i][j] = mfma<ks>(av[ks][i], bv[ks][j], acc[i][j], sa[i], sb[j]);
+          if constexpr (ks < 2) {  // done half a step before the barrier
 #pragma unroll
-      for (int i = 0; i < FU; ++i)
-        store_units<decltype(bf16)::value, decltype(whole)::value>(
-            a.y, t0 + (wt * FT + j) * 16 + row, a.n, u0 + (wu * FU + i) * 16 + 4 * kb, a.units, acc[i][j]);
-  };
-  store_kind(a, put);
+            for (int r = first_of(ks * M + s, 3 * OPS, M + M / 2); r < first_of(ks * M + s + 1, 3 * OPS, M + M / 2); ++r)
+              read(r);
+          } else {
+#pragma unroll
+            for (int g = first_of((ks - 2) * M + s, C::LOADS, 2 * M); g < first_of((ks - 2) * M + s + 1, C::LOADS, 2 * M); ++g)
+              issue(ahead, buf, g);
+          }
+          if constexpr (ks == 3) {
+#pragma unroll
+            for (int r = first_of(s, 2 * OPS, M / 2 + 1); r < first_of(s + 1, 2 * OPS, M / 2 + 1); ++r) read_next(r);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      step(std::integral_constant<int, 0>{});
+      step(std::integral_constant<int, 1>{});
+      lds_barrier();  // every wave has read all of this stage
+      __builtin_amdgcn_sched_barrier(0);
+      step(std::integral_constant<int, 2>{});
+      // The next stage has landed once only this step's loads are pending, and
+      // in a tile's first stage the stores of the tile before, which were
+      // asked for later than it.
+      wait_vmcnt_either<C::LOADS / 2 + C::MIN_STORES, C::LOADS / 2>(stores & (uint32_t)(kt == 0));
+      lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      step(std::integral_constant<int, 3>{});
+#pragma unroll
+      for (int i = 0; i < FU; ++i) sa[i] = na[i];
+#pragma unroll
+      for (int j = 0; j < FT; ++j) sb[j] = nb[j];
+      buf ^= 1;
+    }
+
+    store_tile<C>(a, acc, cur.t0 + wt * FT * 32, cur.u0 + wu * FU * 32, smem + 2 * C::STAGE + wave * C::OUT);
+    if (!more) break;
+    cur = next;
+    L += stride;
+    stores = 1;
+  }
+  wait_vmcnt<0>();  // no load may write to LDS behind the workgroup's end
 }
 
 template <int XT, int FU, int FT, int WAVES>
@@ -351,26 +556,42 @@ hipError_t launch_direct(const Mx4ProductArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class C>
+template <class C, bool FEW>
 hipError_t launch_tiled(const Mx4ProductArgs& a, hipStream_t s) {
+  // a smaller matrix would be read in front of its first row
+  if ((!FEW && a.n < C::BT) || (FEW && a.n >= C::BT) || a.units < C::BU || a.cols <= 256) return hipErrorInvalidValue;
   const int tb = (int)((a.n + C::BT - 1) / C::BT), ub = (a.units + C::BU - 1) / C::BU;
-  TWELL_LAUNCH("mx4_product_tiled", mx4_product_tiled<C>, dim3((unsigned)((int64_t)tb * ub)), C::NT, 0, s, a, tb, ub);
+  const int64_t tiles = (int64_t)tb * ub;
+  const int64_t fit = 256 * C::OCC;  // workgroups that run at a time
+  const dim3 grid((unsigned)(tiles < fit ? tiles : fit));
+  if (mx4_code_bytes(a.cols) % 128 == 0)
+    TWELL_LAUNCH("mx4_product_tiled", (mx4_product_tiled<C, false, FEW>), grid, C::NT, 0, s, a, tb, ub);
+  else
+    TWELL_LAUNCH("mx4_product_tiled", (mx4_product_tiled<C, true, FEW>), grid, C::NT, 0, s, a, tb, ub);
   return hipGetLastError();
 }
 
-using Big = TileCfg<256, 256, 2, 4, 4, 1>;
+using Big = TileCfg<4, 4, 2, 2, 1>;
+using Mid = TileCfg<2, 2, 2, 2, 2>;
+static_assert(Big::BU == kMx4BigTile && Big::BT == kMx4BigTile && Mid::BU == kMx4MidTile && Mid::BT == kMx4MidTile,
+              "the plan's tiles");
 
 }  // namespace
 
-hipError_t launch_mx4_product(const Mx4ProductArgs& a, hipStream_t s) {
-  if (a.x != nullptr)
-    return a.x_bf16 ? launch_direct<X_BF16, 1, 1, 8>(a, s) : launch_direct<X_F32, 1, 1, 8>(a, s);
-  if (a.n <= 16) return launch_direct<X_MX4, 1, 1, 8>(a, s);
-  if (a.n <= 32) return launch_direct<X_MX4, 1, 2, 8>(a, s);
-  if (a.n <= 64) return launch_direct<X_MX4, 1, 4, 8>(a, s);
-  const int64_t tiles = ((a.n + 255) / 256) * ((a.units + 255) / 256);
-  if (tiles < 128) return launch_direct<X_MX4, 4, 4, 4>(a, s);
-  return launch_tiled<Big>(a, s);
+hipError_t launch_mx4_product(Mx4Plan plan, const Mx4ProductArgs& a, hipStream_t s) {
+  switch (plan) {
+    case MX4_FUSED:
+      return a.x_bf16 ? launch_direct<X_BF16, 1, 1, 8>(a, s) : launch_direct<X_F32, 1, 1, 8>(a, s);
+    case MX4_BIG:
+      return launch_tiled<Big, false>(a, s);
+    case MX4_MID:
+      return a.n < Mid::BT ? launch_tiled<Mid, true>(a, s) : launch_tiled<Mid, false>(a, s);
+    default:
+      if (a.n <= 16) return launch_direct<X_MX4, 1, 1, 8>(a, s);
+      if (a.n <= 32) return launch_direct<X_MX4, 1, 2, 8>(a, s);
+      if (a.n <= 64) return launch_direct<X_MX4, 1, 4, 8>(a, s);
+      return launch_direct<X_MX4, 4, 4, 4>(a, s);
+  }
 }
 
 }  // namespace twell

@@ -39,9 +39,43 @@ struct Units {
   __device__ __forceinline__ bool valid(int k) const { return row[k] < rows; }
 };
 
+// One row's scale codes of 512 columns (16 bytes) to their places in the two
+// stages; threads of a wave take neighbouring rows, whose 8 bytes lie together.
+__device__ __forceinline__ void arrange(const Mx4Arrange& a, int64_t i, int cols) {
+  const int segs = (cols + 511) / 512;
+  const int64_t seg = i / a.rows, r = i - seg * a.rows;
+  if (seg >= segs) return;
+  const u32x4_t v = *reinterpret_cast<const u32x4_t*>(a.scale + (r * segs + seg) * 16);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t stage = 2 * seg + h;
+    if (256 * stage >= cols) return;
+    *reinterpret_cast<uint2*>(a.out + (stage * a.pitch + r) * 8) =
+        uint2{__builtin_amdgcn_perm(v[2 * h + 1], v[2 * h], 0x06040200u),
+              __builtin_amdgcn_perm(v[2 * h + 1], v[2 * h], 0x07050301u)};
+  }
+}
+unsigned arrange_blocks(const Mx4Arrange& a, int cols) {
+  return (unsigned)((a.rows * ((cols + 511) / 512) + kThreads - 1) / kThreads);
+}
+
+__global__ __launch_bounds__(kThreads) void mx4_arrange_kernel(Mx4Arrange a, Mx4Arrange b, unsigned blocks_a, int cols) {
+  if (blockIdx.x < blocks_a)
+    arrange(a, (int64_t)blockIdx.x * kThreads + threadIdx.x, cols);
+  else
+    arrange(b, (int64_t)(blockIdx.x - blocks_a) * kThreads + threadIdx.x, cols);
+}
+
+// Workgroups from `blocks` on arrange `also`.
 template <typename TS, bool TAIL>
 __global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(const TS* __restrict__ in, int64_t rows, int cols,
-                                                                uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
+                                                                uint8_t* __restrict__ q, uint8_t* __restrict__ scale,
+                                                                uint8_t* __restrict__ arranged, int64_t pitch,
+                                                                unsigned blocks, Mx4Arrange also) {
+  if (blockIdx.x >= blocks) {
+    arrange(also, (int64_t)(blockIdx.x - blocks) * kThreads + threadIdx.x, cols);
+    return;
+  }
   const int lane = threadIdx.x & 63;
   const int cbytes = mx4_code_bytes(cols), sbytes = mx4_scale_bytes(cols);
   Units u(rows, cols);
@@ -60,7 +94,15 @@ __global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(const TS* __rest
     const int at = 256 * u.seg[k] + 4 * lane;  // of the row's code bytes
     if (at < cbytes) *reinterpret_cast<uint32_t*>(q + u.row[k] * cbytes + at) = c;
     // blocks behind the row's last hold zeros: code 0
-    if ((lane & 3) == 0) scale[u.row[k] * sbytes + 16 * u.seg[k] + lane / 4] = (uint8_t)code;
+    if ((lane & 3) == 0) {
+      const int b = lane / 4;
+      if (arranged == nullptr) {
+        scale[u.row[k] * sbytes + 16 * u.seg[k] + b] = (uint8_t)code;
+      } else {
+        const int64_t stage = 2 * u.seg[k] + b / 8;
+        if (256 * stage < cols) arranged[(stage * pitch + u.row[k]) * 8 + 4 * (b & 1) + b / 2 % 4] = (uint8_t)code;
+      }
+    }
   }
 }
 
@@ -107,14 +149,17 @@ unsigned unit_blocks(int64_t rows, int cols) {
 }
 
 template <typename TS>
-hipError_t quantize_typed(const void* in, int64_t rows, int cols, uint8_t* q, uint8_t* scale, hipStream_t s) {
-  const dim3 grid(unit_blocks(rows, cols));
+hipError_t quantize_typed(const void* in, int64_t rows, int cols, uint8_t* q, uint8_t* scale, uint8_t* arranged,
+                          int64_t pitch, const Mx4Arrange* also, hipStream_t s) {
+  const unsigned blocks = unit_blocks(rows, cols);
+  const Mx4Arrange more = also != nullptr ? *also : Mx4Arrange{};
+  const dim3 grid(blocks + (also != nullptr ? arrange_blocks(more, cols) : 0u));
   if (cols % 8 == 0)
     TWELL_LAUNCH("quantize_mx4", (mx4_quantize_kernel<TS, false>), grid, kThreads, 0, s, (const TS*)in, rows, cols, q,
-                 scale);
+                 scale, arranged, pitch, blocks, more);
   else
     TWELL_LAUNCH("quantize_mx4", (mx4_quantize_kernel<TS, true>), grid, kThreads, 0, s, (const TS*)in, rows, cols, q,
-                 scale);
+                 scale, arranged, pitch, blocks, more);
   return hipGetLastError();
 }
 
@@ -133,9 +178,16 @@ hipError_t dequantize_typed(const uint8_t* q, const uint8_t* scale, int64_t rows
 }  // namespace
 
 hipError_t launch_quantize_mx4(const void* in, int is_bf16, int64_t rows, int cols, uint8_t* q, uint8_t* scale,
-                               hipStream_t s) {
-  return is_bf16 ? quantize_typed<uint16_t>(in, rows, cols, q, scale, s)
-                 : quantize_typed<float>(in, rows, cols, q, scale, s);
+                               uint8_t* arranged, int64_t pitch, const Mx4Arrange* also, hipStream_t s) {
+  return is_bf16 ? quantize_typed<uint16_t>(in, rows, cols, q, scale, arranged, pitch, also, s)
+                 : quantize_typed<float>(in, rows, cols, q, scale, arranged, pitch, also, s);
+}
+
+hipError_t launch_mx4_arrange(const Mx4Arrange& a, const Mx4Arrange& b, int cols, hipStream_t s) {
+  const unsigned blocks = arrange_blocks(a, cols);
+  TWELL_LAUNCH("mx4_arrange", mx4_arrange_kernel, dim3(blocks + arrange_blocks(b, cols)), kThreads, 0, s, a, b, blocks,
+               cols);
+  return hipGetLastError();
 }
 
 hipError_t launch_dequantize_mx4(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols, int out_bf16,

@@ -57,15 +57,21 @@ twell_status check_mx4_shape(int64_t rows, int32_t cols) {
 size_t mx4_codes(int64_t rows, int32_t cols) { return (size_t)rows * twell::mx4_code_bytes(cols); }
 size_t mx4_scales(int64_t rows, int32_t cols) { return (size_t)rows * twell::mx4_scale_bytes(cols); }
 
-// Shape, weights and output shared by the products.
-twell_status check_mx4_product(int64_t n, int32_t cols, int32_t units, const uint8_t* w_q, const uint8_t* w_scale,
-                               twell_dtype y_dtype, void* y, twell::Mx4ProductArgs* a) {
-  twell_status st = check_mx4_shape(n, cols);
+twell_status check_mx4_dims(int64_t n, int32_t cols, int32_t units) {
+  const twell_status st = check_mx4_shape(n, cols);
   if (st != TWELL_OK) return st;
   if (units <= 0) return fail(TWELL_ERR_INVALID_ARG, "units must be > 0");
   if (units > (1 << 24)) return fail(TWELL_ERR_UNSUPPORTED, "units above 2^24");
   if (((n + 15) / 16) * ((units + 15) / 16) > 0x7FFFFFFFll)
     return fail(TWELL_ERR_UNSUPPORTED, "more than 2^31 - 1 output tiles of 16 x 16");
+  return TWELL_OK;
+}
+
+// Shape, weights and output shared by the products.
+twell_status check_mx4_product(int64_t n, int32_t cols, int32_t units, const uint8_t* w_q, const uint8_t* w_scale,
+                               twell_dtype y_dtype, void* y, twell::Mx4ProductArgs* a) {
+  const twell_status st = check_mx4_dims(n, cols, units);
+  if (st != TWELL_OK) return st;
   if (bad_dtype(y_dtype)) return fail(TWELL_ERR_INVALID_ARG, "dtypes must be bf16 or fp32");
   OPS_CHECK_PTR(w_q, mx4_codes(units, cols), "w_q");
   OPS_CHECK_PTR(w_scale, mx4_scales(units, cols), "w_scale");
@@ -80,8 +86,43 @@ twell_status check_mx4_product(int64_t n, int32_t cols, int32_t units, const uin
   return TWELL_OK;
 }
 
-size_t linear_ws_bytes(int64_t n, int32_t cols) {
-  return twell::mx4_product_quantises(n) ? 0 : mx4_codes(n, cols) + mx4_scales(n, cols);
+// Workspaces: the arranged scales of w and x (tiled plans), and in front of
+// them, for the product that quantises x, its MX4 rows (their scales only where
+// they are not arranged at once).
+struct ProductLayout {
+  size_t x_q, x_scale, w_arr, x_arr, total;
+};
+ProductLayout product_layout(twell::Mx4Plan plan, int64_t n, int32_t cols, int32_t units, bool quantise) {
+  const bool tiled = twell::mx4_tiled(plan);
+  ProductLayout L{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t off = at;
+    at += (bytes + 15) / 16 * 16;
+    return off;
+  };
+  const bool rows = quantise && plan != twell::MX4_FUSED;
+  L.x_q = take(rows ? mx4_codes(n, cols) : 0);
+  L.x_scale = take(rows && !tiled ? mx4_scales(n, cols) : 0);
+  L.w_arr = take(tiled ? twell::mx4_arranged_bytes(units, cols) : 0);
+  L.x_arr = take(tiled ? twell::mx4_arranged_bytes(twell::mx4_arranged_rows(n), cols) : 0);
+  L.total = at;
+  return L;
+}
+
+twell_status product_ws(int64_t n, int32_t cols, int32_t units, bool quantise, size_t* ws_bytes) {
+  const twell_status st = check_mx4_dims(n, cols, units);
+  if (st != TWELL_OK) return st;
+  if (ws_bytes == nullptr) return fail(TWELL_ERR_INVALID_ARG, "ws_bytes is NULL");
+  *ws_bytes = n == 0 ? 0 : product_layout(twell::mx4_plan(n, cols, units, !quantise), n, cols, units, quantise).total;
+  twell::set_error(TWELL_OK, "");
+  return TWELL_OK;
+}
+
+twell_status check_ws(void* ws, size_t have, size_t need, const char* small) {
+  if (have < need) return fail(TWELL_ERR_WORKSPACE, small);
+  if (twell::bad_ptr(ws, need)) return fail(TWELL_ERR_WORKSPACE, "workspace is NULL or not 16-byte aligned");
+  return TWELL_OK;
 }
 
 }  // namespace
@@ -194,7 +235,8 @@ twell_status twell_quantize_mx4(int64_t rows, int32_t cols, twell_dtype dtype, c
   OPS_CHECK_PTR(scale, mx4_scales(rows, cols), "scale");
   ok();
   if (rows == 0) return TWELL_OK;
-  return hip_status(twell::launch_quantize_mx4(in, dtype == TWELL_BF16, rows, cols, q, scale, (hipStream_t)stream),
+  return hip_status(twell::launch_quantize_mx4(in, dtype == TWELL_BF16, rows, cols, q, scale, nullptr, 0, nullptr,
+                                               (hipStream_t)stream),
                     "twell_quantize_mx4");
 }
 
@@ -212,55 +254,73 @@ twell_status twell_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t* q, 
                     "twell_dequantize_mx4");
 }
 
+twell_status twell_matmul_mx4_ws(int64_t n, int32_t cols, int32_t units, size_t* ws_bytes) {
+  return product_ws(n, cols, units, false, ws_bytes);
+}
+
 twell_status twell_matmul_mx4(int64_t n, int32_t cols, int32_t units, const uint8_t* x_q, const uint8_t* x_scale,
-                              const uint8_t* w_q, const uint8_t* w_scale, twell_dtype y_dtype, void* y,
-                              void* stream) {
+                              const uint8_t* w_q, const uint8_t* w_scale, twell_dtype y_dtype, void* y, void* ws,
+                              size_t ws_bytes, void* stream) {
   twell::Mx4ProductArgs a{};
-  const twell_status st = check_mx4_product(n, cols, units, w_q, w_scale, y_dtype, y, &a);
+  twell_status st = check_mx4_product(n, cols, units, w_q, w_scale, y_dtype, y, &a);
   if (st != TWELL_OK) return st;
   OPS_CHECK_PTR(x_q, mx4_codes(n, cols), "x_q");
   OPS_CHECK_PTR(x_scale, mx4_scales(n, cols), "x_scale");
+  if (n == 0) return ok();
+  const twell::Mx4Plan plan = twell::mx4_plan(n, cols, units, true);
+  const ProductLayout L = product_layout(plan, n, cols, units, false);
+  if ((st = check_ws(ws, ws_bytes, L.total, "workspace smaller than twell_matmul_mx4_ws says")) != TWELL_OK) return st;
   ok();
-  if (n == 0) return TWELL_OK;
   a.x_q = x_q;
   a.x_scale = x_scale;
-  return hip_status(twell::launch_mx4_product(a, (hipStream_t)stream), "twell_matmul_mx4");
+  if (twell::mx4_tiled(plan)) {
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    const twell::Mx4Arrange w{w_scale, base + L.w_arr, units, units};
+    const twell::Mx4Arrange x{x_scale, base + L.x_arr, n, twell::mx4_arranged_rows(n)};
+    const hipError_t e = twell::launch_mx4_arrange(w, x, cols, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_status(e, "twell_matmul_mx4");
+    a.w_arr = w.out;
+    a.x_arr = x.out;
+  }
+  return hip_status(twell::launch_mx4_product(plan, a, (hipStream_t)stream), "twell_matmul_mx4");
 }
 
-twell_status twell_linear_mx4_ws(int64_t n, int32_t cols, size_t* ws_bytes) {
-  const twell_status st = check_mx4_shape(n, cols);
-  if (st != TWELL_OK) return st;
-  if (ws_bytes == nullptr) return fail(TWELL_ERR_INVALID_ARG, "ws_bytes is NULL");
-  *ws_bytes = linear_ws_bytes(n, cols);
-  return ok();
+twell_status twell_linear_mx4_ws(int64_t n, int32_t cols, int32_t units, size_t* ws_bytes) {
+  return product_ws(n, cols, units, true, ws_bytes);
 }
 
 twell_status twell_linear_mx4(int64_t n, int32_t cols, int32_t units, twell_dtype x_dtype, const void* x,
                               const uint8_t* w_q, const uint8_t* w_scale, twell_dtype y_dtype, void* y, void* ws,
                               size_t ws_bytes, void* stream) {
   twell::Mx4ProductArgs a{};
-  const twell_status st = check_mx4_product(n, cols, units, w_q, w_scale, y_dtype, y, &a);
+  twell_status st = check_mx4_product(n, cols, units, w_q, w_scale, y_dtype, y, &a);
   if (st != TWELL_OK) return st;
   if (bad_dtype(x_dtype)) return fail(TWELL_ERR_INVALID_ARG, "dtypes must be bf16 or fp32");
   OPS_CHECK_PTR(x, (size_t)n * cols * size_of(x_dtype), "x");
-  const size_t need = linear_ws_bytes(n, cols);
-  if (ws_bytes < need) return fail(TWELL_ERR_WORKSPACE, "workspace smaller than twell_linear_mx4_ws says");
-  if (twell::bad_ptr(ws, need)) return fail(TWELL_ERR_WORKSPACE, "workspace is NULL or not 16-byte aligned");
+  if (n == 0) return ok();
+  const twell::Mx4Plan plan = twell::mx4_plan(n, cols, units, false);
+  const ProductLayout L = product_layout(plan, n, cols, units, true);
+  if ((st = check_ws(ws, ws_bytes, L.total, "workspace smaller than twell_linear_mx4_ws says")) != TWELL_OK) return st;
   ok();
-  if (n == 0) return TWELL_OK;
-  if (twell::mx4_product_quantises(n)) {
+  const int x_bf16 = x_dtype == TWELL_BF16;
+  if (plan == twell::MX4_FUSED) {
     a.x = x;
-    a.x_bf16 = x_dtype == TWELL_BF16;
+    a.x_bf16 = x_bf16;
   } else {
-    uint8_t* x_q = static_cast<uint8_t*>(ws);
-    uint8_t* x_scale = x_q + mx4_codes(n, cols);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    const bool tiled = twell::mx4_tiled(plan);
+    uint8_t* const x_arr = tiled ? base + L.x_arr : nullptr;
+    const twell::Mx4Arrange w{w_scale, base + L.w_arr, units, units};
     const hipError_t e =
-        twell::launch_quantize_mx4(x, x_dtype == TWELL_BF16, n, cols, x_q, x_scale, (hipStream_t)stream);
+        twell::launch_quantize_mx4(x, x_bf16, n, cols, base + L.x_q, tiled ? nullptr : base + L.x_scale, x_arr,
+                                   twell::mx4_arranged_rows(n), tiled ? &w : nullptr, (hipStream_t)stream);
     if (e != hipSuccess) return hip_status(e, "twell_linear_mx4");
-    a.x_q = x_q;
-    a.x_scale = x_scale;
+    a.x_q = base + L.x_q;
+    a.x_scale = base + L.x_scale;
+    a.w_arr = w.out;
+    a.x_arr = x_arr;
   }
-  return hip_status(twell::launch_mx4_product(a, (hipStream_t)stream), "twell_linear_mx4");
+  return hip_status(twell::launch_mx4_product(plan, a, (hipStream_t)stream), "twell_linear_mx4");
 }
 
 }  // extern "C"

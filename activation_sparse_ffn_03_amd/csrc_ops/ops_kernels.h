@@ -56,29 +56,59 @@ hipError_t launch_add_rms_norm_bwd(const NormBwdArgs& a, hipStream_t s);
 constexpr int kMx4MaxCols = 1 << 20;
 __host__ __device__ inline int mx4_code_bytes(int cols) { return (cols + 127) / 128 * 64; }
 __host__ __device__ inline int mx4_scale_bytes(int cols) { return (cols + 511) / 512 * 16; }
+// Scale codes arranged for the tiled product: [stage of 256 columns][row][8],
+// the even blocks' four codes, then the odd blocks'.
+struct Mx4Arrange {
+  const uint8_t* scale;  // [rows] MX4 rows' scales
+  uint8_t* out;          // [ceil(cols / 256)][pitch][8]
+  int64_t rows, pitch;
+};
+// With `arranged` the scale codes are written there (pitch `pitch`) in place of
+// `scale`, and `also` is arranged by further workgroups of the same launch.
 hipError_t launch_quantize_mx4(const void* in, int is_bf16, int64_t rows, int cols, uint8_t* q, uint8_t* scale,
-                               hipStream_t s);
+                               uint8_t* arranged, int64_t pitch, const Mx4Arrange* also, hipStream_t s);
+hipError_t launch_mx4_arrange(const Mx4Arrange& a, const Mx4Arrange& b, int cols, hipStream_t s);
 hipError_t launch_dequantize_mx4(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols, int out_bf16,
                                  void* out, hipStream_t s);
 
-// y[i][c] = sum over blocks b of 2^(xs + ws - 254) * sum_k xq wq. Either x_q
-// and x_scale hold x's MX4 rows, or x holds bf16 / fp32 rows that the kernel
-// quantises itself (mx4_product_quantises).
+// How a product of n tokens, cols columns and `units` units runs.
+enum Mx4Plan {
+  MX4_FUSED,   // few tokens: straight from memory, x quantised in registers
+  MX4_DIRECT,  // straight from memory
+  MX4_MID,     // 128 x 128 tiles through LDS
+  MX4_BIG      // 256 x 256 tiles through LDS
+};
+constexpr int kMx4MidTile = 128, kMx4BigTile = 256;
+constexpr int kMx4FusedTokens = 16;   // up to here the product quantises x itself
+constexpr int kMx4DirectTokens = 64;  // up to here the weights are read once however few their tiles
+inline Mx4Plan mx4_plan(int64_t n, int cols, int units, bool x_is_mx4) {
+  if (n <= kMx4FusedTokens && !x_is_mx4) return MX4_FUSED;
+  if (n <= kMx4DirectTokens || units < kMx4MidTile || cols <= 256) return MX4_DIRECT;
+  if (n < kMx4BigTile || units < kMx4BigTile) return MX4_MID;
+  // 256 x 256 tiles once there are more of them than compute units
+  const int64_t tiles = ((n + 255) / 256) * ((units + 255) / 256);
+  return tiles > 256 ? MX4_BIG : MX4_MID;
+}
+inline bool mx4_tiled(Mx4Plan p) { return p == MX4_MID || p == MX4_BIG; }
+// Rows that the arranged scales of x are given: those of one tile at least.
+__host__ __device__ inline int64_t mx4_arranged_rows(int64_t n) { return n < kMx4MidTile ? kMx4MidTile : n; }
+inline size_t mx4_arranged_bytes(int64_t rows, int cols) { return (size_t)((cols + 255) / 256) * rows * 8; }
+
+// y[i][c] = sum over blocks b of 2^(xs + ws - 254) * sum_k xq wq.
 struct Mx4ProductArgs {
   int64_t n;
   int cols, units;
-  const uint8_t* x_q;
-  const uint8_t* x_scale;
-  const void* x;  // null: x_q and x_scale
+  const uint8_t* x_q;      // MX4 rows of x (not MX4_FUSED)
+  const uint8_t* x_scale;  // MX4_DIRECT
+  const void* x;           // MX4_FUSED: bf16 / fp32 rows
   int x_bf16;
   const uint8_t* w_q;
   const uint8_t* w_scale;
+  const uint8_t* x_arr;    // MX4_MID, MX4_BIG: arranged scales, pitch mx4_arranged_rows(n) and units
+  const uint8_t* w_arr;
   void* y;  // [n][units]
   int y_bf16;
 };
-// Tokens up to which the product quantises x in its registers.
-constexpr int kMx4FusedTokens = 16;
-inline bool mx4_product_quantises(int64_t n) { return n <= kMx4FusedTokens; }
-hipError_t launch_mx4_product(const Mx4ProductArgs& a, hipStream_t s);
+hipError_t launch_mx4_product(Mx4Plan plan, const Mx4ProductArgs& a, hipStream_t s);
 
 }  // namespace twell

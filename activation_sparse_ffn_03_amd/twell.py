@@ -32,7 +32,8 @@ EXPORTS = ("twell_status_str", "twell_last_error", "twell_n_tiles", "twell_query
            "twell_gate_pack_fp8_ws", "twell_ffn_fwd", "twell_ffn_forward", "twell_ffn_forward_fp8",
            "twell_ffn_forward_noalloc", "twell_route_hybrid", "twell_ffn_bwd", "twell_add_rms_norm",
            "twell_add_rms_norm_bwd_ws", "twell_add_rms_norm_bwd", "twell_mx4_sizes", "twell_quantize_mx4",
-           "twell_dequantize_mx4", "twell_matmul_mx4", "twell_linear_mx4_ws", "twell_linear_mx4", "twell_trace_start",
+           "twell_dequantize_mx4", "twell_matmul_mx4_ws", "twell_matmul_mx4", "twell_linear_mx4_ws",
+           "twell_linear_mx4", "twell_trace_start",
            "twell_trace_stop", "twell_trace_count", "twell_trace_dropped", "twell_trace_get")
 
 # Bytes of the library's static scratch used by twell_ffn_forward_noalloc.
@@ -132,9 +133,11 @@ def lib() -> ctypes.CDLL:
         L.twell_dequantize_mx4.restype = ctypes.c_int
         L.twell_dequantize_mx4.argtypes = [i64, i32, vp, vp, ctypes.c_int, vp, vp]
         L.twell_matmul_mx4.restype = ctypes.c_int
-        L.twell_matmul_mx4.argtypes = [i64, i32, i32, vp, vp, vp, vp, ctypes.c_int, vp, vp]
+        L.twell_matmul_mx4.argtypes = [i64, i32, i32, vp, vp, vp, vp, ctypes.c_int, vp, vp, sz, vp]
+        L.twell_matmul_mx4_ws.restype = ctypes.c_int
+        L.twell_matmul_mx4_ws.argtypes = [i64, i32, i32, psz]
         L.twell_linear_mx4_ws.restype = ctypes.c_int
-        L.twell_linear_mx4_ws.argtypes = [i64, i32, psz]
+        L.twell_linear_mx4_ws.argtypes = [i64, i32, i32, psz]
         L.twell_linear_mx4.restype = ctypes.c_int
         L.twell_linear_mx4.argtypes = [i64, i32, i32, ctypes.c_int, vp, vp, vp, ctypes.c_int, vp, vp, sz, vp]
         L.twell_trace_start.restype = ctypes.c_int
@@ -519,24 +522,36 @@ def dequantize_mx4(codes, scales, cols: int, dtype=torch.bfloat16, out=None, str
     return out
 
 
-def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bfloat16, out=None, stream=None):
+def matmul_mx4_ws(rows: int, cols: int, units: int) -> int:
+    """Workspace bytes of matmul_mx4."""
+    n = ctypes.c_size_t()
+    _check(lib().twell_matmul_mx4_ws(rows, cols, units, ctypes.byref(n)), "twell_matmul_mx4_ws")
+    return n.value
+
+
+def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bfloat16, out=None, ws=None,
+               stream=None):
     """x · w^T of MX4 rows with `cols` columns (twell_matmul_mx4): [rows of x,
-    rows of w] in bf16 or fp32, written into `out` when given."""
+    rows of w] in bf16 or fp32, written into `out` when given; ws (bytes of
+    matmul_mx4_ws) is allocated here when not."""
     n, units = x_codes.shape[0], w_codes.shape[0]
-    (xq, xs), (wq, ws) = mx4_shapes(n, cols), mx4_shapes(units, cols)
+    (xq, xs), (wq, wsc) = mx4_shapes(n, cols), mx4_shapes(units, cols)
     args = (_addr(x_codes, "x_codes", xq, torch.uint8), _addr(x_scales, "x_scales", xs, torch.uint8),
-            _addr(w_codes, "w_codes", wq, torch.uint8), _addr(w_scales, "w_scales", ws, torch.uint8))
+            _addr(w_codes, "w_codes", wq, torch.uint8), _addr(w_scales, "w_scales", wsc, torch.uint8))
     if out is None:
         out = torch.empty((n, units), dtype=dtype, device=x_codes.device)
+    if ws is None:
+        ws = torch.empty(matmul_mx4_ws(n, cols, units), dtype=torch.uint8, device=x_codes.device)
     _check(lib().twell_matmul_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units)),
-                                  _stream(stream)), "twell_matmul_mx4")
+                                  ws.data_ptr() or None, ws.numel() * ws.element_size(), _stream(stream)),
+           "twell_matmul_mx4")
     return out
 
 
-def linear_mx4_ws(rows: int, cols: int) -> int:
+def linear_mx4_ws(rows: int, cols: int, units: int) -> int:
     """Workspace bytes of linear_mx4."""
     n = ctypes.c_size_t()
-    _check(lib().twell_linear_mx4_ws(rows, cols, ctypes.byref(n)), "twell_linear_mx4_ws")
+    _check(lib().twell_linear_mx4_ws(rows, cols, units, ctypes.byref(n)), "twell_linear_mx4_ws")
     return n.value
 
 
@@ -555,7 +570,7 @@ def linear_mx4(x, w_codes, w_scales, dtype=torch.bfloat16, out=None, ws=None, st
     if out is None:
         out = torch.empty((n, units), dtype=dtype, device=x.device)
     if ws is None:
-        ws = torch.empty(linear_mx4_ws(n, cols), dtype=torch.uint8, device=x.device)
+        ws = torch.empty(linear_mx4_ws(n, cols, units), dtype=torch.uint8, device=x.device)
     _check(lib().twell_linear_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units)),
                                   ws.data_ptr() or None, ws.numel() * ws.element_size(), _stream(stream)),
            "twell_linear_mx4")

@@ -400,17 +400,23 @@ twell_status twell_quantize_mx4(int64_t rows, int32_t cols, twell_dtype dtype, c
 twell_status twell_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t* q, const uint8_t* scale,
                                   twell_dtype dtype, void* out, void* stream);
 
+/* Workspace bytes of twell_matmul_mx4 (host-only query; may be 0): for larger
+ * products both operands' scale codes in the order the tiles take them. */
+twell_status twell_matmul_mx4_ws(int64_t n, int32_t cols, int32_t units, size_t* ws_bytes);
+
 /* y[i][c] = sum_k x[i,k] * w[c,k] for MX4 rows x ([n] rows of cols columns) and
  * w ([units] rows): the products of a block's codes are exact, their sums and
  * the scaled blocks' are held in fp32, y [n][units] is rounded once to
- * y_dtype. NaN scales make their row or column of y NaN. n == 0 is a no-op. */
+ * y_dtype. NaN scales make their row or column of y NaN. n == 0 is a no-op.
+ * ws: at least the queried bytes (NULL allowed when that is 0). */
 twell_status twell_matmul_mx4(int64_t n, int32_t cols, int32_t units, const uint8_t* x_q, const uint8_t* x_scale,
-                              const uint8_t* w_q, const uint8_t* w_scale, twell_dtype y_dtype, void* y,
-                              void* stream);
+                              const uint8_t* w_q, const uint8_t* w_scale, twell_dtype y_dtype, void* y, void* ws,
+                              size_t ws_bytes, void* stream);
 
-/* Workspace bytes of twell_linear_mx4 (host-only query): the MX4 rows of x, or
- * 0 for small n, where the product quantises x as it reads it. */
-twell_status twell_linear_mx4_ws(int64_t n, int32_t cols, size_t* ws_bytes);
+/* Workspace bytes of twell_linear_mx4 (host-only query): the MX4 rows of x and
+ * what twell_matmul_mx4 needs, or 0 for small n, where the product quantises x
+ * as it reads it. */
+twell_status twell_linear_mx4_ws(int64_t n, int32_t cols, int32_t units, size_t* ws_bytes);
 
 /* twell_quantize_mx4 of x [n][cols] (bf16 or fp32) and twell_matmul_mx4 in one
  * call: the gate's pre-activation for twell_pack_preact when w is the gate

@@ -106,7 +106,8 @@ def _product_tol(xv, wv, y, dtype):
 # rows and units below, at and above every tile's edge; widths with part blocks, part steps and part scale words
 PRODUCTS = [(1, 1, 1), (1, 128, 16), (1, 4096, 1000), (2, 33, 17), (5, 520, 300), (15, 1990, 64), (16, 2048, 129),
             (17, 96, 31), (24, 2048, 250), (32, 1000, 48), (33, 640, 99), (63, 130, 100), (64, 512, 512), (65, 129, 65),
-            (100, 1990, 130), (128, 256, 4), (200, 700, 511), (257, 4096, 300), (1003, 1990, 81)]
+            (100, 1990, 130), (128, 256, 4), (200, 700, 511), (257, 4096, 300), (1003, 1990, 81),
+            (65, 257, 128), (127, 300, 136), (128, 384, 128), (129, 385, 132), (130, 512, 192), (255, 640, 255)]
 
 
 @pytest.mark.parametrize("n,cols,units", PRODUCTS)
@@ -136,8 +137,8 @@ def test_products(n, cols, units):
             assert torch.equal(again, y)
 
 
-@pytest.mark.parametrize("n,cols,units", [(3000, 640, 4352), (4099, 1990, 3075), (8192, 130, 2053), (2304, 4096, 4096),
-                                          (700, 2048, 5632)])
+@pytest.mark.parametrize("n,cols,units", [(4352, 640, 4352), (4099, 1990, 4611), (8192, 130, 2053), (8195, 384, 2304),
+                                          (2304, 4096, 8192), (700, 2048, 5632), (1001, 1152, 1003), (90, 4096, 2056)])
 def test_large_products_are_exact(n, cols, units):
     """Small whole numbers: every sum is exact in fp32, whatever its order, so y is too. Covers whole grids of the
     tiled product with edges on both sides, against float64 on the GPU's own fp32-exact product."""
@@ -158,7 +159,7 @@ def test_large_products_are_exact(n, cols, units):
         assert torch.equal(tw.linear_mx4(x.to(xdt), wq, ws), want.to(BF))
 
 
-@pytest.mark.parametrize("n,units", [(4, 40), (20, 40), (70, 70), (2100, 2100)])
+@pytest.mark.parametrize("n,units", [(4, 40), (20, 40), (70, 70), (70, 300), (300, 200), (4500, 4500)])
 def test_nan_blocks_mark_their_row_and_column(n, units):
     require_gpu()
     cols = 300
@@ -183,7 +184,7 @@ def test_empty():
     assert tw.linear_mx4(e, *w).shape == (0, 5) and tw.matmul_mx4(q, s, *w, 300).shape == (0, 5)
 
 
-@pytest.mark.parametrize("n", [3, 40, 2100])
+@pytest.mark.parametrize("n", [3, 40, 100, 2100, 8200])
 def test_other_stream_and_graph_replay(n):
     require_gpu()
     cols, units = 520, 2100
@@ -197,7 +198,7 @@ def test_other_stream_and_graph_replay(n):
     torch.cuda.current_stream().wait_stream(side)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
-    y, space = torch.empty(n, units, dtype=BF, device="cuda"), tw.alloc_workspace(tw.linear_mx4_ws(n, cols))
+    y, space = torch.empty(n, units, dtype=BF, device="cuda"), tw.alloc_workspace(tw.linear_mx4_ws(n, cols, units))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         tw.linear_mx4(x, wq, ws, out=y, ws=space)

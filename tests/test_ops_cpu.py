@@ -103,8 +103,22 @@ def test_mx4_sizes_and_shapes():
     assert _sizes(-1, 64)[0] == 1 and _sizes(1, 0)[0] == 1 and _sizes(1, (1 << 20) + 1)[0] == 2
     assert _sizes(1 << 31, 64)[0] == 2 and _sizes((1 << 31) - 1, 1 << 20)[0] == 2
     assert tw.lib().twell_mx4_sizes(1, 64, None, None) == 1
-    assert tw.linear_mx4_ws(1, 4096) == 0
-    assert tw.linear_mx4_ws(1000, 1990) == 1000 * (1024 + 64)
+
+
+def test_mx4_product_workspaces():
+    """Nothing for few tokens, x's MX4 rows for some more, and for tiles both operands' scales by 256 columns (8 bytes
+    a row, 128 rows at least) in place of x's scale rows."""
+    assert tw.linear_mx4_ws(1, 4096, 11008) == 0 and tw.linear_mx4_ws(0, 4096, 11008) == 0
+    assert tw.linear_mx4_ws(40, 1990, 8100) == 40 * (1024 + 64) and tw.matmul_mx4_ws(40, 1990, 8100) == 0
+    assert tw.linear_mx4_ws(1000, 1990, 100) == 1000 * (1024 + 64)  # fewer units than a tile
+    assert tw.linear_mx4_ws(1000, 200, 8100) == 1000 * (128 + 16)   # one stage of columns
+    arranged = 8 * 8 * (8100 + 1000)
+    assert tw.linear_mx4_ws(1000, 1990, 8100) == 1000 * 1024 + arranged and tw.matmul_mx4_ws(1000, 1990, 8100) == arranged
+    assert tw.matmul_mx4_ws(70, 300, 128) == 2 * 8 * (128 + 128)
+    for f in (tw.lib().twell_linear_mx4_ws, tw.lib().twell_matmul_mx4_ws):
+        assert f(1, 64, 8, None) == 1
+        n = ctypes.c_size_t()
+        assert f(1, 64, 0, ctypes.byref(n)) == 1 and f(-1, 64, 8, ctypes.byref(n)) == 1 and f(1, 1 << 21, 8, ctypes.byref(n)) == 2
 
 
 def test_mx4_refusals():
@@ -114,10 +128,14 @@ def test_mx4_refusals():
     assert q(a=None) == 1 and q(c=ODD) == 1 and q(s=None) == 1 and b"scale" in L.twell_last_error()
     d = lambda rows=4, cols=64, c=FAKE, s=FAKE, dt=0, o=FAKE: L.twell_dequantize_mx4(rows, cols, c, s, dt, o, None)  # noqa: E731
     assert d(rows=-1) == 1 and d(c=None) == 1 and d(s=ODD) == 1 and d(dt=2) == 1 and d(o=None) == 1
-    m = lambda n=4, k=64, u=8, a=FAKE, b=FAKE, c=FAKE, e=FAKE, dt=0, y=FAKE: L.twell_matmul_mx4(n, k, u, a, b, c, e, dt, y, None)  # noqa: E731
+    m = lambda n=4, k=64, u=8, a=FAKE, b=FAKE, c=FAKE, e=FAKE, dt=0, y=FAKE, ws=None, b2=0: L.twell_matmul_mx4(  # noqa: E731
+        n, k, u, a, b, c, e, dt, y, ws, b2, None)
     for kw in (dict(n=-1), dict(k=0), dict(u=0), dict(a=None), dict(b=ODD), dict(c=None), dict(e=None), dict(dt=3), dict(y=None)):
         assert m(**kw) == 1, kw
     assert m(u=(1 << 24) + 1) == 2 and m(n=(1 << 31) - 1, u=1 << 20) == 2
+    need = 2 * 8 * (128 + 128)
+    assert m(n=70, k=300, u=128) == 3 and m(n=70, k=300, u=128, ws=FAKE, b2=need - 1) == 3
+    assert m(n=70, k=300, u=128, ws=ODD, b2=need) == 3 and b"workspace" in L.twell_last_error()
     f = lambda n=64, k=64, u=8, xd=0, x=FAKE, c=FAKE, e=FAKE, dt=0, y=FAKE, ws=FAKE, b=64 * 80: L.twell_linear_mx4(  # noqa: E731
         n, k, u, xd, x, c, e, dt, y, ws, b, None)
     for kw in (dict(xd=9), dict(x=None), dict(x=ODD), dict(c=None), dict(y=ODD)):
@@ -129,7 +147,7 @@ def test_mx4_of_no_rows_needs_no_device():
     L = tw.lib()
     assert L.twell_quantize_mx4(0, 64, 0, None, None, None, None) == 0
     assert L.twell_dequantize_mx4(0, 64, None, None, 0, None, None) == 0
-    assert L.twell_matmul_mx4(0, 64, 8, None, None, FAKE, FAKE, 0, None, None) == 0
+    assert L.twell_matmul_mx4(0, 64, 8, None, None, FAKE, FAKE, 0, None, None, 0, None) == 0
     assert L.twell_linear_mx4(0, 64, 8, 0, None, FAKE, FAKE, 0, None, None, 0, None) == 0
 
 
