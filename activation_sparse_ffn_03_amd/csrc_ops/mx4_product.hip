@@ -86,13 +86,13 @@ __device__ __forceinline__ void store_kind(const Mx4ProductArgs& a, Put put) {
 
 // ---------------------------------------------------------------- direct
 
-// Block kb of 128 columns kt of one row of x, quantised: codes and scale code.
+// Block b of a row of x, quantised: codes and scale code (zeros behind its end).
 template <typename TX, bool TAIL>
-__device__ __forceinline__ u32x4_t quantize_block(const TX* row, int kt, int kb, int cols, uint32_t& code) {
+__device__ __forceinline__ u32x4_t quantize_block(const TX* row, int b, int cols, uint32_t& code) {
   Raw8<TX> raw[4];
   uint32_t m = 0;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) raw[c].template load<TAIL>(row, 16 * kt + 4 * kb + c, cols);
+  for (int c = 0; c < 4; ++c) raw[c].template load<TAIL>(row, 4 * b + c, cols);
 #pragma unroll
   for (int c = 0; c < 4; ++c) m = max(m, raw[c].max_bits());
   code = mx4_scale_code(m);
@@ -103,34 +103,46 @@ __device__ __forceinline__ u32x4_t quantize_block(const TX* row, int kt, int kb,
   return q;
 }
 
-// Tile of 16 FU units by 16 FT tokens.
+// Tile of 16 FU units by 16 FT tokens. A wave's step is 256 columns, a whole
+// cache line of codes a row: lane l holds blocks 2 (l >> 4) and 2 (l >> 4) + 1
+// of its row's eight, one for each of two matrix instructions (which blocks
+// share an instruction is free as long as both operands agree).
+// With bf16 or fp32 x (one tile of tokens, at most kMx4FusedBlocks blocks) each
+// workgroup quantises all of x into LDS, one block a thread at a time, while
+// its first weights are on their way.
 template <int XT, int FU, int FT, int WAVES, bool TAIL>
 __global__ __launch_bounds__(64 * WAVES) void mx4_product_direct(Mx4ProductArgs a, int token_tiles) {
   __shared__ f32x4_t red[WAVES][FU * FT][64];
+  constexpr int XBLOCKS = XT == X_MX4 ? 1 : kMx4FusedBlocks;
+  __shared__ u32x4_t x_codes[XBLOCKS];
+  __shared__ uint8_t x_scales[XBLOCKS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int row = lane & 15, kb = lane >> 4;
   const int64_t L = xcd_run_block(blockIdx.x, gridDim.x);  // neighbours in one L2 share their weights
   const int64_t t0 = L % token_tiles * (16 * FT);
   const int u0 = (int)(L / token_tiles) * (16 * FU);
   const int cbytes = mx4_code_bytes(a.cols), sbytes = mx4_scale_bytes(a.cols);
-  const int KT = cbytes / 64;
+  const int steps = (cbytes + 127) / 128;
 
   // Rows behind the last unit or token read the last one: their results are
   // not stored.
   const uint8_t *wq[FU], *ws[FU], *xq[FT], *xs[FT];
-  int64_t tok[FT];
 #pragma unroll
   for (int i = 0; i < FU; ++i) {
     const int64_t u = min(u0 + 16 * i + row, a.units - 1);
-    wq[i] = a.w_q + u * cbytes + 16 * kb;
-    ws[i] = a.w_scale + u * sbytes + kb;
+    wq[i] = a.w_q + u * cbytes + 32 * kb;
+    ws[i] = a.w_scale + u * sbytes + 2 * kb;
   }
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
-    const int64_t t = t0 + 16 * j + row;
-    tok[j] = t < a.n ? t : a.n - 1;
-    xq[j] = a.x_q + tok[j] * cbytes + 16 * kb;
-    xs[j] = a.x_scale + tok[j] * sbytes + kb;
+    const int64_t t = min(t0 + 16 * j + row, a.n - 1);
+    if constexpr (XT == X_MX4) {
+      xq[j] = a.x_q + t * cbytes + 32 * kb;
+      xs[j] = a.x_scale + t * sbytes + 2 * kb;
+    } else {
+      xq[j] = reinterpret_cast<const uint8_t*>(x_codes + t * 8 * steps + 2 * kb);
+      xs[j] = x_scales + t * 8 * steps + 2 * kb;
+    }
   }
   f32x4_t acc[FU][FT];
 #pragma unroll
@@ -138,37 +150,63 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_product_direct(Mx4ProductArgs 
 #pragma unroll
     for (int j = 0; j < FT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // several steps' loads in flight at a time; a step behind the last is zeros
-  constexpr int DEPTH = FU * FT >= 16 ? 2 : 4;
-  for (int k0 = wave; k0 < KT; k0 += DEPTH * WAVES) {
-    u32x4_t aw[DEPTH][FU], bx[DEPTH][FT];
-    uint32_t sa[DEPTH][FU], sb[DEPTH][FT];
+  // several steps' loads in flight at a time; blocks behind the rows' last are
+  // zeros (rows end with a whole 128 columns, 2 blocks of each lane or none)
+  constexpr int DEPTH = FU * FT >= 16 ? 1 : 2;
+  u32x4_t aw[DEPTH][2][FU], bx[DEPTH][2][FT];
+  uint32_t sa[DEPTH][FU], sb[DEPTH][FT];
+  auto load_w = [&](int k0) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
       const int kt = k0 + d * WAVES;
-      const bool in = kt < KT;
+      const bool in = 128 * kt + 32 * kb < cbytes;
 #pragma unroll
       for (int i = 0; i < FU; ++i) {
-        aw[d][i] = in ? *reinterpret_cast<const u32x4_t*>(wq[i] + 64 * kt) : u32x4_t{0u, 0u, 0u, 0u};
-        sa[d][i] = in ? ws[i][4 * kt] : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          aw[d][h][i] = in ? *reinterpret_cast<const u32x4_t*>(wq[i] + 128 * kt + 16 * h) : u32x4_t{0u, 0u, 0u, 0u};
+        sa[d][i] = in ? *reinterpret_cast<const uint16_t*>(ws[i] + 8 * kt) : 0u;
       }
+    }
+  };
+  if constexpr (XT != X_MX4) {
+    load_w(wave);
+    using TX = std::conditional_t<XT == X_BF16, uint16_t, float>;
+    for (int b = threadIdx.x; b < (int)a.n * 8 * steps; b += 64 * WAVES) {
+      const int t = b / (8 * steps);
+      uint32_t code;
+      x_codes[b] = quantize_block<TX, TAIL>(static_cast<const TX*>(a.x) + (int64_t)t * a.cols, b - t * 8 * steps, a.cols,
+                                            code);
+      x_scales[b] = (uint8_t)code;
+    }
+    lds_barrier();
+  }
+  for (int k0 = wave; k0 < steps; k0 += DEPTH * WAVES) {
+    if (XT == X_MX4 || k0 != wave) load_w(k0);
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      const int kt = k0 + d * WAVES;
+      const bool in = 128 * kt + 32 * kb < cbytes;
 #pragma unroll
       for (int j = 0; j < FT; ++j) {
-        if constexpr (XT == X_MX4) {
-          bx[d][j] = in ? *reinterpret_cast<const u32x4_t*>(xq[j] + 64 * kt) : u32x4_t{0u, 0u, 0u, 0u};
-          sb[d][j] = in ? xs[j][4 * kt] : 0;
-        } else {
-          using TX = std::conditional_t<XT == X_BF16, uint16_t, float>;
-          bx[d][j] = quantize_block<TX, TAIL>(static_cast<const TX*>(a.x) + tok[j] * a.cols, kt, kb, a.cols, sb[d][j]);
-        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          bx[d][h][j] = in ? *reinterpret_cast<const u32x4_t*>(xq[j] + 128 * kt + 16 * h)
+                           : u32x4_t{0u, 0u, 0u, 0u};
+        sb[d][j] = in ? *reinterpret_cast<const uint16_t*>(xs[j] + 8 * kt) : 0u;
       }
     }
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
+    for (int d = 0; d < DEPTH; ++d) {
 #pragma unroll
       for (int i = 0; i < FU; ++i)
 #pragma unroll
-        for (int j = 0; j < FT; ++j) acc[i][j] = mfma(aw[d][i], bx[d][j], acc[i][j], sa[d][i], sb[d][j]);
+        for (int j = 0; j < FT; ++j) acc[i][j] = mfma<0>(aw[d][0][i], bx[d][0][j], acc[i][j], sa[d][i], sb[d][j]);
+#pragma unroll
+      for (int i = 0; i < FU; ++i)
+#pragma unroll
+        for (int j = 0; j < FT; ++j) acc[i][j] = mfma<1>(aw[d][1][i], bx[d][1][j], acc[i][j], sa[d][i], sb[d][j]);
+    }
   }
 
 #pragma unroll
@@ -581,16 +619,21 @@ static_assert(Big::BU == kMx4BigTile && Big::BT == kMx4BigTile && Mid::BU == kMx
 hipError_t launch_mx4_product(Mx4Plan plan, const Mx4ProductArgs& a, hipStream_t s) {
   switch (plan) {
     case MX4_FUSED:
-      return a.x_bf16 ? launch_direct<X_BF16, 1, 1, 8>(a, s) : launch_direct<X_F32, 1, 1, 8>(a, s);
+      // up to 4 tokens 16 units and 4 waves a workgroup, above twice of both: x
+      // is quantised half as often (us at 1 and 8 x 4096 x 11008: 6.6 and 10.7
+      // against 8.0 and 10.6; 16 x 2048 x 5632: 7.3 against 5.7)
+      if (a.n <= 4) return a.x_bf16 ? launch_direct<X_BF16, 1, 1, 4>(a, s) : launch_direct<X_F32, 1, 1, 4>(a, s);
+      return a.x_bf16 ? launch_direct<X_BF16, 2, 1, 8>(a, s) : launch_direct<X_F32, 2, 1, 8>(a, s);
     case MX4_BIG:
       return launch_tiled<Big, false>(a, s);
     case MX4_MID:
       return a.n < Mid::BT ? launch_tiled<Mid, true>(a, s) : launch_tiled<Mid, false>(a, s);
     default:
-      if (a.n <= 16) return launch_direct<X_MX4, 1, 1, 8>(a, s);
-      if (a.n <= 32) return launch_direct<X_MX4, 1, 2, 8>(a, s);
-      if (a.n <= 64) return launch_direct<X_MX4, 1, 4, 8>(a, s);
-      return launch_direct<X_MX4, 4, 4, 4>(a, s);
+      if (a.n <= 16) return launch_direct<X_MX4, 1, 1, 4>(a, s);
+      // 64 x 64 tiles where they are many (us with the quantisation, 64 x 64
+      // against 32 x 32: 8192 x 128 x 2048 31 against 35; 300 x 256 x 8192 11.5
+      // against 10.7)
+      return a.n * a.units > 3000000 ? launch_direct<X_MX4, 4, 4, 4>(a, s) : launch_direct<X_MX4, 2, 2, 4>(a, s);
   }
 }
 

@@ -73,19 +73,31 @@ hipError_t launch_dequantize_mx4(const uint8_t* q, const uint8_t* scale, int64_t
 
 // How a product of n tokens, cols columns and `units` units runs.
 enum Mx4Plan {
-  MX4_FUSED,   // few tokens: straight from memory, x quantised in registers
+  MX4_FUSED,   // few tokens: straight from memory, x quantised in LDS
   MX4_DIRECT,  // straight from memory
   MX4_MID,     // 128 x 128 tiles through LDS
   MX4_BIG      // 256 x 256 tiles through LDS
 };
 constexpr int kMx4MidTile = 128, kMx4BigTile = 256;
-constexpr int kMx4FusedTokens = 16;   // up to here the product quantises x itself
-constexpr int kMx4DirectTokens = 64;  // up to here the weights are read once however few their tiles
+// Blocks of x (columns rounded up to 256) up to which each workgroup quantises
+// x itself: one launch in place of two (us at 2, 4, 8 x 4096 x 11008: 6.7, 8.4,
+// 10.6 against 10.4, 10.9, 11.6; 16 x 2048 x 5632: 5.7 against 7.3).
+constexpr int kMx4FusedBlocks = 1024;
+inline bool mx4_fused(int64_t n, int cols) { return n <= 16 && n * ((cols + 255) / 256) * 8 <= kMx4FusedBlocks; }
+// Multiplications from which tiles through LDS are faster than straight from
+// memory (us with the quantisation, tiles against straight: 64 x 2048 x 5632,
+// 0.74e9, 10.7 against 10.2; 1000 x 2048 x 256, 0.52e9, 11.2 against 9.3; 4000 x
+// 300 x 512, 0.61e9, 10.6 against 11.9; 32 x 4096 x 11008, 1.4e9, 15.2 against
+// 16.4; 64 x 4096 x 11008, 2.9e9, 15.8 against 22.5).
+constexpr int64_t kMx4TiledWork = 600000000;
 inline Mx4Plan mx4_plan(int64_t n, int cols, int units, bool x_is_mx4) {
-  if (n <= kMx4FusedTokens && !x_is_mx4) return MX4_FUSED;
-  if (n <= kMx4DirectTokens || units < kMx4MidTile || cols <= 256) return MX4_DIRECT;
+  if (!x_is_mx4 && mx4_fused(n, cols)) return MX4_FUSED;
+  if (n <= 16 || units < kMx4MidTile || cols <= 256 || n * cols < kMx4TiledWork / units) return MX4_DIRECT;
   if (n < kMx4BigTile || units < kMx4BigTile) return MX4_MID;
-  // 256 x 256 tiles once there are more of them than compute units
+  // 256 x 256 tiles once there are more of them than compute units (us without
+  // the quantisation, 256 against 128: 1003 x 1990 x 8100, 128 tiles, 25.6
+  // against 20.4; 2048 x 4096 x 11008, 344 tiles, 58.5 against 60.3; 4096 x 4096
+  // x 11008, 688 tiles, 92 against 107)
   const int64_t tiles = ((n + 255) / 256) * ((units + 255) / 256);
   return tiles > 256 ? MX4_BIG : MX4_MID;
 }

@@ -397,6 +397,14 @@ def _addr(t: Optional[torch.Tensor], what: str, shape, dtype=None):
     return t.data_ptr() or None
 
 
+def _queue(stream, t: torch.Tensor) -> int:
+    """Handle of `stream`, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    # current_stream() makes a Stream object and takes 3 us; this is its handle alone
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
 class NormOut(NamedTuple):
     """What add_rms_norm puts out; fields that were not asked for are None."""
     residual: Optional[torch.Tensor]  # [rows, cols] r', dtype of the residual
@@ -445,7 +453,7 @@ def add_rms_norm(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None
         _addr(out.residual, "out.residual", shape, residual.dtype), F32 if out.out is None else _code(out.out, "out.out"),
         _addr(out.out, "out.out", shape), _addr(out.codes, "out.codes", shape, torch.uint8),
         _addr(out.scale, "out.scale", row, torch.float32), _addr(out.rstd, "out.rstd", row, torch.float32),
-        _stream(stream)), "twell_add_rms_norm")
+        _queue(stream, residual)), "twell_add_rms_norm")
     return out
 
 
@@ -478,8 +486,8 @@ def add_rms_norm_bwd(d_out, residual, rstd, weight, d_residual=None, out=None, w
             _addr(dw, "dw", shape[1:], torch.float32))
     if ws is None:
         ws = torch.empty(add_rms_norm_bwd_ws(rows, cols), dtype=torch.uint8, device=residual.device)
-    _check(lib().twell_add_rms_norm_bwd(*args, ws.data_ptr() or None, ws.numel() * ws.element_size(), _stream(stream)),
-           "twell_add_rms_norm_bwd")
+    _check(lib().twell_add_rms_norm_bwd(*args, ws.data_ptr() or None, ws.numel() * ws.element_size(),
+                                        _queue(stream, residual)), "twell_add_rms_norm_bwd")
     return dr, dw
 
 
@@ -506,7 +514,7 @@ def quantize_mx4(a, out=None, stream=None):
     q, s = alloc_mx4(rows, cols, a.device) if out is None else out
     qs, ss = mx4_shapes(rows, cols)
     _check(lib().twell_quantize_mx4(rows, cols, dt, src, _addr(q, "codes", qs, torch.uint8),
-                                    _addr(s, "scales", ss, torch.uint8), _stream(stream)), "twell_quantize_mx4")
+                                    _addr(s, "scales", ss, torch.uint8), _queue(stream, a)), "twell_quantize_mx4")
     return q, s
 
 
@@ -518,7 +526,7 @@ def dequantize_mx4(codes, scales, cols: int, dtype=torch.bfloat16, out=None, str
     if out is None:
         out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
     _check(lib().twell_dequantize_mx4(rows, cols, q, s, _code(out, "out"), _addr(out, "out", (rows, cols)),
-                                      _stream(stream)), "twell_dequantize_mx4")
+                                      _queue(stream, codes)), "twell_dequantize_mx4")
     return out
 
 
@@ -543,7 +551,7 @@ def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bflo
     if ws is None:
         ws = torch.empty(matmul_mx4_ws(n, cols, units), dtype=torch.uint8, device=x_codes.device)
     _check(lib().twell_matmul_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units)),
-                                  ws.data_ptr() or None, ws.numel() * ws.element_size(), _stream(stream)),
+                                  ws.data_ptr() or None, ws.numel() * ws.element_size(), _queue(stream, x_codes)),
            "twell_matmul_mx4")
     return out
 
@@ -572,7 +580,7 @@ def linear_mx4(x, w_codes, w_scales, dtype=torch.bfloat16, out=None, ws=None, st
     if ws is None:
         ws = torch.empty(linear_mx4_ws(n, cols, units), dtype=torch.uint8, device=x.device)
     _check(lib().twell_linear_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units)),
-                                  ws.data_ptr() or None, ws.numel() * ws.element_size(), _stream(stream)),
+                                  ws.data_ptr() or None, ws.numel() * ws.element_size(), _queue(stream, x)),
            "twell_linear_mx4")
     return out
 

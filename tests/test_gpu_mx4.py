@@ -138,7 +138,8 @@ def test_products(n, cols, units):
 
 
 @pytest.mark.parametrize("n,cols,units", [(4352, 640, 4352), (4099, 1990, 4611), (8192, 130, 2053), (8195, 384, 2304),
-                                          (2304, 4096, 8192), (700, 2048, 5632), (1001, 1152, 1003), (90, 4096, 2056)])
+                                          (2304, 4096, 8192), (700, 2048, 5632), (1001, 1152, 1003), (90, 4096, 2056),
+                                          (70, 4997, 2055), (127, 4100, 1500), (40003, 384, 130)])
 def test_large_products_are_exact(n, cols, units):
     """Small whole numbers: every sum is exact in fp32, whatever its order, so y is too. Covers whole grids of the
     tiled product with edges on both sides, against float64 on the GPU's own fp32-exact product."""
@@ -157,6 +158,28 @@ def test_large_products_are_exact(n, cols, units):
         got = tw.linear_mx4(x.to(xdt), wq, ws, dtype=F32)
         assert torch.equal(got, want)
         assert torch.equal(tw.linear_mx4(x.to(xdt), wq, ws), want.to(BF))
+
+
+@pytest.mark.parametrize("n,cols,units", [(100, 4096, 2048), (77, 3333, 4111), (300, 2050, 1024), (600, 1990, 1001),
+                                          (130, 1100, 6000), (4400, 1000, 4352), (4107, 2999, 4333)])
+def test_large_products(n, cols, units):
+    """The tiles on ordinary values, against float64 of the values that the operands stand for."""
+    require_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.randn(n, cols, generator=gen, device="cuda") * torch.exp(torch.randn(n, 1, generator=gen, device="cuda"))
+    w = torch.randn(units, cols, generator=gen, device="cuda") / cols ** 0.5
+    xq, xs = tw.quantize_mx4(x)
+    wq, ws = tw.quantize_mx4(w)
+    xv, wv = (tw.dequantize_mx4(*v, cols, dtype=F32).double() for v in ((xq, xs), (wq, ws)))
+    want = torch.matmul(xv, wv.t())
+    size = torch.matmul(xv.abs(), wv.abs().t())
+    tol = size * ((cols / 8 + cols / 64 + 12) * U)
+    y = tw.linear_mx4(x, wq, ws, dtype=F32)
+    assert bool(((y.double() - want).abs() <= tol).all())
+    assert torch.equal(tw.matmul_mx4(xq, xs, wq, ws, cols, dtype=F32), y)
+    b = tw.linear_mx4(x, wq, ws)
+    assert torch.equal(b, y.to(BF))
+    assert torch.equal(tw.linear_mx4(x, wq, ws), b)
 
 
 @pytest.mark.parametrize("n,units", [(4, 40), (20, 40), (70, 70), (70, 300), (300, 200), (4500, 4500)])

@@ -109,12 +109,14 @@ def test_mx4_product_workspaces():
     """Nothing for few tokens, x's MX4 rows for some more, and for tiles both operands' scales by 256 columns (8 bytes
     a row, 128 rows at least) in place of x's scale rows."""
     assert tw.linear_mx4_ws(1, 4096, 11008) == 0 and tw.linear_mx4_ws(0, 4096, 11008) == 0
-    assert tw.linear_mx4_ws(40, 1990, 8100) == 40 * (1024 + 64) and tw.matmul_mx4_ws(40, 1990, 8100) == 0
+    assert tw.linear_mx4_ws(30, 1990, 8100) == 30 * (1024 + 64) and tw.matmul_mx4_ws(30, 1990, 8100) == 0
     assert tw.linear_mx4_ws(1000, 1990, 100) == 1000 * (1024 + 64)  # fewer units than a tile
     assert tw.linear_mx4_ws(1000, 200, 8100) == 1000 * (128 + 16)   # one stage of columns
     arranged = 8 * 8 * (8100 + 1000)
     assert tw.linear_mx4_ws(1000, 1990, 8100) == 1000 * 1024 + arranged and tw.matmul_mx4_ws(1000, 1990, 8100) == arranged
-    assert tw.matmul_mx4_ws(70, 300, 128) == 2 * 8 * (128 + 128)
+    # fewer tokens than a tile: x's scales are given a tile's rows
+    assert tw.matmul_mx4_ws(100, 4096, 11008) == 16 * 8 * (11008 + 128)
+    assert tw.matmul_mx4_ws(100, 1000, 1000) == 0  # too little work for tiles
     for f in (tw.lib().twell_linear_mx4_ws, tw.lib().twell_matmul_mx4_ws):
         assert f(1, 64, 8, None) == 1
         n = ctypes.c_size_t()
@@ -133,9 +135,10 @@ def test_mx4_refusals():
     for kw in (dict(n=-1), dict(k=0), dict(u=0), dict(a=None), dict(b=ODD), dict(c=None), dict(e=None), dict(dt=3), dict(y=None)):
         assert m(**kw) == 1, kw
     assert m(u=(1 << 24) + 1) == 2 and m(n=(1 << 31) - 1, u=1 << 20) == 2
-    need = 2 * 8 * (128 + 128)
-    assert m(n=70, k=300, u=128) == 3 and m(n=70, k=300, u=128, ws=FAKE, b2=need - 1) == 3
-    assert m(n=70, k=300, u=128, ws=ODD, b2=need) == 3 and b"workspace" in L.twell_last_error()
+    need = 16 * 8 * (11008 + 128)
+    tiles = dict(n=100, k=4096, u=11008)
+    assert m(**tiles) == 3 and m(**tiles, ws=FAKE, b2=need - 1) == 3
+    assert m(**tiles, ws=ODD, b2=need) == 3 and b"workspace" in L.twell_last_error()
     f = lambda n=64, k=64, u=8, xd=0, x=FAKE, c=FAKE, e=FAKE, dt=0, y=FAKE, ws=FAKE, b=64 * 80: L.twell_linear_mx4(  # noqa: E731
         n, k, u, xd, x, c, e, dt, y, ws, b, None)
     for kw in (dict(xd=9), dict(x=None), dict(x=ODD), dict(c=None), dict(y=ODD)):
