@@ -2,11 +2,7 @@
 //
 // A row is dealt to its threads in chunks of 8 elements (16 bytes of bf16, 32
 // of fp32): thread t of T takes chunks t, t + T, ...; elements behind the row's
-// end read as zeros and are not written. TAIL is set when the row
-// length is not a multiple of 8: rows then start at any element, so chunks are
-// read and written with element-aligned vector accesses (global memory takes
-// them at any alignment on gfx950), and the row's last, partial chunk one
-// element at a time. Without TAIL every chunk is 16-byte aligned.
+// end read as zeros and are not written.
 #pragma once
 
 #include "../csrc/twell_device.h"
@@ -24,14 +20,51 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 
+// How a row's chunks lie:
+//   ROWS_ALIGNED  rows are whole chunks, every chunk 16-byte aligned;
+//   ROWS_ANY      rows of 8 elements or more that start at any element: accesses
+//                 are element-aligned vectors (global memory takes them at any
+//                 alignment on gfx950), and a partial last chunk is moved back
+//                 to the row's last 8 elements, the first `dup` of which belong
+//                 to the chunk before, too: both compute and write the same, and
+//                 a sum over the row leaves them out. Nothing is written before
+//                 all of a row is read, so that an output may be its input;
+//   ROWS_SHORT    rows of fewer than 8 elements, one at a time.
+enum RowKind { ROWS_ALIGNED, ROWS_ANY, ROWS_SHORT };
+
+template <int KIND>
+__device__ __forceinline__ int chunk_col(int i, int cols) {
+  return KIND == ROWS_ANY ? min(8 * i, cols - 8) : 8 * i;
+}
+// Whether element k of chunk i counts in a sum.
+template <int KIND>
+__device__ __forceinline__ bool chunk_counts(int i, int k, int cols) {
+  return KIND != ROWS_ANY || chunk_col<KIND>(i, cols) + k >= 8 * i;
+}
+
 template <typename T>
 struct Raw8;
 
 template <>
 struct Raw8<uint16_t> {
   u32x4_t v;
-  template <bool TAIL>
+  template <int KIND>
   __device__ __forceinline__ void load(const uint16_t* row, int i, int cols) {
+    if constexpr (KIND == ROWS_SHORT) {
+      load_filled<true>(row, i, cols);
+    } else {
+      v = u32x4_t{0u, 0u, 0u, 0u};
+      const uint16_t* p = row + chunk_col<KIND>(i, cols);
+      if (8 * i < cols) {
+        if constexpr (KIND == ROWS_ALIGNED) v = *reinterpret_cast<const u32x4_t*>(p);
+        else v = *reinterpret_cast<const u32x4_a2_t*>(p);
+      }
+    }
+  }
+  // Chunk i as it is: a partial last one is filled with zeros (TAIL: there may
+  // be one, and rows start at any element).
+  template <bool TAIL>
+  __device__ __forceinline__ void load_filled(const uint16_t* row, int i, int cols) {
     v = u32x4_t{0u, 0u, 0u, 0u};
     const uint16_t* p = row + 8 * i;
     if constexpr (!TAIL) {
@@ -57,8 +90,26 @@ struct Raw8<uint16_t> {
 template <>
 struct Raw8<float> {
   u32x4_t v[2];
-  template <bool TAIL>
+  template <int KIND>
   __device__ __forceinline__ void load(const float* row, int i, int cols) {
+    if constexpr (KIND == ROWS_SHORT) {
+      load_filled<true>(row, i, cols);
+    } else {
+      v[0] = v[1] = u32x4_t{0u, 0u, 0u, 0u};
+      const float* p = row + chunk_col<KIND>(i, cols);
+      if (8 * i < cols) {
+        if constexpr (KIND == ROWS_ALIGNED) {
+          v[0] = *reinterpret_cast<const u32x4_t*>(p);
+          v[1] = *reinterpret_cast<const u32x4_t*>(p + 4);
+        } else {
+          v[0] = *reinterpret_cast<const u32x4_a4_t*>(p);
+          v[1] = *reinterpret_cast<const u32x4_a4_t*>(p + 4);
+        }
+      }
+    }
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void load_filled(const float* row, int i, int cols) {
     v[0] = v[1] = u32x4_t{0u, 0u, 0u, 0u};
     const float* p = row + 8 * i;
     if constexpr (!TAIL) {
@@ -85,45 +136,70 @@ struct Raw8<float> {
 };
 
 // Writes chunk i of a row; for bf16 the values are rounded.
-template <bool TAIL>
+template <int KIND>
 __device__ __forceinline__ void store8(uint16_t* row, int i, int cols, const float (&x)[8]) {
   const u32x4_t v = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
-  uint16_t* p = row + 8 * i;
-  if constexpr (!TAIL) {
-    if (8 * i < cols) *reinterpret_cast<u32x4_t*>(p) = v;
-  } else if (8 * i + 8 <= cols) {
-    *reinterpret_cast<u32x4_a2_t*>(p) = v;
-  } else {
+  uint16_t* p = row + chunk_col<KIND>(i, cols);
+  if constexpr (KIND == ROWS_SHORT) {
 #pragma unroll
     for (int k = 0; k < 7; ++k)
       if (8 * i + k < cols) p[k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+  } else if (8 * i < cols) {
+    if constexpr (KIND == ROWS_ALIGNED) *reinterpret_cast<u32x4_t*>(p) = v;
+    else *reinterpret_cast<u32x4_a2_t*>(p) = v;
   }
 }
-template <bool TAIL>
+template <int KIND>
 __device__ __forceinline__ void store8(float* row, int i, int cols, const float (&x)[8]) {
-  float* p = row + 8 * i;
-  if constexpr (!TAIL) {
-    if (8 * i < cols) {
-      *reinterpret_cast<f32x4_t*>(p) = f32x4_t{x[0], x[1], x[2], x[3]};
-      *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{x[4], x[5], x[6], x[7]};
-    }
-  } else if (8 * i + 8 <= cols) {
-    *reinterpret_cast<u32x4_a4_t*>(p) = __builtin_bit_cast(u32x4_t, f32x4_t{x[0], x[1], x[2], x[3]});
-    *reinterpret_cast<u32x4_a4_t*>(p + 4) = __builtin_bit_cast(u32x4_t, f32x4_t{x[4], x[5], x[6], x[7]});
-  } else {
+  float* p = row + chunk_col<KIND>(i, cols);
+  const u32x4_t lo = __builtin_bit_cast(u32x4_t, f32x4_t{x[0], x[1], x[2], x[3]});
+  const u32x4_t hi = __builtin_bit_cast(u32x4_t, f32x4_t{x[4], x[5], x[6], x[7]});
+  if constexpr (KIND == ROWS_SHORT) {
 #pragma unroll
     for (int k = 0; k < 7; ++k)
       if (8 * i + k < cols) p[k] = x[k];
+  } else if (8 * i < cols) {
+    if constexpr (KIND == ROWS_ALIGNED) {
+      *reinterpret_cast<u32x4_t*>(p) = lo;
+      *reinterpret_cast<u32x4_t*>(p + 4) = hi;
+    } else {
+      *reinterpret_cast<u32x4_a4_t*>(p) = lo;
+      *reinterpret_cast<u32x4_a4_t*>(p + 4) = hi;
+    }
+  }
+}
+// Chunk i as it is, of a partial last one the elements there are.
+template <bool TAIL, typename T>
+__device__ __forceinline__ void store8_exact(T* row, int i, int cols, const float (&x)[8]) {
+  if constexpr (!TAIL) {
+    store8<ROWS_ALIGNED>(row, i, cols, x);
+  } else if (8 * i + 8 <= cols) {
+    store8<ROWS_ANY>(row, i, cols, x);
+  } else {
+    store8<ROWS_SHORT>(row, i, cols, x);
+  }
+}
+// Eight bytes a chunk.
+template <int KIND>
+__device__ __forceinline__ void store8(uint8_t* row, int i, int cols, const u32x2_t& v) {
+  uint8_t* p = row + chunk_col<KIND>(i, cols);
+  if constexpr (KIND == ROWS_SHORT) {
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+      if (8 * i + k < cols) p[k] = (uint8_t)(v[k >> 2] >> (8 * (k & 3)));
+  } else if (8 * i < cols) {
+    if constexpr (KIND == ROWS_ALIGNED) *reinterpret_cast<u32x2_t*>(p) = v;
+    else *reinterpret_cast<u32x2_a1_t*>(p) = v;
   }
 }
 
 // Weight chunks of this thread as floats (bf16 or fp32 storage, uniform).
-template <int T, int C, bool TAIL>
+template <int T, int C, int KIND>
 __device__ __forceinline__ void load_weight(const void* w, int is_bf16, int t, int cols, float (&wv)[C][8]) {
   if (is_bf16) {
     Raw8<uint16_t> raw[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) raw[c].template load<TAIL>(static_cast<const uint16_t*>(w), t + T * c, cols);
+    for (int c = 0; c < C; ++c) raw[c].template load<KIND>(static_cast<const uint16_t*>(w), t + T * c, cols);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -131,7 +207,7 @@ __device__ __forceinline__ void load_weight(const void* w, int is_bf16, int t, i
   } else {
     Raw8<float> raw[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) raw[c].template load<TAIL>(static_cast<const float*>(w), t + T * c, cols);
+    for (int c = 0; c < C; ++c) raw[c].template load<KIND>(static_cast<const float*>(w), t + T * c, cols);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -139,16 +215,41 @@ __device__ __forceinline__ void load_weight(const void* w, int is_bf16, int t, i
   }
 }
 
-// Largest of a 32-bit pattern over the wave, in every lane: quad and row
-// steps by DPP, then across the four rows of 16 lanes.
-__device__ __forceinline__ uint32_t wave_max_bits(uint32_t m) {
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, false));
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xF, 0xF, false));
-  const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)m, 0), b = (uint32_t)__builtin_amdgcn_readlane((int)m, 16);
-  const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)m, 32), d = (uint32_t)__builtin_amdgcn_readlane((int)m, 48);
-  return max(max(a, b), max(c, d));
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t m) {
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, CTRL, 0xF, 0xF, false));
+}
+
+// Sum, and largest 32-bit pattern, over each group of G lanes of a wave, in
+// every lane of it: quad and row steps by DPP give the 16 lanes of a row theirs.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+  if constexpr (G == 64) return wave_sum_dpp(v);
+  v = dpp_add<0xB1, 0xF>(v);   // lanes 1 0 3 2
+  v = dpp_add<0x4E, 0xF>(v);   // lanes 2 3 0 1
+  v = dpp_add<0x141, 0xF>(v);  // mirror of 8
+  v = dpp_add<0x140, 0xF>(v);  // mirror of 16
+  if constexpr (G == 32) v += __shfl_xor(v, 16, 64);
+  return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t m) {
+  m = dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4E>(dpp_max<0xB1>(m))));
+  if constexpr (G == 32) m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+  if constexpr (G == 64) {
+    const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)m, 0), b = (uint32_t)__builtin_amdgcn_readlane((int)m, 16);
+    const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)m, 32), d = (uint32_t)__builtin_amdgcn_readlane((int)m, 48);
+    m = max(max(a, b), max(c, d));
+  }
+  return m;
+}
+
+// Calls f(KIND) with the kind of rows of `cols` elements.
+template <typename F>
+auto row_kind(int cols, F f) {
+  if (cols % 8 == 0) return f(std::integral_constant<int, ROWS_ALIGNED>{});
+  if (cols >= 8) return f(std::integral_constant<int, ROWS_ANY>{});
+  return f(std::integral_constant<int, ROWS_SHORT>{});
 }
 
 }  // namespace twell

@@ -92,7 +92,7 @@ __device__ __forceinline__ u32x4_t quantize_block(const TX* row, int b, int cols
   Raw8<TX> raw[4];
   uint32_t m = 0;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) raw[c].template load<TAIL>(row, 4 * b + c, cols);
+  for (int c = 0; c < 4; ++c) raw[c].template load_filled<TAIL>(row, 4 * b + c, cols);
 #pragma unroll
   for (int c = 0; c < 4; ++c) m = max(m, raw[c].max_bits());
   code = mx4_scale_code(m);
@@ -249,7 +249,7 @@ struct TileCfg {
   static constexpr int MIN_STORES = 2 * FU * FT;            // of a wave at a tile's end: 16-byte stores of bf16
   static_assert(LOADS / 2 + MIN_STORES <= 63, "vmcnt");
   static_assert(NW == 4, "the key of the LDS rows");
-  static_assert(BU % 128 == 0 && BT % 128 == 0 && (SROWS % NW == 0 || NW % SROWS == 0), "loads split evenly over the waves");
+  static_assert(BU % 128 == 0 && BT % 128 == 0 && (SROWS % NW == 0 || SROWS < NW), "loads split evenly over the waves");
   static_assert(OCC * LDS <= 160 * 1024, "LDS of a compute unit");
 };
 

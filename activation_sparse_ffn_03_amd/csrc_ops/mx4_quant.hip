@@ -82,7 +82,7 @@ __global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(const TS* __rest
   Raw8<TS> raw[kUnits];
 #pragma unroll
   for (int k = 0; k < kUnits; ++k)
-    raw[k].template load<TAIL>(in + u.row[k] * cols, 64 * u.seg[k] + lane, u.valid(k) ? cols : 0);
+    raw[k].template load_filled<TAIL>(in + u.row[k] * cols, 64 * u.seg[k] + lane, u.valid(k) ? cols : 0);
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
     if (!u.valid(k)) return;
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint8_t*
     const float s = __uint_as_float(sc[k] == 0u ? 0x00400000u : sc[k] == 255u ? 0x7FC00000u : sc[k] << 23);
     float x[8];
     mx4_values(w[k], s, x);
-    store8<TAIL>(out + u.row[k] * cols, 64 * u.seg[k] + lane, cols, x);
+    store8_exact<TAIL>(out + u.row[k] * cols, 64 * u.seg[k] + lane, cols, x);
   }
 }
 

@@ -23,8 +23,6 @@
 namespace twell {
 namespace {
 
-constexpr int kThreads = 256;
-
 // Codes of 8 quotients n / sc. With FAST the row's largest magnitude is finite
 // and its scale normal, so that every quotient is at most 448.001 and the
 // hardware conversion (nearest, ties to even) is right as it stands. Otherwise
@@ -55,17 +53,22 @@ __device__ __forceinline__ u32x2_t encode8(const float (&n)[8], float sc) {
 // 448 * 2^-126: from here the scale is a normal number.
 constexpr uint32_t kNormalScaleBits = 0x04E00000u;
 
-// TR: the stream's type; TD: the addition's (void: none). WPR waves a row, C
-// chunks of 8 elements a thread. WPR = 1: four rows a workgroup, no barrier.
-template <typename TR, typename TD, int WPR, int C, bool TAIL>
-__global__ __launch_bounds__(kThreads) void add_rms_norm_kernel(NormArgs a) {
-  constexpr int T = 64 * WPR;
+// TR: the stream's type; TD: the addition's (void: none). A row is taken by T
+// threads, C chunks of 8 elements each: up to 64 threads several rows share a
+// workgroup of four waves and need no barrier, above that a row has one of its
+// own.
+template <int T>
+constexpr int norm_threads() { return T > 64 ? T : 256; }
+template <typename TR, typename TD, int T, int C, int KIND>
+__global__ __launch_bounds__(norm_threads<T>()) void add_rms_norm_kernel(NormArgs a) {
   constexpr bool ADD = !std::is_void_v<TD>;
   using TDs = std::conditional_t<ADD, TD, TR>;
+  constexpr int G = T < 64 ? T : 64;  // lanes of a wave that share a row
+  constexpr int WPR = T / G;          // waves of a row
   const int wave = threadIdx.x >> 6;
-  const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
-  if (row >= a.rows) return;  // whole waves, and with WPR > 1 whole workgroups
-  const int t = WPR == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+  const int64_t row = WPR > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T;
+  if (row >= a.rows) return;  // whole groups of lanes, and with WPR > 1 whole workgroups
+  const int t = threadIdx.x % T;
   const int cols = a.cols;
   const int64_t off = row * cols;
 
@@ -73,11 +76,11 @@ __global__ __launch_bounds__(kThreads) void add_rms_norm_kernel(NormArgs a) {
   Raw8<TDs> rd[ADD ? C : 1];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    rr[c].template load<TAIL>(static_cast<const TR*>(a.residual) + off, t + T * c, cols);
-    if constexpr (ADD) rd[c].template load<TAIL>(static_cast<const TD*>(a.delta) + off, t + T * c, cols);
+    rr[c].template load<KIND>(static_cast<const TR*>(a.residual) + off, t + T * c, cols);
+    if constexpr (ADD) rd[c].template load<KIND>(static_cast<const TD*>(a.delta) + off, t + T * c, cols);
   }
   float w[C][8];
-  load_weight<T, C, TAIL>(a.w, a.w_bf16, t, cols, w);
+  load_weight<T, C, KIND>(a.w, a.w_bf16, t, cols, w);
 
   float x[C][8];
   float ss = 0.f;
@@ -96,20 +99,23 @@ __global__ __launch_bounds__(kThreads) void add_rms_norm_kernel(NormArgs a) {
         x[c][k + 1] = bf16hi_to_f32(p);
       }
     }
-    if (a.residual_out != nullptr)
-      store8<TAIL>(static_cast<TR*>(a.residual_out) + off, t + T * c, cols, x[c]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fmaf(x[c][k], x[c][k], ss);
+    for (int k = 0; k < 8; ++k)
+      if (chunk_counts<KIND>(t + T * c, k, cols)) ss = fmaf(x[c][k], x[c][k], ss);
   }
   __shared__ float red_sum[WPR];
   __shared__ uint32_t red_max[WPR];
-  ss = wave_sum_dpp(ss);
+  ss = group_sum<G>(ss);
   if constexpr (WPR > 1) {
     if ((threadIdx.x & 63) == 0) red_sum[wave] = ss;
     lds_barrier();
     ss = 0.f;
 #pragma unroll
     for (int i = 0; i < WPR; ++i) ss += red_sum[i];
+  }
+  if (a.residual_out != nullptr) {  // behind the sum: every thread has read its part of the row
+#pragma unroll
+    for (int c = 0; c < C; ++c) store8<KIND>(static_cast<TR*>(a.residual_out) + off, t + T * c, cols, x[c]);
   }
   const float rho = 1.0f / sqrtf(ss / (float)cols + a.eps);
   if (a.rstd != nullptr && t == 0) a.rstd[row] = rho;
@@ -125,17 +131,17 @@ __global__ __launch_bounds__(kThreads) void add_rms_norm_kernel(NormArgs a) {
   if (a.out != nullptr) {
     if (a.out_bf16) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) store8<TAIL>(static_cast<uint16_t*>(a.out) + off, t + T * c, cols, x[c]);
+      for (int c = 0; c < C; ++c) store8<KIND>(static_cast<uint16_t*>(a.out) + off, t + T * c, cols, x[c]);
     } else {
 #pragma unroll
-      for (int c = 0; c < C; ++c) store8<TAIL>(static_cast<float*>(a.out) + off, t + T * c, cols, x[c]);
+      for (int c = 0; c < C; ++c) store8<KIND>(static_cast<float*>(a.out) + off, t + T * c, cols, x[c]);
     }
   }
   if (a.q == nullptr) return;
 
   // Elements past the row's end hold 0 * rho * 0: 0, or NaN in a row whose rho
   // is not finite, which cannot be (eps > 0) unless the row itself holds NaN.
-  mb = wave_max_bits(mb);
+  mb = group_max<G>(mb);
   if constexpr (WPR > 1) {
     if ((threadIdx.x & 63) == 0) red_max[wave] = mb;
     lds_barrier();
@@ -145,22 +151,9 @@ __global__ __launch_bounds__(kThreads) void add_rms_norm_kernel(NormArgs a) {
   float sc = __uint_as_float(mb) / 448.0f;
   sc = sc > 0.f ? sc : 1.0f;  // NaN fails the test
   if (t == 0) a.q_scale[row] = sc;
-  uint8_t* qrow = a.q + off;
   auto encode = [&](auto fast) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int i = t + T * c;
-      const u32x2_t v = encode8<decltype(fast)::value>(x[c], sc);
-      if constexpr (!TAIL) {
-        if (8 * i < cols) *reinterpret_cast<u32x2_t*>(qrow + 8 * i) = v;
-      } else if (8 * i + 8 <= cols) {
-        *reinterpret_cast<u32x2_a1_t*>(qrow + 8 * i) = v;
-      } else {
-#pragma unroll
-        for (int k = 0; k < 7; ++k)
-          if (8 * i + k < cols) qrow[8 * i + k] = (uint8_t)(v[k >> 2] >> (8 * (k & 3)));
-      }
-    }
+    for (int c = 0; c < C; ++c) store8<KIND>(a.q + off, t + T * c, cols, encode8<decltype(fast)::value>(x[c], sc));
   };
   if (mb < 0x7F800000u && mb >= kNormalScaleBits)
     encode(std::true_type{});
@@ -168,31 +161,34 @@ __global__ __launch_bounds__(kThreads) void add_rms_norm_kernel(NormArgs a) {
     encode(std::false_type{});
 }
 
-template <typename TR, typename TD, int WPR, int C>
+template <typename TR, typename TD, int T, int C>
 hipError_t launch_cfg(const NormArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(WPR == 1 ? (a.rows + 3) / 4 : a.rows));
-  if (a.cols % 8 == 0)
-    TWELL_LAUNCH("add_rms_norm", (add_rms_norm_kernel<TR, TD, WPR, C, false>), grid, kThreads, 0, s, a);
-  else
-    TWELL_LAUNCH("add_rms_norm", (add_rms_norm_kernel<TR, TD, WPR, C, true>), grid, kThreads, 0, s, a);
-  return hipGetLastError();
+  const dim3 grid((unsigned)(T > 64 ? a.rows : (a.rows + 256 / T - 1) / (256 / T)));
+  return row_kind(a.cols, [&](auto kind) {
+    constexpr int KIND = decltype(kind)::value;
+    if constexpr (KIND != ROWS_SHORT || T == 16)
+      TWELL_LAUNCH("add_rms_norm", (add_rms_norm_kernel<TR, TD, T, C, KIND>), grid, norm_threads<T>(), 0, s, a);
+    return hipGetLastError();
+  });
 }
 
-// Rows below which a row gets a whole workgroup instead of one wave.
-constexpr int64_t kWaveRows = 1024;
-
+// As many threads as there are chunks, up to 512, then several chunks a thread
+// (us, other counts beside the chosen one: 16384 x 95 bf16 with codes 16
+// threads 5.4, 32 7.0, 64 10.3; 8192 x 768 128 threads 11.9, 64 12.2, 256 14.5;
+// 7248 x 1135 256 threads 10.3, 128 10.7, 512 13.7; 4096 x 2048 fp32 256
+// threads 25.5, 128 27.2, 64 28.3; 16384 x 4096 bf16 512 threads 103, 256 105,
+// 64 115; 1 x 4096 512 threads 2.9, 256 3.1, 128 3.8).
 template <typename TR, typename TD>
 hipError_t launch_typed(const NormArgs& a, hipStream_t s) {
-  if (a.cols <= 512) return launch_cfg<TR, TD, 1, 1>(a, s);
-  if (a.cols <= 4096 && a.rows >= kWaveRows) {
-    if (a.cols <= 1024) return launch_cfg<TR, TD, 1, 2>(a, s);
-    if (a.cols <= 2048) return launch_cfg<TR, TD, 1, 4>(a, s);
-    return launch_cfg<TR, TD, 1, 8>(a, s);
-  }
-  if (a.cols <= 2048) return launch_cfg<TR, TD, 4, 1>(a, s);
-  if (a.cols <= 4096) return launch_cfg<TR, TD, 4, 2>(a, s);
-  if (a.cols <= 8192) return launch_cfg<TR, TD, 4, 4>(a, s);
-  return launch_cfg<TR, TD, 4, 8>(a, s);
+  const int n = a.cols;
+  if (n <= 128) return launch_cfg<TR, TD, 16, 1>(a, s);
+  if (n <= 256) return launch_cfg<TR, TD, 32, 1>(a, s);
+  if (n <= 512) return launch_cfg<TR, TD, 64, 1>(a, s);
+  if (n <= 1024) return launch_cfg<TR, TD, 128, 1>(a, s);
+  if (n <= 2048) return launch_cfg<TR, TD, 256, 1>(a, s);
+  if (n <= 4096) return launch_cfg<TR, TD, 512, 1>(a, s);
+  if (n <= 8192) return launch_cfg<TR, TD, 512, 2>(a, s);
+  return launch_cfg<TR, TD, 512, 4>(a, s);
 }
 
 }  // namespace

@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename TR, typename TG, int WPR, int C, bool TAIL>
+template <typename TR, typename TG, int WPR, int C, int KIND>
 __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs a) {
   constexpr int T = 64 * WPR;
   constexpr int RPI = 4 / WPR;  // rows a workgroup takes at a time
@@ -29,7 +29,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs a) {
   const int64_t r0 = b * per + (b < rem ? b : rem), r1 = r0 + per + (b < rem ? 1 : 0);
 
   float w[C][8], dw[C][8];
-  load_weight<T, C, TAIL>(a.w, a.w_bf16, t, cols, w);
+  load_weight<T, C, KIND>(a.w, a.w_bf16, t, cols, w);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -43,13 +43,13 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs a) {
     Raw8<TG> rg[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      rr[c].template load<TAIL>(static_cast<const TR*>(a.residual) + off, t + T * c, cols);
-      rg[c].template load<TAIL>(static_cast<const TG*>(a.d_out) + off, t + T * c, cols);
+      rr[c].template load<KIND>(static_cast<const TR*>(a.residual) + off, t + T * c, cols);
+      rg[c].template load<KIND>(static_cast<const TG*>(a.d_out) + off, t + T * c, cols);
     }
     if (a.d_residual != nullptr) {
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        rs[c].template load<TAIL>(static_cast<const TR*>(a.d_residual) + off, t + T * c, cols);
+        rs[c].template load<KIND>(static_cast<const TR*>(a.d_residual) + off, t + T * c, cols);
     }
     const float rho = a.rstd[row];
     float dot = 0.f;
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float xh = rr[c].get(k) * rho, g = rg[c].get(k);
-        dot = fmaf(g * w[c][k], xh, dot);
+        if (chunk_counts<KIND>(t + T * c, k, cols)) dot = fmaf(g * w[c][k], xh, dot);
         dw[c][k] = fmaf(g, xh, dw[c][k]);
       }
     dot = wave_sum_dpp(dot);
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs a) {
         d[k] = rho * (rg[c].get(k) * w[c][k] - xh * cm);
         if (a.d_residual != nullptr) d[k] += rs[c].get(k);
       }
-      store8<TAIL>(static_cast<TR*>(a.dr) + off, t + T * c, cols, d);
+      store8<KIND>(static_cast<TR*>(a.dr) + off, t + T * c, cols, d);
     }
   }
 
@@ -103,7 +103,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs a) {
     if (wave < 3) return;  // the last wave holds the sums
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c) store8<TAIL>(part, t + T * c, cols, dw[c]);
+  for (int c = 0; c < C; ++c) store8<KIND>(part, t + T * c, cols, dw[c]);
 }
 
 // dw[col] = sum over the partial rows: a workgroup takes 64 columns, each of
@@ -129,10 +129,11 @@ __global__ __launch_bounds__(1024) void norm_dw_sum(const float* __restrict__ pa
 template <typename TR, typename TG, int WPR, int C>
 hipError_t launch_cfg(const NormBwdArgs& a, hipStream_t s) {
   const int groups = norm_bwd_groups(a.rows, a.cols);
-  if (a.cols % 8 == 0)
-    TWELL_LAUNCH("add_rms_norm_bwd", (norm_bwd_kernel<TR, TG, WPR, C, false>), dim3(groups), kThreads, 0, s, a);
-  else
-    TWELL_LAUNCH("add_rms_norm_bwd", (norm_bwd_kernel<TR, TG, WPR, C, true>), dim3(groups), kThreads, 0, s, a);
+  row_kind(a.cols, [&](auto kind) {
+    constexpr int KIND = decltype(kind)::value;
+    if constexpr (KIND != ROWS_SHORT || (WPR == 1 && C == 1))
+      TWELL_LAUNCH("add_rms_norm_bwd", (norm_bwd_kernel<TR, TG, WPR, C, KIND>), dim3(groups), kThreads, 0, s, a);
+  });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || groups == 1) return e;
   TWELL_LAUNCH("norm_dw_sum", norm_dw_sum, dim3((a.cols + 63) / 64), 1024, 0, s, a.part, groups, a.cols, a.dw);
