@@ -14,7 +14,7 @@
 //                       every WAVES-th 128 columns of the whole tile, straight
 //                       from memory into registers; the waves' sums are added
 //                       in LDS in a fixed order. With bf16 or fp32 x it also
-//                       quantises x in registers.
+//                       quantises x, into LDS.
 //   mx4_product_tiled   many tokens: tiles through a ring of LDS stages.
 #include "mx4_device.h"
 #include "ops_kernels.h"

@@ -40,14 +40,17 @@ struct NormBwdArgs {
   float* dw;               // [cols]
   float* part;             // [norm_bwd_groups][cols] (workspace; unused for one group)
 };
-// Row width up to which the backward gives a row to one wave (above: to a
-// workgroup of four).
-constexpr int kNormBwdWaveCols = 2048;
-// Workgroups of the norm's backward; each keeps one partial dw row. Two a
-// compute unit, and no more than there are rows for.
+// Rows that a workgroup of the norm's backward takes side by side.
+inline int norm_bwd_rows(int cols) {
+  return cols <= 128 ? 16 : cols <= 512 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1;
+}
+// Workgroups of the norm's backward; each keeps one partial dw row. One a
+// compute unit (two of the 256 threads that rows of up to 256 get), and no more
+// than there are rows for: more partial rows cost the second launch more than
+// they gain the first (4096x512 with two 9.2 us, with one 8.5).
 inline int norm_bwd_groups(int64_t rows, int cols) {
-  const int64_t need = cols <= kNormBwdWaveCols ? (rows + 3) / 4 : rows;
-  return (int)(need < 1 ? 1 : need > 512 ? 512 : need);
+  const int64_t need = (rows + norm_bwd_rows(cols) - 1) / norm_bwd_rows(cols), most = cols <= 256 ? 512 : 256;
+  return (int)(need < 1 ? 1 : need > most ? most : need);
 }
 hipError_t launch_add_rms_norm_bwd(const NormBwdArgs& a, hipStream_t s);
 

@@ -368,7 +368,8 @@ twell_status twell_add_rms_norm_bwd_ws(int64_t rows, int32_t cols, size_t* ws_by
  * fp32, summed in a fixed order. d_out [rows][cols] d_out_dtype; d_residual
  * [rows][cols] res_dtype, the gradient of residual_out, or NULL when nothing
  * else reads the stream. The codes have no gradient. Both outputs are fully
- * overwritten (rows == 0: dw = 0). ws: at least the queried bytes. */
+ * overwritten (rows == 0: dw = 0); neither may overlap an input. ws: at least the
+ * queried bytes. */
 twell_status twell_add_rms_norm_bwd(int64_t rows, int32_t cols, twell_dtype d_out_dtype, const void* d_out,
                                     twell_dtype res_dtype, const void* d_residual, const void* residual,
                                     const float* rstd, twell_dtype weight_dtype, const void* weight, void* dr,

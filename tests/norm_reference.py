@@ -39,7 +39,7 @@ def backward64(d_out, d_residual, r, rho, weight):
 
 def backward_tol(d_out, d_residual, r, rho, weight, groups):
     """|dr - dr64| and |dw - dw64|. The row's mean is off by ROW_ADDS + 3 roundings of its absolute terms; what it
-    meets in dr has at most 6 more. dw is a chain over one thread's rows, four waves, then groups / 16 and 16 sums."""
+    meets in dr has at most 6 more. dw is a chain over one thread's rows and the rows side by side, then groups / 16 and 16 sums."""
     x, g, w = r.double(), d_out.double(), weight.double()
     rho = rho.double().reshape(-1, 1)
     xh, u = x * rho, g * w

@@ -186,7 +186,7 @@ def test_backward(rows, cols):
         torch.cuda.synchronize()
         _check_guards(g1, g2)
         want_r, want_w = ref.backward64(g, s, r, rstd.cpu(), w)
-        groups = max(1, min(512, -(-rows // 4) if cols <= 2048 else rows))
+        groups = tw.add_rms_norm_bwd_ws(rows, cols) // (4 * cols) or 1
         tol_r, tol_w = ref.backward_tol(g, s, r, rstd.cpu(), w, groups)
         assert bool(((dr.cpu().double() - want_r).abs() <= tol_r).all())
         assert bool(((dw.cpu().double() - want_w).abs() <= tol_w).all())

@@ -44,8 +44,8 @@ def _bwd(rows=600, cols=64, gt=0, g=FAKE, rt=0, ds=None, r=FAKE, rstd=FAKE, wt=0
 
 def test_norm_backward_workspace():
     assert tw.add_rms_norm_bwd_ws(4, 64) == 0          # one workgroup writes dw itself
-    assert tw.add_rms_norm_bwd_ws(600, 64) == 150 * 64 * 4
-    assert tw.add_rms_norm_bwd_ws(600, 4096) == 512 * 4096 * 4
+    assert tw.add_rms_norm_bwd_ws(600, 64) == 38 * 64 * 4
+    assert tw.add_rms_norm_bwd_ws(600, 4096) == 256 * 4096 * 4
     with pytest.raises(tw.TwellError):
         tw.add_rms_norm_bwd_ws(4, 20000)
     assert tw.lib().twell_add_rms_norm_bwd_ws(4, 64, None) == 1
@@ -55,7 +55,7 @@ def test_norm_backward_workspace():
     (dict(rows=-1), 1, b"rows"), (dict(cols=16385), 2, b"16384"), (dict(gt=3), 1, b"dtypes"), (dict(g=None), 1, b"d_out"),
     (dict(ds=ODD), 1, b"d_residual"), (dict(r=None), 1, b"residual"), (dict(rstd=None), 1, b"rstd"),
     (dict(w=None), 1, b"weight"), (dict(dr=None), 1, b"dr"), (dict(dw=ODD), 1, b"dw"),
-    (dict(n=150 * 64 * 4 - 1), 3, b"workspace"), (dict(ws=None), 3, b"workspace"), (dict(ws=ODD), 3, b"workspace"),
+    (dict(n=38 * 64 * 4 - 1), 3, b"workspace"), (dict(ws=None), 3, b"workspace"), (dict(ws=ODD), 3, b"workspace"),
 ])
 def test_norm_backward_refusals(kw, code, word):
     assert _bwd(**kw) == code
