@@ -698,3 +698,95 @@ class TwellFFN:
         ffn_bwd(self.dims, self.dtype, self.hyb, x, dy, w_gate_t, w_up_t, w_down, l1_lambda, self.dx, self.dw_gate_t,
                 self.dw_up_t, self.dw_down, self.ws_bwd, stream=stream)
         return self.dx, self.dw_gate_t, self.dw_up_t, self.dw_down
+
+
+class TwellServe:
+    """The block with the norm in front of it, as a decoder serves it: buffers
+    for one problem (bf16), and per call
+      add_rms_norm -> gate -> pack -> up / down
+    on a residual stream that is updated in place.
+
+    gate: "bf16"  the bf16 gate weight [d_ff, d_model];
+          "fp8"   (codes, row scales) from quantize_e4m3: the norm writes the
+                  E4M3 codes of its rows itself, no launch quantises x;
+          "mx4"   (codes, scales) from quantize_mx4: linear_mx4 writes the
+                  pre-activation, pack_preact packs it.
+    Up and down projections read the normed rows in bf16 either way.
+    stream_dtype is the type of the residual stream. All buffers are allocated
+    once here, with torch, on `device`."""
+
+    def __init__(self, dims: Dims, gate: str = "bf16", eps: float = 1e-6, stream_dtype=torch.bfloat16, device="cuda"):
+        if gate not in ("bf16", "fp8", "mx4"):
+            raise ValueError("gate must be 'bf16', 'fp8' or 'mx4'")
+        if stream_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("the residual stream is bf16 or fp32")
+        self.dims, self.gate, self.eps, self.stream_dtype = dims, gate, float(eps), stream_dtype
+        self.sizes = query_sizes(dims, BF16)
+        self.pack = alloc_pack(dims, BF16, device)
+        N, D, F = dims.n_tokens, dims.d_model, dims.d_ff
+        self.x = torch.empty((N, D), dtype=torch.bfloat16, device=device)
+        self.x_q = torch.empty((N, D), dtype=torch.uint8, device=device) if gate == "fp8" else None
+        self.x_scale = torch.empty(N, dtype=torch.float32, device=device) if gate == "fp8" else None
+        self.y = torch.empty((N, D), dtype=torch.float32, device=device)
+        self.ws_fwd = alloc_workspace(self.sizes["ws_fwd"], device)
+        if gate == "mx4":
+            self.g = torch.empty((N, F), dtype=torch.float32, device=device)
+            self.ws_gate = torch.empty(linear_mx4_ws(N, D, F), dtype=torch.uint8, device=device)
+        else:
+            self.ws_gate = alloc_workspace(self.sizes["ws_gate"], device) if self.sizes["ws_gate"] else None
+
+    def forward(self, residual, delta, norm_weight, w_gate, w_up_t, w_down, t, stream=None):
+        """residual += delta in place (delta None: the stream stays as it is),
+        then the block on its norm. Returns y [n_tokens, d_model] fp32, the
+        delta of whatever comes next; the next call overwrites it, after it has
+        read it where it is that call's delta."""
+        d, N, D, F = self.dims, self.dims.n_tokens, self.dims.d_model, self.dims.d_ff
+        if residual.dtype != self.stream_dtype or tuple(residual.shape) != (N, D):
+            raise ValueError(f"residual must be {self.stream_dtype} [{N}, {D}]")
+        _addr(w_up_t, "w_up_t", (F, D), torch.bfloat16)
+        _addr(w_down, "w_down", (F, D), torch.bfloat16)
+        _addr(t, "t", (N,), torch.float32)
+        if self.gate == "bf16":
+            _addr(w_gate, "w_gate", (F, D), torch.bfloat16)
+        elif self.gate == "fp8":
+            _addr(w_gate[0], "w_gate codes", (F, D), torch.uint8)
+            _addr(w_gate[1], "w_gate scales", (F,), torch.float32)
+        else:
+            wq, wsc = mx4_shapes(F, D)
+            _addr(w_gate[0], "w_gate codes", wq, torch.uint8)
+            _addr(w_gate[1], "w_gate scales", wsc, torch.uint8)
+        add_rms_norm(residual, norm_weight, delta, self.eps, stream=stream,
+                     out=NormOut(None if delta is None else residual, self.x, self.x_q, self.x_scale, None))
+        if self.gate == "bf16":
+            ffn_forward(d, BF16, self.x, w_gate, t, self.pack, w_up_t, w_down, self.y, ws=self.ws_fwd,
+                        gate_ws=self.ws_gate, stream=stream)
+        elif self.gate == "fp8":
+            ffn_forward_fp8(d, self.x_q, self.x_scale, *w_gate, t, self.pack, self.x, w_up_t, w_down, self.y,
+                            ws=self.ws_fwd, gate_ws=self.ws_gate, stream=stream)
+        else:
+            linear_mx4(self.x, *w_gate, out=self.g, ws=self.ws_gate, stream=stream)
+            pack_preact(d, BF16, self.g, t, self.pack, stream=stream)
+            ffn_fwd(d, BF16, self.pack, self.x, w_up_t, w_down, self.y, ws=self.ws_fwd, stream=stream)
+        return self.y
+
+    def capture_supported(self) -> bool:
+        """False on the forwards whose graph capture is not cleared for
+        TwellFFN (see there), and on the MX4 gate at the same sizes, which
+        shares their overflow products."""
+        d = self.dims
+        heavy = self.gate != "fp8" and not self.sizes["ws_gate"] and d.d_model > 2048
+        return not (heavy and d.slots < d.tile_n and d.ovf_cap > 0)
+
+    def capture(self, residual, delta, norm_weight, w_gate, w_up_t, w_down, t) -> "torch.cuda.CUDAGraph":
+        """Record forward() on these tensors into a HIP graph, after one eager
+        call on a copy of the stream. A replay adds what delta holds then to
+        the stream and leaves the result in self.y."""
+        if not self.capture_supported():
+            raise TwellError(2, "TwellServe.capture", "graph capture of this forward (d_model > 2048 with possible "
+                             "overflow rows) is disabled; call forward() eagerly")
+        self.forward(residual.clone(), delta, norm_weight, w_gate, w_up_t, w_down, t)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            self.forward(residual, delta, norm_weight, w_gate, w_up_t, w_down, t)
+        return graph

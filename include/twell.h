@@ -175,9 +175,9 @@ twell_status twell_gate_pack_ws(const twell_dims* dims, twell_dtype dtype, const
                                 const void* w_gate_t, const float* t, const twell_pack* out,
                                 float* g_dump, void* ws, size_t ws_bytes, void* stream);
 
-/* Test entry: the same pack epilogue fed from a given pre-activation g [N][F]
- * fp32 instead of the GEMM. Produces exactly what twell_gate_pack would for
- * that g. */
+/* The same pack epilogue fed from a given pre-activation g [N][F] fp32 instead
+ * of the GEMM (for example that of twell_linear_mx4). Produces exactly what
+ * twell_gate_pack would for that g. */
 twell_status twell_pack_preact(const twell_dims* dims, twell_dtype dtype, const float* g,
                                const float* t, const twell_pack* out, void* stream);
 

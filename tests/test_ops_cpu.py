@@ -169,3 +169,18 @@ def test_mx4_binding_refuses_what_does_not_fit():
         tw.linear_mx4(x[0], *w)
     with pytest.raises(ValueError, match="shape"):
         tw.dequantize_mx4(*w, 200)
+
+
+def test_serve_refuses_settings():
+    dims = tw.make_dims(1, 64, 128, 64, 64)
+    with pytest.raises(ValueError, match="gate"):
+        tw.TwellServe(dims, "int4", device="cpu")
+    with pytest.raises(ValueError, match="stream"):
+        tw.TwellServe(dims, "mx4", stream_dtype=torch.float16, device="cpu")
+    s = tw.TwellServe(tw.make_dims(128, 4096, 256, 64, 8, 0, 16), "mx4", device="cpu")
+    assert not s.capture_supported()  # as the bf16 gate at this size
+    with pytest.raises(tw.TwellError, match="capture"):
+        s.capture(None, None, None, None, None, None, None)
+    with pytest.raises(ValueError, match="GPU"):
+        s.forward(torch.zeros(128, 4096, dtype=torch.bfloat16), None, None, None,
+                  *[torch.zeros(256, 4096, dtype=torch.bfloat16)] * 2, torch.zeros(128))
