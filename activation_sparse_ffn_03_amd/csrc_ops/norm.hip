@@ -193,13 +193,39 @@ hipError_t launch_typed(const NormArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_add_rms_norm(const NormArgs& a, hipStream_t s) {
+static hipError_t launch_rows(const NormArgs& a, hipStream_t s) {
   if (a.res_bf16) {
     if (a.delta == nullptr) return launch_typed<uint16_t, void>(a, s);
     return a.delta_bf16 ? launch_typed<uint16_t, uint16_t>(a, s) : launch_typed<uint16_t, float>(a, s);
   }
   if (a.delta == nullptr) return launch_typed<float, void>(a, s);
   return a.delta_bf16 ? launch_typed<float, uint16_t>(a, s) : launch_typed<float, float>(a, s);
+}
+
+// A launch holds less than 2^32 threads, up to 512 for a row: more rows than
+// that allows take several.
+hipError_t launch_add_rms_norm(const NormArgs& all, hipStream_t s) {
+  constexpr int64_t kLaunchRows = 1 << 22;
+  NormArgs a = all;
+  auto skip = [&](auto*& p, size_t bytes_a_row) {
+    using P = std::remove_reference_t<decltype(p)>;
+    if (p != nullptr)
+      p = reinterpret_cast<P>(reinterpret_cast<uintptr_t>(p) + kLaunchRows * bytes_a_row);
+  };
+  const size_t er = a.res_bf16 ? 2 : 4, ed = a.delta_bf16 ? 2 : 4, eo = a.out_bf16 ? 2 : 4, cols = (size_t)a.cols;
+  for (int64_t left = all.rows; left > 0; left -= kLaunchRows) {
+    a.rows = left < kLaunchRows ? left : kLaunchRows;
+    const hipError_t e = launch_rows(a, s);
+    if (e != hipSuccess) return e;
+    skip(a.residual, cols * er);
+    skip(a.delta, cols * ed);
+    skip(a.residual_out, cols * er);
+    skip(a.out, cols * eo);
+    skip(a.q, cols);
+    skip(a.q_scale, 4);
+    skip(a.rstd, 4);
+  }
+  return hipSuccess;
 }
 
 }  // namespace twell

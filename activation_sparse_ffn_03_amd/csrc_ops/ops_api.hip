@@ -1,7 +1,7 @@
 // C ABI of the operators around the block: host-side validation, then kernel
 // launches on the caller's stream. See include/twell.h for the contract of
 // every call.
-#include <string>
+#include <cstdio>
 
 #include "../csrc/twell_host.h"
 #include "../csrc/twell_internal.h"
@@ -13,7 +13,9 @@ twell_status fail(twell_status st, const char* why) { return twell::set_error(st
 
 twell_status hip_status(hipError_t e, const char* where) {
   if (e == hipSuccess) return TWELL_OK;
-  return twell::set_error(TWELL_ERR_HIP, (std::string(where) + ": " + hipGetErrorString(e)).c_str());
+  char why[256];  // no allocation, nothing to throw
+  std::snprintf(why, sizeof why, "%s: %s", where, hipGetErrorString(e));
+  return twell::set_error(TWELL_ERR_HIP, why);
 }
 
 twell_status ok() {
@@ -50,7 +52,8 @@ twell_status check_mx4_shape(int64_t rows, int32_t cols) {
   if (rows < 0 || cols <= 0) return fail(TWELL_ERR_INVALID_ARG, "rows must be >= 0 and cols > 0");
   if (rows > 0x7FFFFFFFll) return fail(TWELL_ERR_UNSUPPORTED, "rows above 2^31 - 1");
   if (cols > twell::kMx4MaxCols) return fail(TWELL_ERR_UNSUPPORTED, "cols above 2^20");
-  if (rows * ((cols + 511) / 512) > (1ll << 34)) return fail(TWELL_ERR_UNSUPPORTED, "rows x cols above 2^43");
+  // one launch: 16 threads a piece of 512 columns, less than 2^32 threads
+  if (rows * ((cols + 511) / 512) > (1ll << 27)) return fail(TWELL_ERR_UNSUPPORTED, "more than 2^27 pieces of 512 columns");
   return TWELL_OK;
 }
 
@@ -58,12 +61,14 @@ size_t mx4_codes(int64_t rows, int32_t cols) { return (size_t)rows * twell::mx4_
 size_t mx4_scales(int64_t rows, int32_t cols) { return (size_t)rows * twell::mx4_scale_bytes(cols); }
 
 twell_status check_mx4_dims(int64_t n, int32_t cols, int32_t units) {
-  const twell_status st = check_mx4_shape(n, cols);
+  twell_status st = check_mx4_shape(n, cols);
   if (st != TWELL_OK) return st;
   if (units <= 0) return fail(TWELL_ERR_INVALID_ARG, "units must be > 0");
   if (units > (1 << 24)) return fail(TWELL_ERR_UNSUPPORTED, "units above 2^24");
-  if (((n + 15) / 16) * ((units + 15) / 16) > 0x7FFFFFFFll)
-    return fail(TWELL_ERR_UNSUPPORTED, "more than 2^31 - 1 output tiles of 16 x 16");
+  if ((st = check_mx4_shape(units, cols)) != TWELL_OK) return st;
+  // one launch: a workgroup of 256 threads a tile of 64 x 64, less than 2^32 threads
+  if (((n + 63) / 64) * ((units + 63) / 64) >= (1ll << 24))
+    return fail(TWELL_ERR_UNSUPPORTED, "2^24 output tiles of 64 x 64 or more");
   return TWELL_OK;
 }
 

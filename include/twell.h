@@ -386,7 +386,8 @@ twell_status twell_add_rms_norm_bwd(int64_t rows, int32_t cols, twell_dtype d_ou
  * (two codes a byte, the even column's in the low half) and 16 scale bytes for
  * every 512 begun; both are filled with zeros behind the last column, and the
  * products rely on it. Rows follow one another without gaps. Any cols from 1
- * to 2^20. */
+ * to 2^20; rows x ceil(cols / 512) up to 2^27 (TWELL_ERR_UNSUPPORTED above,
+ * as for a product with 2^24 output tiles of 64 x 64 or more). */
 
 /* Byte sizes of `rows` MX4 rows (host-only query). */
 twell_status twell_mx4_sizes(int64_t rows, int32_t cols, size_t* q_bytes, size_t* scale_bytes);

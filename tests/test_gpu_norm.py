@@ -337,3 +337,19 @@ def test_block_trains():
     for a, b in zip((r, d, blk.norm.weight, blk.ffn.w_gate_t, blk.ffn.w_up_t, blk.ffn.w_down), p64):
         # fp32 sums of at most a few hundred terms of mixed sign
         assert float((a.grad.cpu().double() - b.grad).abs().max()) <= 1e-4 * float(b.grad.abs().max())
+
+
+def test_more_rows_than_a_launch_takes():
+    """Rows behind the first launch's 2^22 come out as they do alone."""
+    require_gpu()
+    rows, cols = 2 * (1 << 22) + 5, 9
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = torch.randn(rows, cols, generator=g, device="cuda").to(BF)
+    d = torch.randn(rows, cols, generator=g, device="cuda")
+    w = torch.randn(cols, generator=g, device="cuda")
+    got = tw.add_rms_norm(r, w, delta=d, eps=EPS, codes=True, rstd=True)
+    for at in (0, (1 << 22) - 3, (1 << 23) - 3, rows - 5):
+        part = slice(at, at + 7)
+        want = tw.add_rms_norm(r[part].clone(), w, delta=d[part].clone(), eps=EPS, codes=True, rstd=True)
+        for a, b in zip(got, want):
+            assert torch.equal(a[part], b)
