@@ -405,6 +405,14 @@ def _queue(stream, t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
+def _new(stream, make):
+    """What make() allocates, from the pool of the stream that will use it."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
 class NormOut(NamedTuple):
     """What add_rms_norm puts out; fields that were not asked for are None."""
     residual: Optional[torch.Tensor]  # [rows, cols] r', dtype of the residual
@@ -441,7 +449,7 @@ def add_rms_norm(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None
     rows, cols = shape
     rc = _code(residual, "residual")
     if out is None:
-        out = alloc_norm(residual, out_dtype, codes, rstd)
+        out = _new(stream, lambda: alloc_norm(residual, out_dtype, codes, rstd))
     elif not isinstance(out, NormOut):
         out = NormOut(*out)
     if (out.codes is None) != (out.scale is None):
@@ -477,7 +485,8 @@ def add_rms_norm_bwd(d_out, residual, rstd, weight, d_residual=None, out=None, w
     rows, cols = shape
     gc, rc, wc = _code(d_out, "d_out"), _code(residual, "residual"), _code(weight, "weight")
     if out is None:
-        dr, dw = torch.empty_like(residual), torch.empty(cols, dtype=torch.float32, device=residual.device)
+        dr, dw = _new(stream, lambda: (torch.empty_like(residual),
+                                       torch.empty(cols, dtype=torch.float32, device=residual.device)))
     else:
         dr, dw = out
     args = (rows, cols, gc, _addr(d_out, "d_out", shape), rc, _addr(d_residual, "d_residual", shape, residual.dtype),
@@ -485,7 +494,8 @@ def add_rms_norm_bwd(d_out, residual, rstd, weight, d_residual=None, out=None, w
             _addr(weight, "weight", shape[1:]), _addr(dr, "dr", shape, residual.dtype),
             _addr(dw, "dw", shape[1:], torch.float32))
     if ws is None:
-        ws = torch.empty(add_rms_norm_bwd_ws(rows, cols), dtype=torch.uint8, device=residual.device)
+        ws = _new(stream, lambda: torch.empty(add_rms_norm_bwd_ws(rows, cols), dtype=torch.uint8,
+                                              device=residual.device))
     _check(lib().twell_add_rms_norm_bwd(*args, ws.data_ptr() or None, ws.numel() * ws.element_size(),
                                         _queue(stream, residual)), "twell_add_rms_norm_bwd")
     return dr, dw
@@ -511,7 +521,7 @@ def quantize_mx4(a, out=None, stream=None):
     rows, cols = a.shape
     dt = _code(a, "a")
     src = _addr(a, "a", a.shape)
-    q, s = alloc_mx4(rows, cols, a.device) if out is None else out
+    q, s = _new(stream, lambda: alloc_mx4(rows, cols, a.device)) if out is None else out
     qs, ss = mx4_shapes(rows, cols)
     _check(lib().twell_quantize_mx4(rows, cols, dt, src, _addr(q, "codes", qs, torch.uint8),
                                     _addr(s, "scales", ss, torch.uint8), _queue(stream, a)), "twell_quantize_mx4")
@@ -524,7 +534,7 @@ def dequantize_mx4(codes, scales, cols: int, dtype=torch.bfloat16, out=None, str
     qs, ss = mx4_shapes(rows, cols)
     q, s = _addr(codes, "codes", qs, torch.uint8), _addr(scales, "scales", ss, torch.uint8)
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
+        out = _new(stream, lambda: torch.empty((rows, cols), dtype=dtype, device=codes.device))
     _check(lib().twell_dequantize_mx4(rows, cols, q, s, _code(out, "out"), _addr(out, "out", (rows, cols)),
                                       _queue(stream, codes)), "twell_dequantize_mx4")
     return out
@@ -547,9 +557,9 @@ def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bflo
     args = (_addr(x_codes, "x_codes", xq, torch.uint8), _addr(x_scales, "x_scales", xs, torch.uint8),
             _addr(w_codes, "w_codes", wq, torch.uint8), _addr(w_scales, "w_scales", wsc, torch.uint8))
     if out is None:
-        out = torch.empty((n, units), dtype=dtype, device=x_codes.device)
+        out = _new(stream, lambda: torch.empty((n, units), dtype=dtype, device=x_codes.device))
     if ws is None:
-        ws = torch.empty(matmul_mx4_ws(n, cols, units), dtype=torch.uint8, device=x_codes.device)
+        ws = _new(stream, lambda: torch.empty(matmul_mx4_ws(n, cols, units), dtype=torch.uint8, device=x_codes.device))
     _check(lib().twell_matmul_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units)),
                                   ws.data_ptr() or None, ws.numel() * ws.element_size(), _queue(stream, x_codes)),
            "twell_matmul_mx4")
@@ -576,9 +586,9 @@ def linear_mx4(x, w_codes, w_scales, dtype=torch.bfloat16, out=None, ws=None, st
     args = (_code(x, "x"), _addr(x, "x", x.shape), _addr(w_codes, "w_codes", wq, torch.uint8),
             _addr(w_scales, "w_scales", wsc, torch.uint8))
     if out is None:
-        out = torch.empty((n, units), dtype=dtype, device=x.device)
+        out = _new(stream, lambda: torch.empty((n, units), dtype=dtype, device=x.device))
     if ws is None:
-        ws = torch.empty(linear_mx4_ws(n, cols, units), dtype=torch.uint8, device=x.device)
+        ws = _new(stream, lambda: torch.empty(linear_mx4_ws(n, cols, units), dtype=torch.uint8, device=x.device))
     _check(lib().twell_linear_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units)),
                                   ws.data_ptr() or None, ws.numel() * ws.element_size(), _queue(stream, x)),
            "twell_linear_mx4")

@@ -152,3 +152,25 @@ def test_refusals():
         p.serve.forward(p.residual, p.delta, w[0], w[1], w[2].float(), *w[3:])
     with pytest.raises(ValueError, match="t must"):
         p.serve.forward(p.residual, p.delta, *w[:4], p.t[:1])
+
+
+def test_buffers_of_another_stream_belong_to_it():
+    """With stream= the outputs and workspaces that a call makes come from that stream's pool, so that what the
+    current stream allocates next does not get them while the other still works there."""
+    require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(600, 1024, generator=g, device="cuda")
+    w = tw.quantize_mx4(torch.randn(2048, 1024, generator=g, device="cuda"))
+    gr, wn = torch.randn(600, 1024, generator=g, device="cuda"), torch.ones(1024, device="cuda")
+    want = tw.linear_mx4(x, *w, dtype=F32)
+    n = tw.add_rms_norm(x, wn, rstd=True)
+    want_dr, want_dw = tw.add_rms_norm_bwd(gr, x, n.rstd, wn)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(8):
+        y = tw.linear_mx4(x, *w, dtype=F32, stream=s)
+        dr, dw = tw.add_rms_norm_bwd(gr, x, n.rstd, wn, stream=s)
+        junk = [torch.full((k,), 0xFF, dtype=torch.uint8, device="cuda") for k in (1 << 18, 1 << 20, 1 << 21)]
+        s.synchronize()
+        assert torch.equal(y, want) and torch.equal(dr, want_dr) and torch.equal(dw, want_dw)
+        del junk
