@@ -13,6 +13,8 @@ typedef uint32_t u32x4_a2_t __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_a4_t __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_a1_t __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32x2_a2_t __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4_a4_t __attribute__((ext_vector_type(4), aligned(4)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
 // Two floats to bf16, nearest with ties to even, NaN kept (v_cvt_pk_bf16_f32).

@@ -44,43 +44,26 @@ __device__ __forceinline__ f32x16_t mfma(const u32x4_t& a, const u32x4_t& b, con
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(a), operand(b), acc, 4, 4, B, (int)sa, B, (int)sb);
 }
 
-// Four neighbouring units of one token. WHOLE: units is a multiple of 4, so
-// that the four exist together and are aligned.
-template <bool BF16, bool WHOLE>
-__device__ __forceinline__ void store_units(void* y, int64_t token, int64_t n, int unit, int units, const f32x4_t& v) {
-  if (token >= n || unit >= units) return;
-  const int64_t at = token * units + unit;
-  if constexpr (BF16) {
-    uint16_t* p = static_cast<uint16_t*>(y) + at;
-    const u32x2_t w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-    if constexpr (WHOLE) {
-      *reinterpret_cast<u32x2_t*>(p) = w;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (unit + k < units) p[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
-    }
-  } else {
-    float* p = static_cast<float*>(y) + at;
-    if constexpr (WHOLE) {
-      *reinterpret_cast<f32x4_t*>(p) = v;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (unit + k < units) p[k] = v[k];
-    }
-  }
-}
-// Calls put(BF16, WHOLE) with what the product's output has.
-template <typename Put>
-__device__ __forceinline__ void store_kind(const Mx4ProductArgs& a, Put put) {
-  const bool whole = a.units % 4 == 0;
+// Four neighbouring units of one token (fewer at the row's end), at any element.
+__device__ __forceinline__ void store_units(const Mx4ProductArgs& a, int64_t token, int unit, const f32x4_t& v) {
+  if (token >= a.n || unit >= a.units) return;
+  const int64_t at = token * a.units + unit;
+  const int have = a.units - unit;
   if (a.y_bf16) {
-    if (whole) put(std::true_type{}, std::true_type{});
-    else put(std::true_type{}, std::false_type{});
+    uint16_t* p = static_cast<uint16_t*>(a.y) + at;
+    const u32x2_t w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    if (have >= 4) {
+      *reinterpret_cast<u32x2_a2_t*>(p) = w;
+    } else {
+      for (int k = 0; k < have; ++k) p[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+    }
   } else {
-    if (whole) put(std::false_type{}, std::true_type{});
-    else put(std::false_type{}, std::false_type{});
+    float* p = static_cast<float*>(a.y) + at;
+    if (have >= 4) {
+      *reinterpret_cast<f32x4_a4_t*>(p) = v;
+    } else {
+      for (int k = 0; k < have; ++k) p[k] = v[k];
+    }
   }
 }
 
@@ -218,10 +201,7 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_product_direct(Mx4ProductArgs 
     f32x4_t s = red[0][f][lane];
 #pragma unroll
     for (int v = 1; v < WAVES; ++v) s += red[v][f][lane];
-    store_kind(a, [&](auto bf16, auto whole) {
-      store_units<decltype(bf16)::value, decltype(whole)::value>(a.y, t0 + 16 * (f % FT) + row, a.n,
-                                                                 u0 + 16 * (f / FT) + 4 * kb, a.units, s);
-    });
+    store_units(a, t0 + 16 * (f % FT) + row, u0 + 16 * (f / FT) + 4 * kb, s);
   }
 }
 
@@ -281,83 +261,73 @@ __device__ __forceinline__ void tile_of(int64_t L, int tb, int ub, int& t, int& 
   u = in / g;
 }
 
-// A wave's results to memory. Where rows of y are 16-byte aligned they go
-// through LDS, 32 tokens by 128 bytes at a time, so that each store writes
-// whole lines (8 tokens, 128 bytes each) instead of 32-byte pieces, each of
-// which is a request of its own to L2.
-template <class C>
+// A wave's results to memory, through LDS, 32 tokens by 128 bytes at a time
+// (16 by 128 where two workgroups share the LDS), so that a store writes whole
+// lines (8 tokens, 128 bytes each) instead of 32-byte pieces, each of which is
+// a request of its own to L2. Rows of y may begin at any element: global memory
+// takes 16 bytes at any address, a line's 128 then touch two (us
+// without the quantisation, this way against 8 or 2 bytes a lane from the
+// registers: 1003 x 1990 x 8100 14.6 : 18.1, x 8101 14.7 : 34.0, 5000 x 2048 x
+// 8101 55.7 : 141; rows of whole lines, x 8192, 14.5).
+template <class C, bool FEW>
 __device__ __forceinline__ void store_tile(const Mx4ProductArgs& a, const f32x16_t (&acc)[C::FU][C::FT], int64_t t0,
                                            int u0, char* out) {
   const int lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5;
   const int esz = a.y_bf16 ? 2 : 4;
-  if (a.units * esz % 16 == 0 && u0 * esz % 16 == 0) {
-    char* y = static_cast<char*>(a.y) + (t0 * a.units + u0) * esz;
-    const int64_t pitch = (int64_t)a.units * esz;
-    const int64_t left = a.n - t0;  // tokens there are
-    constexpr int TOK = C::TOK;
-    // TOK tokens from tok0, bytes [at, at + 128) of the wave's units. A wave's
-    // LDS operations are done in their order; the statements around the reads
-    // keep the compiler to it, which sees no lane's write of what another reads.
-    auto flush = [&](int tok0, int at) {
-      asm volatile("" ::: "memory");
+  char* y = static_cast<char*>(a.y) + (t0 * a.units + u0) * esz;
+  const int64_t pitch = (int64_t)a.units * esz;
+  const int64_t left = a.n - t0;  // tokens there are
+  constexpr int TOK = C::TOK;
+  // TOK tokens from tok0, bytes [at, at + 128) of the wave's units. A wave's
+  // LDS operations are done in their order; the statements around the reads
+  // keep the compiler to it, which sees no lane's write of what another reads.
+  auto flush = [&](int tok0, int at) {
+    asm volatile("" ::: "memory");
 #pragma unroll
-      for (int r = 0; r < TOK / 8; ++r) {
-        const int tok = 8 * r + (lane >> 3);
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(out + tok * 144 + 16 * (lane & 7));
-        if (tok0 + tok < left) *reinterpret_cast<u32x4_t*>(y + (tok0 + tok) * pitch + at + 16 * (lane & 7)) = v;
-      }
-      asm volatile("" ::: "memory");
-    };
+    for (int r = 0; r < TOK / 8; ++r) {
+      const int tok = 8 * r + (lane >> 3);
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(out + tok * 144 + 16 * (lane & 7));
+      if (!FEW || tok0 + tok < left) *reinterpret_cast<u32x4_a2_t*>(y + (tok0 + tok) * pitch + at + 16 * (lane & 7)) = v;
+    }
+    asm volatile("" ::: "memory");
+  };
 #pragma unroll
-    for (int j = 0; j < C::FT; ++j)
+  for (int j = 0; j < C::FT; ++j)
 #pragma unroll
-      for (int h = 0; h < 32 / TOK; ++h) {  // lanes of TOK tokens write, all read
-        const bool mine = row / TOK == h;
-        char* line = out + row % TOK * 144;
-        if (a.y_bf16) {
-          static_assert(C::FU % 2 == 0, "64 units a line");
+    for (int h = 0; h < 32 / TOK; ++h) {  // lanes of TOK tokens write, all read
+      const bool mine = row / TOK == h;
+      char* line = out + row % TOK * 144;
+      if (a.y_bf16) {
+        static_assert(C::FU % 2 == 0, "64 units a line");
 #pragma unroll
-          for (int i = 0; i < C::FU; i += 2) {
-            if (mine) {
+        for (int i = 0; i < C::FU; i += 2) {
+          if (mine) {
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const f32x16_t& v = acc[i + k][j];
-                  *reinterpret_cast<u32x2_t*>(line + 64 * k + 16 * q + 8 * half) =
-                      u32x2_t{pack_bf16(v[4 * q], v[4 * q + 1]), pack_bf16(v[4 * q + 2], v[4 * q + 3])};
-                }
-            }
-            flush(32 * j + TOK * h, 64 * i);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < C::FU; ++i) {
-            if (mine) {
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const f32x16_t& v = acc[i][j];
-                *reinterpret_cast<f32x4_t*>(line + 32 * q + 16 * half) =
-                    f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                const f32x16_t& v = acc[i + k][j];
+                *reinterpret_cast<u32x2_t*>(line + 64 * k + 16 * q + 8 * half) =
+                    u32x2_t{pack_bf16(v[4 * q], v[4 * q + 1]), pack_bf16(v[4 * q + 2], v[4 * q + 3])};
               }
-            }
-            flush(32 * j + TOK * h, 128 * i);
           }
+          flush(32 * j + TOK * h, 64 * i);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < C::FU; ++i) {
+          if (mine) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f32x16_t& v = acc[i][j];
+              *reinterpret_cast<f32x4_t*>(line + 32 * q + 16 * half) =
+                  f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            }
+          }
+          flush(32 * j + TOK * h, 128 * i);
         }
       }
-    return;
-  }
-  store_kind(a, [&](auto bf16, auto whole) {
-#pragma unroll
-    for (int j = 0; j < C::FT; ++j)
-#pragma unroll
-      for (int i = 0; i < C::FU; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          store_units<decltype(bf16)::value, decltype(whole)::value>(
-              a.y, t0 + 32 * j + row, a.n, u0 + 32 * i + 8 * q + 4 * half, a.units,
-              f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
-  });
+    }
 }
 
 // Needs at least BU units, BT tokens (without FEW) and two stages of columns. The last tile
@@ -572,11 +542,11 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx4_product_tiled(Mx4ProductArg
       buf ^= 1;
     }
 
-    store_tile<C>(a, acc, cur.t0 + wt * FT * 32, cur.u0 + wu * FU * 32, smem + 2 * C::STAGE + wave * C::OUT);
+    store_tile<C, FEW>(a, acc, cur.t0 + wt * FT * 32, cur.u0 + wu * FU * 32, smem + 2 * C::STAGE + wave * C::OUT);
     if (!more) break;
     cur = next;
     L += stride;
-    stores = 1;
+    stores = FEW ? 0u : 1u;  // FEW: some have no token to store, and may not have been issued
   }
   wait_vmcnt<0>();  // no load may write to LDS behind the workgroup's end
 }
