@@ -330,12 +330,15 @@ __device__ __forceinline__ void store_tile(const Mx4ProductArgs& a, const f32x16
     }
 }
 
-// Needs at least BU units, BT tokens (without FEW) and two stages of columns. The last tile
+// Needs at least BU units and BT tokens (without FEW). The last tile
 // of a row or column of tiles is moved back to end with the matrix: what it
 // shares with its neighbour is computed by both, to the same bits.
-// HALF: the last stage has only 128 columns. FEW: fewer than BT tokens, one
-// row of tiles; rows behind the last read the last one and are not stored.
-template <class C, bool HALF, bool FEW>
+// HALF: the last stage has only 128 columns. ONE: there is one stage; loads run
+// two ahead, so it is read again as a second, whose codes of w count as zeros
+// (what it multiplies costs little, the product is bound by its stores then).
+// FEW: fewer than BT tokens, one row of tiles; rows behind the last read the
+// last one and are not stored.
+template <class C, bool HALF, bool ONE, bool FEW>
 __global__ __launch_bounds__(C::NT, C::OCC) void mx4_product_tiled(Mx4ProductArgs a, int tb, int ub) {
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
   constexpr int FU = C::FU, FT = C::FT;
@@ -343,7 +346,7 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx4_product_tiled(Mx4ProductArg
   const int wu = wave / C::WT, wt = wave % C::WT;
   const int row = lane & 31, half = lane >> 5;
   const int cbytes = mx4_code_bytes(a.cols);
-  const int KT = (cbytes + 127) / 128;
+  const int KT = ONE ? 2 : (cbytes + 127) / 128;
 
   // This workgroup's tiles: every n-th (n workgroups on the XCD) of its XCD's run.
   const int64_t tiles = (int64_t)tb * ub;
@@ -401,13 +404,13 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx4_product_tiled(Mx4ProductArg
   };
   auto stage_at = [&](const Tile& c, const Tile& n, int kt) {  // past c's last: of n
     const bool in = kt < KT;
-    const int k = in ? kt : kt - KT;
+    const int k = ONE ? 0 : in ? kt : kt - KT;
     Stage r;
     r.wq = (in ? c.wq : n.wq) + 128 * k;
     r.xq = (in ? c.xq : n.xq) + 128 * k;
 #pragma unroll
     for (int g = 0; g < C::SG; ++g) r.sc[g] = (in ? c.sc[g] : n.sc[g]) + k * sstep[g];
-    r.off = HALF && k == KT - 1 ? off_last : off;
+    r.off = HALF && (ONE || k == KT - 1) ? off_last : off;
     return r;
   };
   auto issue = [&](const Stage& t, uint32_t buf, int g) {
@@ -480,7 +483,9 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx4_product_tiled(Mx4ProductArg
       // fourth. Loads are spread over two steps: a wave that issues them at
       // once waits for the address unit and keeps its matrix core waiting.
       const Stage ahead = stage_at(cur, next, kt + 2);
-      const uint32_t live = HALF && kt == KT - 1 ? 0u : ~0u;  // of the last two steps
+      // masks of this stage's last two steps, of its others, and of the next one's first
+      const uint32_t last = HALF && (ONE || kt == KT - 1) ? 0u : ~0u;
+      const uint32_t live = ONE && kt == 1 ? 0u : ~0u, live_next = ONE && kt == 0 ? 0u : ~0u;
       uint32_t na[FU], nb[FT];
       constexpr int OPS = FU + FT, M = FU * FT;  // operands and matrix instructions of a step
       // read r of the 3 OPS behind the first step's operands
@@ -488,14 +493,16 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx4_product_tiled(Mx4ProductArg
         const int ks = 1 + r / OPS, k = r % OPS;
         if (k < FU) {
           av[ks][k] = read_a(k, ks, buf);
-          if (HALF && ks >= 2) av[ks][k] &= live;
+          if (ONE || (HALF && ks >= 2)) av[ks][k] &= ks >= 2 ? last & live : live;
         } else {
           bv[ks][k - FU] = read_b(k - FU, ks, buf);
         }
       };
       auto read_next = [&](int r) {
-        if (r < FU) av[0][r] = read_a(r, 0, buf ^ 1);
-        else if (r < OPS) bv[0][r - FU] = read_b(r - FU, 0, buf ^ 1);
+        if (r < FU) {
+          av[0][r] = read_a(r, 0, buf ^ 1);
+          if (ONE) av[0][r] &= live_next;
+        } else if (r < OPS) bv[0][r - FU] = read_b(r - FU, 0, buf ^ 1);
         else if (r < OPS + FU) na[r - OPS] = read_scale((wu * FU + r - OPS) * 32 + row, buf ^ 1);
         else nb[r - OPS - FU] = read_scale(C::BU + (wt * FT + r - OPS - FU) * 32 + row, buf ^ 1);
       };
@@ -567,15 +574,26 @@ hipError_t launch_direct(const Mx4ProductArgs& a, hipStream_t s) {
 template <class C, bool FEW>
 hipError_t launch_tiled(const Mx4ProductArgs& a, hipStream_t s) {
   // a smaller matrix would be read in front of its first row
-  if ((!FEW && a.n < C::BT) || (FEW && a.n >= C::BT) || a.units < C::BU || a.cols <= 256) return hipErrorInvalidValue;
+  if ((!FEW && a.n < C::BT) || (FEW && a.n >= C::BT) || a.units < C::BU || (FEW && a.cols <= 256))
+    return hipErrorInvalidValue;
   const int tb = (int)((a.n + C::BT - 1) / C::BT), ub = (a.units + C::BU - 1) / C::BU;
   const int64_t tiles = (int64_t)tb * ub;
   const int64_t fit = 256 * C::OCC;  // workgroups that run at a time
   const dim3 grid((unsigned)(tiles < fit ? tiles : fit));
-  if (mx4_code_bytes(a.cols) % 128 == 0)
-    TWELL_LAUNCH("mx4_product_tiled", (mx4_product_tiled<C, false, FEW>), grid, C::NT, 0, s, a, tb, ub);
-  else
-    TWELL_LAUNCH("mx4_product_tiled", (mx4_product_tiled<C, true, FEW>), grid, C::NT, 0, s, a, tb, ub);
+  auto go = [&](auto half, auto one) {
+    TWELL_LAUNCH("mx4_product_tiled", (mx4_product_tiled<C, decltype(half)::value, decltype(one)::value, FEW>), grid,
+                 C::NT, 0, s, a, tb, ub);
+  };
+  using No = std::false_type;
+  using Yes = std::true_type;
+  const bool half = mx4_code_bytes(a.cols) % 128 != 0;
+  if (FEW || a.cols > 256) {
+    if (half) go(Yes{}, No{});
+    else go(No{}, No{});
+  } else if constexpr (!FEW) {
+    if (half) go(Yes{}, Yes{});
+    else go(No{}, Yes{});
+  }
   return hipGetLastError();
 }
 
@@ -600,9 +618,10 @@ hipError_t launch_mx4_product(Mx4Plan plan, const Mx4ProductArgs& a, hipStream_t
       return a.n < Mid::BT ? launch_tiled<Mid, true>(a, s) : launch_tiled<Mid, false>(a, s);
     default:
       if (a.n <= 16) return launch_direct<X_MX4, 1, 1, 4>(a, s);
-      // 64 x 64 tiles where they are many (us with the quantisation, 64 x 64
-      // against 32 x 32: 8192 x 128 x 2048 31 against 35; 300 x 256 x 8192 11.5
-      // against 10.7)
+      // 64 x 64 tiles where they are many (us without the quantisation, 64 x 64
+      // against 32 x 32: 100000 x 1024 x 64 26 against 38, 30000 x 4096 x 100 47
+      // against 81, 100 x 256 x 32000 9.4 against 10.4; 300 x 2048 x 256 9.1
+      // against 5.2)
       return a.n * a.units > 3000000 ? launch_direct<X_MX4, 4, 4, 4>(a, s) : launch_direct<X_MX4, 2, 2, 4>(a, s);
   }
 }

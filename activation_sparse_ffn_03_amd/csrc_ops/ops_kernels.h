@@ -87,20 +87,26 @@ constexpr int kMx4MidTile = 128, kMx4BigTile = 256;
 // 10.6 against 10.4, 10.9, 11.6; 16 x 2048 x 5632: 5.7 against 7.3).
 constexpr int kMx4FusedBlocks = 1024;
 inline bool mx4_fused(int64_t n, int cols) { return n <= 16 && n * ((cols + 255) / 256) * 8 <= kMx4FusedBlocks; }
-// Multiplications from which tiles through LDS are faster than straight from
-// memory (us with the quantisation, tiles against straight: 64 x 2048 x 5632,
-// 0.74e9, 10.7 against 10.2; 1000 x 2048 x 256, 0.52e9, 11.2 against 9.3; 4000 x
-// 300 x 512, 0.61e9, 10.6 against 11.9; 32 x 4096 x 11008, 1.4e9, 15.2 against
-// 16.4; 64 x 4096 x 11008, 2.9e9, 15.8 against 22.5).
-constexpr int64_t kMx4TiledWork = 600000000;
+// Multiplications, and results, from either of which tiles through LDS are
+// faster than straight from memory: with few columns the stores count, which go
+// in whole lines from tiles (us with the quantisation, tiles against straight:
+// 64 x 2048 x 5632, 0.74e9, 10.7 against 10.2; 1000 x 2048 x 256, 0.52e9, 11.2
+// against 9.3; 32 x 4096 x 11008, 1.4e9, 15.2 against 16.4; 64 x 4096 x 11008,
+// 2.9e9, 15.8 against 22.5; without it: 1000 x 128 x 1000, 1.0e6 results, 4.6
+// against 3.7; 4000 x 256 x 513, 2.1e6, 5.1 against 8.0; 300 x 256 x 8192,
+// 2.5e6, 5.1 against 7.8; 8192 x 128 x 2048 12.2 against 27.6; 16384 x 64 x
+// 14336 98 against 348).
+constexpr int64_t kMx4TiledWork = 600000000, kMx4TiledResults = 1500000;
 inline Mx4Plan mx4_plan(int64_t n, int cols, int units, bool x_is_mx4) {
   if (!x_is_mx4 && mx4_fused(n, cols)) return MX4_FUSED;
-  if (n <= 16 || units < kMx4MidTile || cols <= 256 || n * cols < kMx4TiledWork / units) return MX4_DIRECT;
+  if (n <= 16 || units < kMx4MidTile || (n < kMx4MidTile && cols <= 256)) return MX4_DIRECT;
+  if (n * cols < kMx4TiledWork / units && n < kMx4TiledResults / units) return MX4_DIRECT;
   if (n < kMx4BigTile || units < kMx4BigTile) return MX4_MID;
   // 256 x 256 tiles once there are more of them than compute units (us without
-  // the quantisation, 256 against 128: 1003 x 1990 x 8100, 128 tiles, 25.6
-  // against 20.4; 2048 x 4096 x 11008, 344 tiles, 58.5 against 60.3; 4096 x 4096
-  // x 11008, 688 tiles, 92 against 107)
+  // the quantisation, 256 against 128: 1003 x 1990 x 8100, 128 tiles, 18.1
+  // against 14.6; 2048 x 4096 x 11008, 344 tiles, 58.5 against 60.3; 5000 x 2048
+  // x 8101, 640 tiles, 52.5 against 55.7; 4096 x 4096 x 11008, 688 tiles, 92
+  // against 107; 8192 x 200 x 8192, 1024 tiles, 32.1 against 34.5)
   const int64_t tiles = ((n + 255) / 256) * ((units + 255) / 256);
   return tiles > 256 ? MX4_BIG : MX4_MID;
 }

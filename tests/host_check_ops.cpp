@@ -87,7 +87,7 @@ hipError_t launch_mx4_product(Mx4Plan plan, const Mx4ProductArgs& a, hipStream_t
   }
   if (mx4_tiled(plan)) {
     const int tile = plan == MX4_BIG ? kMx4BigTile : kMx4MidTile;
-    CHECK(a.units >= tile && (a.n >= tile || plan == MX4_MID) && a.cols > 256, "a tile larger than the operands");
+    CHECK(a.units >= tile && (a.n >= tile || (plan == MX4_MID && a.cols > 256)), "a tile larger than the operands");
     extent(a.x_arr, mx4_arranged_bytes(mx4_arranged_rows(a.n), a.cols), "arranged x scales");
     extent(a.w_arr, mx4_arranged_bytes(a.units, a.cols), "arranged w scales");
   } else {
@@ -179,6 +179,7 @@ int main() {
         mx4_case(n, cols, units, TWELL_F32, TWELL_BF16);
       }
   mx4_case(5000, 300, 4000, TWELL_BF16, TWELL_BF16);
+  mx4_case(5000, 100, 4000, TWELL_F32, TWELL_F32);
   g_where = "plans";
   for (int p = 0; p < 4; ++p) CHECK(twell::g_plans[p] > 0, "plan %d was not reached", p);
 

@@ -161,7 +161,10 @@ def test_large_products_are_exact(n, cols, units):
 
 
 @pytest.mark.parametrize("n,cols,units", [(100, 4096, 2048), (77, 3333, 4111), (300, 2050, 1024), (600, 1990, 1001),
-                                          (130, 1100, 6000), (4400, 1000, 4352), (4107, 2999, 4333)])
+                                          (130, 1100, 6000), (4400, 1000, 4352), (4107, 2999, 4333),
+                                          # one stage of columns, whole and half, both tiles, edges, several tiles a workgroup
+                                          (1500, 64, 1100), (2049, 128, 1003), (1300, 256, 1201), (131, 129, 12001),
+                                          (4097, 200, 4352), (4100, 100, 4501), (9001, 31, 2055), (150, 255, 70001)])
 def test_large_products(n, cols, units):
     """The tiles on ordinary values, against float64 of the values that the operands stand for."""
     require_gpu()
@@ -182,15 +185,15 @@ def test_large_products(n, cols, units):
     assert torch.equal(tw.linear_mx4(x, wq, ws), b)
 
 
-@pytest.mark.parametrize("n,units", [(4, 40), (20, 40), (70, 70), (70, 300), (300, 200), (4500, 4500)])
-def test_nan_blocks_mark_their_row_and_column(n, units):
+@pytest.mark.parametrize("n,units", [(4, 40), (20, 40), (70, 70), (70, 300), (300, 200), (1500, 1100), (4500, 4500)])
+@pytest.mark.parametrize("cols", [300, 100, 256])
+def test_nan_blocks_mark_their_row_and_column(n, units, cols):
     require_gpu()
-    cols = 300
     rng = np.random.default_rng(n)
     x = torch.from_numpy(rng.standard_normal((n, cols)).astype(np.float32)).cuda()
     w = torch.from_numpy(rng.standard_normal((units, cols)).astype(np.float32)).cuda()
     clean = tw.linear_mx4(x, *tw.quantize_mx4(w), dtype=F32)
-    x[2, 290] = float("nan")
+    x[2, cols - 10] = float("nan")
     w[7, 0] = float("inf")
     y = tw.linear_mx4(x, *tw.quantize_mx4(w), dtype=F32)
     bad = torch.zeros(n, units, dtype=torch.bool, device="cuda")

@@ -111,7 +111,8 @@ def test_mx4_product_workspaces():
     assert tw.linear_mx4_ws(1, 4096, 11008) == 0 and tw.linear_mx4_ws(0, 4096, 11008) == 0
     assert tw.linear_mx4_ws(30, 1990, 8100) == 30 * (1024 + 64) and tw.matmul_mx4_ws(30, 1990, 8100) == 0
     assert tw.linear_mx4_ws(1000, 1990, 100) == 1000 * (1024 + 64)  # fewer units than a tile
-    assert tw.linear_mx4_ws(1000, 200, 8100) == 1000 * (128 + 16)   # one stage of columns
+    assert tw.linear_mx4_ws(100, 200, 30000) == 100 * (128 + 16)    # fewer tokens than a tile, and one stage of columns
+    assert tw.linear_mx4_ws(1000, 200, 8100) == 1000 * 128 + 8 * (8100 + 1000)
     arranged = 8 * 8 * (8100 + 1000)
     assert tw.linear_mx4_ws(1000, 1990, 8100) == 1000 * 1024 + arranged and tw.matmul_mx4_ws(1000, 1990, 8100) == arranged
     # fewer tokens than a tile: x's scales are given a tile's rows
