@@ -617,12 +617,11 @@ hipError_t launch_mx4_product(Mx4Plan plan, const Mx4ProductArgs& a, hipStream_t
     case MX4_MID:
       return a.n < Mid::BT ? launch_tiled<Mid, true>(a, s) : launch_tiled<Mid, false>(a, s);
     default:
-      if (a.n <= 16) return launch_direct<X_MX4, 1, 1, 4>(a, s);
-      // 64 x 64 tiles where they are many (us without the quantisation, 64 x 64
-      // against 32 x 32: 100000 x 1024 x 64 26 against 38, 30000 x 4096 x 100 47
-      // against 81, 100 x 256 x 32000 9.4 against 10.4; 300 x 2048 x 256 9.1
-      // against 5.2)
-      return a.n * a.units > 3000000 ? launch_direct<X_MX4, 4, 4, 4>(a, s) : launch_direct<X_MX4, 2, 2, 4>(a, s);
+      switch (mx4_direct_tile(a.n, a.cols, a.units)) {
+        case 1: return launch_direct<X_MX4, 1, 1, 4>(a, s);
+        case 2: return launch_direct<X_MX4, 2, 2, 4>(a, s);
+        default: return launch_direct<X_MX4, 4, 4, 4>(a, s);
+      }
   }
 }
 

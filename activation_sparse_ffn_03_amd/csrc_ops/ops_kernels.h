@@ -87,20 +87,40 @@ constexpr int kMx4MidTile = 128, kMx4BigTile = 256;
 // 10.6 against 10.4, 10.9, 11.6; 16 x 2048 x 5632: 5.7 against 7.3).
 constexpr int kMx4FusedBlocks = 1024;
 inline bool mx4_fused(int64_t n, int cols) { return n <= 16 && n * ((cols + 255) / 256) * 8 <= kMx4FusedBlocks; }
-// Multiplications, and results, from either of which tiles through LDS are
-// faster than straight from memory: with few columns the stores count, which go
-// in whole lines from tiles (us with the quantisation, tiles against straight:
-// 64 x 2048 x 5632, 0.74e9, 10.7 against 10.2; 1000 x 2048 x 256, 0.52e9, 11.2
-// against 9.3; 32 x 4096 x 11008, 1.4e9, 15.2 against 16.4; 64 x 4096 x 11008,
-// 2.9e9, 15.8 against 22.5; without it: 1000 x 128 x 1000, 1.0e6 results, 4.6
-// against 3.7; 4000 x 256 x 513, 2.1e6, 5.1 against 8.0; 300 x 256 x 8192,
-// 2.5e6, 5.1 against 7.8; 8192 x 128 x 2048 12.2 against 27.6; 16384 x 64 x
-// 14336 98 against 348).
-constexpr int64_t kMx4TiledWork = 600000000, kMx4TiledResults = 1500000;
+// Estimates (us, beside about 3 that every product takes) for straight from
+// memory in tiles of 16 f x 16 f and for tiles through LDS. A tile goes through
+// its columns in stages of 256, at what a stage takes a workgroup that has a
+// compute unit to itself, and all tiles together read their rows at about
+// 5 MB/us; tiles through LDS also have their scales arranged. Measured without
+// the quantisation (us; f = 1, 2, 4, then LDS):
+//   32 x 7442 x 799      5.5  9.3 16.3  17.9     300 x 2048 x 256    4.8  5.2  9.1  6.8
+//   352 x 7541 x 448    11.8  9.5 17.0  18.5     400 x 3776 x 448    9.8  7.8 13.9  9.4
+//   24 x 2048 x 5632     6.3  5.1  8.1   6.8     88 x 5603 x 3552   20.9 14.7 16.6 12.5
+//   128 x 5504 x 5119   24.0 16.1 13.7  14.9     64 x 4096 x 11008  31.3 18.6 14.8 10.4
+//   1208 x 1984 x 1024  27.7 16.1 14.9   7.2     864 x 4672 x 2395  70.3 36.5 29.7 15.0
+//   300 x 256 x 8192       -  7.8  8.4   5.1     1000 x 128 x 1000     -  3.7  4.5  4.6
+//   100000 x 1024 x 64  69.5 37.6 26.4     -     8192 x 128 x 2048     - 31.3 27.7 12.2
+inline double mx4_direct_us(int64_t n, int cols, int units, int f) {
+  const double tiles = (double)((n + 16 * f - 1) / (16 * f)) * ((units + 16 * f - 1) / (16 * f));
+  const int count = (cols + 255) / 256;
+  const double stages = f == 1 ? 0.085 * count : f == 2 ? 0.2 * count : 2 + 0.5 * count;
+  const double reads = tiles * 32 * f * mx4_code_bytes(cols) / 5e6;
+  return stages > reads ? stages : reads;
+}
+inline double mx4_tiled_us(int64_t n, int cols, int units) {
+  const double tiles = (double)((n + 127) / 128) * ((units + 127) / 128);
+  return 1.3 + 0.47 * ((cols + 255) / 256) * (tiles > 256 ? tiles / 256 : 1);
+}
+inline int mx4_direct_tile(int64_t n, int cols, int units) {  // f of the fastest
+  int best = 1;
+  for (int f = 2; f <= 4; f *= 2)
+    if (mx4_direct_us(n, cols, units, f) < mx4_direct_us(n, cols, units, best)) best = f;
+  return best;
+}
 inline Mx4Plan mx4_plan(int64_t n, int cols, int units, bool x_is_mx4) {
   if (!x_is_mx4 && mx4_fused(n, cols)) return MX4_FUSED;
   if (n <= 16 || units < kMx4MidTile || (n < kMx4MidTile && cols <= 256)) return MX4_DIRECT;
-  if (n * cols < kMx4TiledWork / units && n < kMx4TiledResults / units) return MX4_DIRECT;
+  if (mx4_direct_us(n, cols, units, mx4_direct_tile(n, cols, units)) <= mx4_tiled_us(n, cols, units)) return MX4_DIRECT;
   if (n < kMx4BigTile || units < kMx4BigTile) return MX4_MID;
   // 256 x 256 tiles once there are more of them than compute units (us without
   // the quantisation, 256 against 128: 1003 x 1990 x 8100, 128 tiles, 18.1
