@@ -139,7 +139,8 @@ def test_products(n, cols, units):
 
 @pytest.mark.parametrize("n,cols,units", [(4352, 640, 4352), (4099, 1990, 4611), (8192, 130, 2053), (8195, 384, 2304),
                                           (2304, 4096, 8192), (700, 2048, 5632), (1001, 1152, 1003), (90, 4096, 2056),
-                                          (70, 4997, 2055), (127, 4100, 1500), (40003, 384, 130)])
+                                          (70, 4997, 2055), (127, 4100, 1500), (40003, 384, 130),
+                                          (70, 600, 70003), (20, 1100, 132001)])
 def test_large_products_are_exact(n, cols, units):
     """Small whole numbers: every sum is exact in fp32, whatever its order, so y is too. Covers whole grids of the
     tiled product with edges on both sides, against float64 on the GPU's own fp32-exact product."""
