@@ -64,20 +64,30 @@ struct Raw8<uint16_t> {
     }
   }
   // Chunk i as it is: a partial last one is filled with zeros (TAIL: there may
-  // be one, and rows start at any element).
+  // be one, and rows start at any element). Of a partial one the row's last 8
+  // elements are loaded, and moved down by `settle`, to be called when all
+  // loads are on their way.
   template <bool TAIL>
   __device__ __forceinline__ void load_filled(const uint16_t* row, int i, int cols) {
     v = u32x4_t{0u, 0u, 0u, 0u};
     const uint16_t* p = row + 8 * i;
     if constexpr (!TAIL) {
       if (8 * i < cols) v = *reinterpret_cast<const u32x4_t*>(p);
-    } else if (8 * i + 8 <= cols) {
-      v = *reinterpret_cast<const u32x4_a2_t*>(p);
+    } else if (cols >= 8) {
+      if (8 * i < cols) v = *reinterpret_cast<const u32x4_a2_t*>(p - max(8 * i + 8 - cols, 0));
     } else {
 #pragma unroll
       for (int k = 0; k < 7; ++k)
         if (8 * i + k < cols) v[k >> 1] |= (uint32_t)p[k] << (16 * (k & 1));
     }
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void settle(int i, int cols) {
+    const int s = 8 * i + 8 - cols;
+    if (!TAIL || cols < 8 || s <= 0 || s >= 8) return;
+    if (s & 4) v = u32x4_t{v[2], v[3], 0u, 0u};
+    if (s & 2) v = u32x4_t{v[1], v[2], v[3], 0u};
+    if (s & 1) v = u32x4_t{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
   }
   // bit pattern of the largest magnitude, as fp32
   __device__ __forceinline__ uint32_t max_bits() const {
@@ -119,13 +129,33 @@ struct Raw8<float> {
         v[0] = *reinterpret_cast<const u32x4_t*>(p);
         v[1] = *reinterpret_cast<const u32x4_t*>(p + 4);
       }
-    } else if (8 * i + 8 <= cols) {
-      v[0] = *reinterpret_cast<const u32x4_a4_t*>(p);
-      v[1] = *reinterpret_cast<const u32x4_a4_t*>(p + 4);
+    } else if (cols >= 8) {
+      if (8 * i < cols) {
+        p -= max(8 * i + 8 - cols, 0);
+        v[0] = *reinterpret_cast<const u32x4_a4_t*>(p);
+        v[1] = *reinterpret_cast<const u32x4_a4_t*>(p + 4);
+      }
     } else {
 #pragma unroll
       for (int k = 0; k < 7; ++k)
         if (8 * i + k < cols) v[k >> 2][k & 3] = __float_as_uint(p[k]);
+    }
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void settle(int i, int cols) {
+    const int s = 8 * i + 8 - cols;
+    if (!TAIL || cols < 8 || s <= 0 || s >= 8) return;
+    if (s & 4) {
+      v[0] = v[1];
+      v[1] = u32x4_t{0u, 0u, 0u, 0u};
+    }
+    if (s & 2) {
+      v[0] = u32x4_t{v[0][2], v[0][3], v[1][0], v[1][1]};
+      v[1] = u32x4_t{v[1][2], v[1][3], 0u, 0u};
+    }
+    if (s & 1) {
+      v[0] = u32x4_t{v[0][1], v[0][2], v[0][3], v[1][0]};
+      v[1] = u32x4_t{v[1][1], v[1][2], v[1][3], 0u};
     }
   }
   __device__ __forceinline__ uint32_t max_bits() const {

@@ -77,7 +77,10 @@ __device__ __forceinline__ u32x4_t quantize_block(const TX* row, int b, int cols
 #pragma unroll
   for (int c = 0; c < 4; ++c) raw[c].template load_filled<TAIL>(row, 4 * b + c, cols);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) m = max(m, raw[c].max_bits());
+  for (int c = 0; c < 4; ++c) {
+    raw[c].template settle<TAIL>(4 * b + c, cols);
+    m = max(m, raw[c].max_bits());
+  }
   code = mx4_scale_code(m);
   const float sc = mx4_scale_operand(code);
   u32x4_t q;
@@ -90,8 +93,8 @@ __device__ __forceinline__ u32x4_t quantize_block(const TX* row, int b, int cols
 // cache line of codes a row: lane l holds blocks 2 (l >> 4) and 2 (l >> 4) + 1
 // of its row's eight, one for each of two matrix instructions (which blocks
 // share an instruction is free as long as both operands agree).
-// With bf16 or fp32 x (one tile of tokens, at most kMx4FusedBlocks blocks) each
-// workgroup quantises all of x into LDS, one block a thread at a time, while
+// With bf16 or fp32 x (a tile's rows of at most kMx4FusedBlocks blocks) each
+// workgroup quantises its tokens into LDS, one block a thread at a time, while
 // its first weights are on their way.
 template <int XT, int FU, int FT, int WAVES, bool TAIL>
 __global__ __launch_bounds__(64 * WAVES) void mx4_product_direct(Mx4ProductArgs a, int token_tiles) {
@@ -123,8 +126,8 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_product_direct(Mx4ProductArgs 
       xq[j] = a.x_q + t * cbytes + 32 * kb;
       xs[j] = a.x_scale + t * sbytes + 2 * kb;
     } else {
-      xq[j] = reinterpret_cast<const uint8_t*>(x_codes + t * 8 * steps + 2 * kb);
-      xs[j] = x_scales + t * 8 * steps + 2 * kb;
+      xq[j] = reinterpret_cast<const uint8_t*>(x_codes + (t - t0) * 8 * steps + 2 * kb);
+      xs[j] = x_scales + (t - t0) * 8 * steps + 2 * kb;
     }
   }
   f32x4_t acc[FU][FT];
@@ -155,10 +158,11 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_product_direct(Mx4ProductArgs 
   if constexpr (XT != X_MX4) {
     load_w(wave);
     using TX = std::conditional_t<XT == X_BF16, uint16_t, float>;
-    for (int b = threadIdx.x; b < (int)a.n * 8 * steps; b += 64 * WAVES) {
+    const int rows = (int)min((int64_t)16 * FT, a.n - t0);
+    for (int b = threadIdx.x; b < rows * 8 * steps; b += 64 * WAVES) {
       const int t = b / (8 * steps);
       uint32_t code;
-      x_codes[b] = quantize_block<TX, TAIL>(static_cast<const TX*>(a.x) + (int64_t)t * a.cols, b - t * 8 * steps, a.cols,
+      x_codes[b] = quantize_block<TX, TAIL>(static_cast<const TX*>(a.x) + (t0 + t) * a.cols, b - t * 8 * steps, a.cols,
                                             code);
       x_scales[b] = (uint8_t)code;
     }
@@ -609,8 +613,10 @@ hipError_t launch_mx4_product(Mx4Plan plan, const Mx4ProductArgs& a, hipStream_t
     case MX4_FUSED:
       // up to 4 tokens 16 units and 4 waves a workgroup, above twice of both: x
       // is quantised half as often (us at 1 and 8 x 4096 x 11008: 6.6 and 10.7
-      // against 8.0 and 10.6; 16 x 2048 x 5632: 7.3 against 5.7)
+      // against 8.0 and 10.6; 16 x 2048 x 5632: 7.3 against 5.7); from 17 on 32
+      // tokens (24 x 2048 x 5632 7.2, in tiles of 16 tokens 9.8, of 16 units 8.7)
       if (a.n <= 4) return a.x_bf16 ? launch_direct<X_BF16, 1, 1, 4>(a, s) : launch_direct<X_F32, 1, 1, 4>(a, s);
+      if (a.n > 16) return a.x_bf16 ? launch_direct<X_BF16, 2, 2, 8>(a, s) : launch_direct<X_F32, 2, 2, 8>(a, s);
       return a.x_bf16 ? launch_direct<X_BF16, 2, 1, 8>(a, s) : launch_direct<X_F32, 2, 1, 8>(a, s);
     case MX4_BIG:
       return launch_tiled<Big, false>(a, s);

@@ -86,6 +86,7 @@ __global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(const TS* __rest
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
     if (!u.valid(k)) return;
+    raw[k].template settle<TAIL>(64 * u.seg[k] + lane, cols);
     uint32_t m = raw[k].max_bits();
     m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));  // lanes 1 0 3 2
     m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));  // lanes 2 3 0 1

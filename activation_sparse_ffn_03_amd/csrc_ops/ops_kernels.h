@@ -76,17 +76,12 @@ hipError_t launch_dequantize_mx4(const uint8_t* q, const uint8_t* scale, int64_t
 
 // How a product of n tokens, cols columns and `units` units runs.
 enum Mx4Plan {
-  MX4_FUSED,   // few tokens: straight from memory, x quantised in LDS
+  MX4_FUSED,   // straight from memory, x quantised in LDS
   MX4_DIRECT,  // straight from memory
   MX4_MID,     // 128 x 128 tiles through LDS
   MX4_BIG      // 256 x 256 tiles through LDS
 };
 constexpr int kMx4MidTile = 128, kMx4BigTile = 256;
-// Blocks of x (columns rounded up to 256) up to which each workgroup quantises
-// x itself: one launch in place of two (us at 2, 4, 8 x 4096 x 11008: 6.7, 8.4,
-// 10.6 against 10.4, 10.9, 11.6; 16 x 2048 x 5632: 5.7 against 7.3).
-constexpr int kMx4FusedBlocks = 1024;
-inline bool mx4_fused(int64_t n, int cols) { return n <= 16 && n * ((cols + 255) / 256) * 8 <= kMx4FusedBlocks; }
 // Estimates (us, beside about 3 that every product takes) for straight from
 // memory in tiles of 16 f x 16 f and for tiles through LDS. A tile goes through
 // its columns in stages of 256, at what a stage takes a workgroup that has a
@@ -117,10 +112,33 @@ inline int mx4_direct_tile(int64_t n, int cols, int units) {  // f of the fastes
     if (mx4_direct_us(n, cols, units, f) < mx4_direct_us(n, cols, units, best)) best = f;
   return best;
 }
+// A product that quantises x itself: one launch in place of two, and each
+// workgroup quantises the rows of its tile (16 tokens, or 32 where there are
+// more) into LDS, up to this many blocks (columns rounded up to 256).
+constexpr int kMx4FusedBlocks = 1536;
+inline int mx4_fused_blocks(int64_t n, int cols) { return (int)(n < 32 ? n : 32) * ((cols + 255) / 256) * 8; }
+// Up to 16 tokens it wins wherever x fits (us, against two launches: 2, 4, 8 x
+// 4096 x 11008 6.7, 8.4, 10.6 against 10.4, 10.9, 11.6; 16 x 3000 x 5632 7.3
+// against 9.1; 12 x 4096 x 4096 7.9 against 7.7), above it by estimate: 512
+// blocks at a time, again and again where there are more workgroups than compute
+// units, against 2.5 for a launch (us, against two launches: 24 x 2048 x 5632
+// 7.2 : 8.0, 24 x 1024 x 4096 4.8 : 6.5, 60 x 1500 x 1500 7.0 : 7.4, 64 x 2048 x
+// 5632 12.0 : 10.7, 100 x 1024 x 4096 7.6 : 8.4, 200 x 512 x 1024 4.2 : 6.3).
+inline bool mx4_fused(int64_t n, int cols, int units, double two_launches_us) {
+  if (mx4_fused_blocks(n, cols) > kMx4FusedBlocks) return false;
+  if (n <= 16) return true;
+  const double groups = (double)((n + 31) / 32) * ((units + 31) / 32);
+  const double stages = 0.2 * ((cols + 255) / 256), reads = groups * 32 * mx4_code_bytes(cols) / 5e6;
+  const double rounds = (mx4_fused_blocks(n, cols) + 511) / 512 * (groups > 256 ? groups / 256 : 1);
+  return (stages > reads ? stages : reads) + 0.9 * rounds <= two_launches_us + 2.5;
+}
 inline Mx4Plan mx4_plan(int64_t n, int cols, int units, bool x_is_mx4) {
-  if (!x_is_mx4 && mx4_fused(n, cols)) return MX4_FUSED;
-  if (n <= 16 || units < kMx4MidTile || (n < kMx4MidTile && cols <= 256)) return MX4_DIRECT;
-  if (mx4_direct_us(n, cols, units, mx4_direct_tile(n, cols, units)) <= mx4_tiled_us(n, cols, units)) return MX4_DIRECT;
+  const double direct = mx4_direct_us(n, cols, units, mx4_direct_tile(n, cols, units));
+  // tiles need their rows, units and two stages of columns; up to 16 tokens most of a tile would be left empty
+  const bool tiles_fit = n > 16 && units >= kMx4MidTile && (n >= kMx4MidTile || cols > 256);
+  const double tiled = tiles_fit ? mx4_tiled_us(n, cols, units) : direct;
+  if (!x_is_mx4 && mx4_fused(n, cols, units, direct < tiled ? direct : tiled)) return MX4_FUSED;
+  if (direct <= tiled) return MX4_DIRECT;
   if (n < kMx4BigTile || units < kMx4BigTile) return MX4_MID;
   // 256 x 256 tiles once there are more of them than compute units (us without
   // the quantisation, 256 against 128: 1003 x 1990 x 8100, 128 tiles, 18.1

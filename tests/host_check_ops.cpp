@@ -80,8 +80,8 @@ hipError_t launch_mx4_product(Mx4Plan plan, const Mx4ProductArgs& a, hipStream_t
   extent(a.y, (size_t)a.n * a.units * (a.y_bf16 ? 2 : 4), "y");
   if (plan == MX4_FUSED) {
     extent(a.x, (size_t)a.n * a.cols * (a.x_bf16 ? 2 : 4), "x");
-    // the kernel holds all of x in this many blocks of shared memory
-    CHECK(a.n <= 16 && a.n * ((a.cols + 255) / 256) * 8 <= kMx4FusedBlocks, "x does not fit");
+    // the kernel holds a tile's rows of x in this many blocks of shared memory
+    CHECK((a.n < 32 ? a.n : 32) * ((a.cols + 255) / 256) * 8 <= kMx4FusedBlocks, "x does not fit");
   } else {
     extent(a.x_q, (size_t)a.n * mx4_code_bytes(a.cols), "x_q");
   }

@@ -163,6 +163,9 @@ def test_large_products_are_exact(n, cols, units):
 
 @pytest.mark.parametrize("n,cols,units", [(100, 4096, 2048), (77, 3333, 4111), (300, 2050, 1024), (600, 1990, 1001),
                                           (130, 1100, 6000), (4400, 1000, 4352), (4107, 2999, 4333),
+                                          # x quantised by the product, several tiles of tokens
+                                          (24, 2048, 5632), (31, 1500, 3001), (60, 1500, 1500), (100, 1001, 2051), (200, 512, 1024),
+                                          (300, 333, 700),
                                           # one stage of columns, whole and half, both tiles, edges, several tiles a workgroup
                                           (1500, 64, 1100), (2049, 128, 1003), (1300, 256, 1201), (131, 129, 12001),
                                           (4097, 200, 4352), (4100, 100, 4501), (9001, 31, 2055), (150, 255, 70001)])
@@ -180,7 +183,10 @@ def test_large_products(n, cols, units):
     tol = size * ((cols / 8 + cols / 64 + 12) * U)
     y = tw.linear_mx4(x, wq, ws, dtype=F32)
     assert bool(((y.double() - want).abs() <= tol).all())
-    assert torch.equal(tw.matmul_mx4(xq, xs, wq, ws, cols, dtype=F32), y)
+    y2 = tw.matmul_mx4(xq, xs, wq, ws, cols, dtype=F32)
+    if tw.linear_mx4_ws(n, cols, units):  # the same product; one that quantises x adds in another order
+        assert torch.equal(y2, y)
+    assert bool(((y2.double() - want).abs() <= tol).all())
     b = tw.linear_mx4(x, wq, ws)
     assert torch.equal(b, y.to(BF))
     assert torch.equal(tw.linear_mx4(x, wq, ws), b)

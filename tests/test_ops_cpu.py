@@ -109,6 +109,7 @@ def test_mx4_product_workspaces():
     """Nothing for few tokens, x's MX4 rows for some more, and for tiles both operands' scales by 256 columns (8 bytes
     a row, 128 rows at least) in place of x's scale rows."""
     assert tw.linear_mx4_ws(1, 4096, 11008) == 0 and tw.linear_mx4_ws(0, 4096, 11008) == 0
+    assert tw.linear_mx4_ws(24, 2048, 5632) == 0 and tw.linear_mx4_ws(200, 512, 1024) == 0
     assert tw.linear_mx4_ws(30, 1990, 8100) == 30 * (1024 + 64) and tw.matmul_mx4_ws(30, 1990, 8100) == 0
     assert tw.linear_mx4_ws(1000, 1990, 100) == 1000 * (1024 + 64)  # fewer units than a tile
     assert tw.linear_mx4_ws(100, 200, 30000) == 100 * (128 + 16)    # fewer tokens than a tile, and one stage of columns
@@ -140,11 +141,12 @@ def test_mx4_refusals():
     tiles = dict(n=100, k=4096, u=11008)
     assert m(**tiles) == 3 and m(**tiles, ws=FAKE, b2=need - 1) == 3
     assert m(**tiles, ws=ODD, b2=need) == 3 and b"workspace" in L.twell_last_error()
-    f = lambda n=64, k=64, u=8, xd=0, x=FAKE, c=FAKE, e=FAKE, dt=0, y=FAKE, ws=FAKE, b=64 * 80: L.twell_linear_mx4(  # noqa: E731
+    f = lambda n=64, k=4096, u=8, xd=0, x=FAKE, c=FAKE, e=FAKE, dt=0, y=FAKE, ws=FAKE, b=64 * 2176: L.twell_linear_mx4(  # noqa: E731
         n, k, u, xd, x, c, e, dt, y, ws, b, None)
     for kw in (dict(xd=9), dict(x=None), dict(x=ODD), dict(c=None), dict(y=ODD)):
         assert f(**kw) == 1, kw
-    assert f(b=64 * 80 - 1) == 3 and f(ws=None) == 3 and f(ws=ODD) == 3
+    assert tw.linear_mx4_ws(64, 4096, 8) == 64 * 2176
+    assert f(b=64 * 2176 - 1) == 3 and f(ws=None) == 3 and f(ws=ODD) == 3
 
 
 def test_mx4_of_no_rows_needs_no_device():
