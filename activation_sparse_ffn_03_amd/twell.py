@@ -9,6 +9,7 @@ built, loading it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import NamedTuple, Optional
@@ -413,6 +414,16 @@ def _new(stream, make):
         return make()
 
 
+def _workspace(ws, need, t: torch.Tensor, stream):
+    """Address and bytes of `ws`, or of `need` bytes allocated here, and what to keep until the call is made."""
+    if ws is not None:
+        return ws.data_ptr() or None, ws.numel() * ws.element_size(), ws
+    if need == 0:
+        return None, 0, None
+    ws = _new(stream, lambda: torch.empty(need, dtype=torch.uint8, device=t.device))
+    return ws.data_ptr(), need, ws
+
+
 class NormOut(NamedTuple):
     """What add_rms_norm puts out; fields that were not asked for are None."""
     residual: Optional[torch.Tensor]  # [rows, cols] r', dtype of the residual
@@ -465,6 +476,7 @@ def add_rms_norm(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def add_rms_norm_bwd_ws(rows: int, cols: int) -> int:
     """Workspace bytes of add_rms_norm_bwd."""
     n = ctypes.c_size_t()
@@ -493,11 +505,8 @@ def add_rms_norm_bwd(d_out, residual, rstd, weight, d_residual=None, out=None, w
             _addr(residual, "residual", shape), _addr(rstd, "rstd", shape[:1], torch.float32), wc,
             _addr(weight, "weight", shape[1:]), _addr(dr, "dr", shape, residual.dtype),
             _addr(dw, "dw", shape[1:], torch.float32))
-    if ws is None:
-        ws = _new(stream, lambda: torch.empty(add_rms_norm_bwd_ws(rows, cols), dtype=torch.uint8,
-                                              device=residual.device))
-    _check(lib().twell_add_rms_norm_bwd(*args, ws.data_ptr() or None, ws.numel() * ws.element_size(),
-                                        _queue(stream, residual)), "twell_add_rms_norm_bwd")
+    at, n, _keep = _workspace(ws, ws is None and add_rms_norm_bwd_ws(rows, cols), residual, stream)
+    _check(lib().twell_add_rms_norm_bwd(*args, at, n, _queue(stream, residual)), "twell_add_rms_norm_bwd")
     return dr, dw
 
 
@@ -540,6 +549,7 @@ def dequantize_mx4(codes, scales, cols: int, dtype=torch.bfloat16, out=None, str
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def matmul_mx4_ws(rows: int, cols: int, units: int) -> int:
     """Workspace bytes of matmul_mx4."""
     n = ctypes.c_size_t()
@@ -558,14 +568,14 @@ def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bflo
             _addr(w_codes, "w_codes", wq, torch.uint8), _addr(w_scales, "w_scales", wsc, torch.uint8))
     if out is None:
         out = _new(stream, lambda: torch.empty((n, units), dtype=dtype, device=x_codes.device))
-    if ws is None:
-        ws = _new(stream, lambda: torch.empty(matmul_mx4_ws(n, cols, units), dtype=torch.uint8, device=x_codes.device))
+    at, nbytes, _keep = _workspace(ws, ws is None and matmul_mx4_ws(n, cols, units), x_codes, stream)
     _check(lib().twell_matmul_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units)),
-                                  ws.data_ptr() or None, ws.numel() * ws.element_size(), _queue(stream, x_codes)),
+                                  at, nbytes, _queue(stream, x_codes)),
            "twell_matmul_mx4")
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def linear_mx4_ws(rows: int, cols: int, units: int) -> int:
     """Workspace bytes of linear_mx4."""
     n = ctypes.c_size_t()
@@ -587,10 +597,9 @@ def linear_mx4(x, w_codes, w_scales, dtype=torch.bfloat16, out=None, ws=None, st
             _addr(w_scales, "w_scales", wsc, torch.uint8))
     if out is None:
         out = _new(stream, lambda: torch.empty((n, units), dtype=dtype, device=x.device))
-    if ws is None:
-        ws = _new(stream, lambda: torch.empty(linear_mx4_ws(n, cols, units), dtype=torch.uint8, device=x.device))
+    at, nbytes, _keep = _workspace(ws, ws is None and linear_mx4_ws(n, cols, units), x, stream)
     _check(lib().twell_linear_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units)),
-                                  ws.data_ptr() or None, ws.numel() * ws.element_size(), _queue(stream, x)),
+                                  at, nbytes, _queue(stream, x)),
            "twell_linear_mx4")
     return out
 
