@@ -416,8 +416,8 @@ twell_status twell_matmul_mx4(int64_t n, int32_t cols, int32_t units, const uint
                               size_t ws_bytes, void* stream);
 
 /* Workspace bytes of twell_linear_mx4 (host-only query): the MX4 rows of x and
- * what twell_matmul_mx4 needs, or 0 for small n, where the product quantises x
- * as it reads it. */
+ * what twell_matmul_mx4 needs, or 0 where the product quantises x itself (few
+ * tokens, or short rows). */
 twell_status twell_linear_mx4_ws(int64_t n, int32_t cols, int32_t units, size_t* ws_bytes);
 
 /* twell_quantize_mx4 of x [n][cols] (bf16 or fp32) and twell_matmul_mx4 in one
