@@ -417,6 +417,13 @@ def _new(stream, make):
 def _workspace(ws, need, t: torch.Tensor, stream):
     """Address and bytes of `ws`, or of `need` bytes allocated here, and what to keep until the call is made."""
     if ws is not None:
+        # the library goes by the size alone: a host address or bytes that a view does not hold would be written
+        if not ws.is_cuda:
+            raise ValueError("ws must be on the GPU")
+        if ws.get_device() != t.get_device():
+            raise ValueError(f"ws must be on cuda:{t.get_device()}, is on cuda:{ws.get_device()}")
+        if not ws.is_contiguous():
+            raise ValueError("ws must be contiguous")
         return ws.data_ptr() or None, ws.numel() * ws.element_size(), ws
     if need == 0:
         return None, 0, None
