@@ -383,8 +383,8 @@ def _code(t: torch.Tensor, what: str) -> int:
     return c
 
 
-def _addr(t: Optional[torch.Tensor], what: str, shape, dtype=None):
-    """Device address of a contiguous tensor of the given shape (and dtype), None for None or an empty tensor."""
+def _addr(t: Optional[torch.Tensor], what: str, shape, dtype=None, device=None):
+    """Device address of a contiguous tensor of the given shape (dtype, device index), None for None or an empty tensor."""
     if t is None:
         return None
     if t.shape != shape:
@@ -393,9 +393,15 @@ def _addr(t: Optional[torch.Tensor], what: str, shape, dtype=None):
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
+    _on_gpu(t, what, device)
+    return t.data_ptr() or None
+
+
+def _on_gpu(t: torch.Tensor, what: str, device) -> None:
     if not t.is_cuda:
         raise ValueError(f"{what} must be on the GPU")
-    return t.data_ptr() or None
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{what} must be on cuda:{device} like the other tensors, is on cuda:{t.get_device()}")
 
 
 def _queue(stream, t: torch.Tensor) -> int:
@@ -418,10 +424,7 @@ def _workspace(ws, need, t: torch.Tensor, stream):
     """Address and bytes of `ws`, or of `need` bytes allocated here, and what to keep until the call is made."""
     if ws is not None:
         # the library goes by the size alone: a host address or bytes that a view does not hold would be written
-        if not ws.is_cuda:
-            raise ValueError("ws must be on the GPU")
-        if ws.get_device() != t.get_device():
-            raise ValueError(f"ws must be on cuda:{t.get_device()}, is on cuda:{ws.get_device()}")
+        _on_gpu(ws, "ws", t.get_device())
         if not ws.is_contiguous():
             raise ValueError("ws must be contiguous")
         return ws.data_ptr() or None, ws.numel() * ws.element_size(), ws
@@ -472,13 +475,14 @@ def add_rms_norm(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None
         out = NormOut(*out)
     if (out.codes is None) != (out.scale is None):
         raise ValueError("codes and scale go together")
-    row = shape[:1]
+    row, dev = shape[:1], residual.get_device()
     _check(lib().twell_add_rms_norm(
         rows, cols, rc, _addr(residual, "residual", shape), BF16 if delta is None else _code(delta, "delta"),
-        _addr(delta, "delta", shape), _code(weight, "weight"), _addr(weight, "weight", shape[1:]), eps,
-        _addr(out.residual, "out.residual", shape, residual.dtype), F32 if out.out is None else _code(out.out, "out.out"),
-        _addr(out.out, "out.out", shape), _addr(out.codes, "out.codes", shape, torch.uint8),
-        _addr(out.scale, "out.scale", row, torch.float32), _addr(out.rstd, "out.rstd", row, torch.float32),
+        _addr(delta, "delta", shape, None, dev), _code(weight, "weight"), _addr(weight, "weight", shape[1:], None, dev), eps,
+        _addr(out.residual, "out.residual", shape, residual.dtype, dev),
+        F32 if out.out is None else _code(out.out, "out.out"), _addr(out.out, "out.out", shape, None, dev),
+        _addr(out.codes, "out.codes", shape, torch.uint8, dev), _addr(out.scale, "out.scale", row, torch.float32, dev),
+        _addr(out.rstd, "out.rstd", row, torch.float32, dev),
         _queue(stream, residual)), "twell_add_rms_norm")
     return out
 
@@ -508,10 +512,11 @@ def add_rms_norm_bwd(d_out, residual, rstd, weight, d_residual=None, out=None, w
                                        torch.empty(cols, dtype=torch.float32, device=residual.device)))
     else:
         dr, dw = out
-    args = (rows, cols, gc, _addr(d_out, "d_out", shape), rc, _addr(d_residual, "d_residual", shape, residual.dtype),
-            _addr(residual, "residual", shape), _addr(rstd, "rstd", shape[:1], torch.float32), wc,
-            _addr(weight, "weight", shape[1:]), _addr(dr, "dr", shape, residual.dtype),
-            _addr(dw, "dw", shape[1:], torch.float32))
+    res, dev = _addr(residual, "residual", shape), residual.get_device()
+    args = (rows, cols, gc, _addr(d_out, "d_out", shape, None, dev), rc,
+            _addr(d_residual, "d_residual", shape, residual.dtype, dev), res,
+            _addr(rstd, "rstd", shape[:1], torch.float32, dev), wc, _addr(weight, "weight", shape[1:], None, dev),
+            _addr(dr, "dr", shape, residual.dtype, dev), _addr(dw, "dw", shape[1:], torch.float32, dev))
     at, n, _keep = _workspace(ws, ws is None and add_rms_norm_bwd_ws(rows, cols), residual, stream)
     _check(lib().twell_add_rms_norm_bwd(*args, at, n, _queue(stream, residual)), "twell_add_rms_norm_bwd")
     return dr, dw
@@ -539,8 +544,9 @@ def quantize_mx4(a, out=None, stream=None):
     src = _addr(a, "a", a.shape)
     q, s = _new(stream, lambda: alloc_mx4(rows, cols, a.device)) if out is None else out
     qs, ss = mx4_shapes(rows, cols)
-    _check(lib().twell_quantize_mx4(rows, cols, dt, src, _addr(q, "codes", qs, torch.uint8),
-                                    _addr(s, "scales", ss, torch.uint8), _queue(stream, a)), "twell_quantize_mx4")
+    dev = a.get_device()
+    _check(lib().twell_quantize_mx4(rows, cols, dt, src, _addr(q, "codes", qs, torch.uint8, dev),
+                                    _addr(s, "scales", ss, torch.uint8, dev), _queue(stream, a)), "twell_quantize_mx4")
     return q, s
 
 
@@ -548,10 +554,11 @@ def dequantize_mx4(codes, scales, cols: int, dtype=torch.bfloat16, out=None, str
     """The values MX4 rows stand for, [rows, cols] in bf16 or fp32 (twell_dequantize_mx4)."""
     rows = codes.shape[0]
     qs, ss = mx4_shapes(rows, cols)
-    q, s = _addr(codes, "codes", qs, torch.uint8), _addr(scales, "scales", ss, torch.uint8)
+    dev = codes.get_device()
+    q, s = _addr(codes, "codes", qs, torch.uint8), _addr(scales, "scales", ss, torch.uint8, dev)
     if out is None:
         out = _new(stream, lambda: torch.empty((rows, cols), dtype=dtype, device=codes.device))
-    _check(lib().twell_dequantize_mx4(rows, cols, q, s, _code(out, "out"), _addr(out, "out", (rows, cols)),
+    _check(lib().twell_dequantize_mx4(rows, cols, q, s, _code(out, "out"), _addr(out, "out", (rows, cols), None, dev),
                                       _queue(stream, codes)), "twell_dequantize_mx4")
     return out
 
@@ -571,12 +578,13 @@ def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bflo
     matmul_mx4_ws) is allocated here when not."""
     n, units = x_codes.shape[0], w_codes.shape[0]
     (xq, xs), (wq, wsc) = mx4_shapes(n, cols), mx4_shapes(units, cols)
-    args = (_addr(x_codes, "x_codes", xq, torch.uint8), _addr(x_scales, "x_scales", xs, torch.uint8),
-            _addr(w_codes, "w_codes", wq, torch.uint8), _addr(w_scales, "w_scales", wsc, torch.uint8))
+    dev = x_codes.get_device()
+    args = (_addr(x_codes, "x_codes", xq, torch.uint8), _addr(x_scales, "x_scales", xs, torch.uint8, dev),
+            _addr(w_codes, "w_codes", wq, torch.uint8, dev), _addr(w_scales, "w_scales", wsc, torch.uint8, dev))
     if out is None:
         out = _new(stream, lambda: torch.empty((n, units), dtype=dtype, device=x_codes.device))
     at, nbytes, _keep = _workspace(ws, ws is None and matmul_mx4_ws(n, cols, units), x_codes, stream)
-    _check(lib().twell_matmul_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units)),
+    _check(lib().twell_matmul_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units), None, dev),
                                   at, nbytes, _queue(stream, x_codes)),
            "twell_matmul_mx4")
     return out
@@ -600,12 +608,13 @@ def linear_mx4(x, w_codes, w_scales, dtype=torch.bfloat16, out=None, ws=None, st
     n, cols = x.shape
     units = w_codes.shape[0]
     wq, wsc = mx4_shapes(units, cols)
-    args = (_code(x, "x"), _addr(x, "x", x.shape), _addr(w_codes, "w_codes", wq, torch.uint8),
-            _addr(w_scales, "w_scales", wsc, torch.uint8))
+    dev = x.get_device()
+    args = (_code(x, "x"), _addr(x, "x", x.shape), _addr(w_codes, "w_codes", wq, torch.uint8, dev),
+            _addr(w_scales, "w_scales", wsc, torch.uint8, dev))
     if out is None:
         out = _new(stream, lambda: torch.empty((n, units), dtype=dtype, device=x.device))
     at, nbytes, _keep = _workspace(ws, ws is None and linear_mx4_ws(n, cols, units), x, stream)
-    _check(lib().twell_linear_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units)),
+    _check(lib().twell_linear_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units), None, dev),
                                   at, nbytes, _queue(stream, x)),
            "twell_linear_mx4")
     return out

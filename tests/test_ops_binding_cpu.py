@@ -44,3 +44,79 @@ def test_workspace_has_to_be_device_memory_in_one_piece():
     ws = _OnGpu((4096,), torch.uint8)
     assert tw._workspace(ws, 1024, x, None)[:2] == (0x100000, 4096)
     assert tw._workspace(None, 0, x, None)[:2] == (None, 0)
+
+
+class _Library:
+    """Stands for the library: notes which calls are made, and on which current device and stream."""
+
+    def __init__(self, current):
+        self.current, self.calls = current, []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, self.current[0], args[-1]))
+            return 0
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    """The binding on a machine of two GPUs, device 0 current, whose current streams are 1000 and 1001."""
+    current = [0]
+
+    class _Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    made = _Library(current)
+    monkeypatch.setattr(tw, "lib", lambda: made)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + index, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", _Device)
+    return made
+
+
+U8, F32, BF = torch.uint8, torch.float32, torch.bfloat16
+
+
+def _calls():
+    """(function, its tensors by name) for every operator; the tensors are made on the device index given."""
+    def t(*shape, dtype=F32):
+        return lambda index: _OnGpu(shape, dtype, index)
+
+    rows, cols, units = 4, 64, 8
+    mx_x = dict(codes=t(rows, 64, dtype=U8), scales=t(rows, 16, dtype=U8))
+    mx_w = dict(w_codes=t(units, 64, dtype=U8), w_scales=t(units, 16, dtype=U8))
+    return [
+        (lambda v, **k: tw.add_rms_norm(v["residual"], v["weight"], delta=v["delta"],
+                                        out=[v[n] for n in ("r", "o", "q", "s", "rstd")], **k),
+         dict(residual=t(rows, cols), weight=t(cols), delta=t(rows, cols, dtype=BF), r=t(rows, cols), o=t(rows, cols),
+              q=t(rows, cols, dtype=U8), s=t(rows), rstd=t(rows))),
+        (lambda v, **k: tw.add_rms_norm_bwd(v["d_out"], v["residual"], v["rstd"], v["weight"], v["d_residual"],
+                                            out=(v["dr"], v["dw"]), ws=v["ws"], **k),
+         dict(d_out=t(rows, cols), residual=t(rows, cols), rstd=t(rows), weight=t(cols), d_residual=t(rows, cols),
+              dr=t(rows, cols), dw=t(cols), ws=t(64, dtype=U8))),
+        (lambda v, **k: tw.quantize_mx4(v["a"], out=(v["codes"], v["scales"]), **k), dict(a=t(rows, cols), **mx_x)),
+        (lambda v, **k: tw.dequantize_mx4(v["codes"], v["scales"], cols, out=v["out"], **k), dict(out=t(rows, cols), **mx_x)),
+        (lambda v, **k: tw.matmul_mx4(v["codes"], v["scales"], v["w_codes"], v["w_scales"], cols, out=v["y"], ws=v["ws"],
+                                      **k), dict(y=t(rows, units), ws=t(64, dtype=U8), **mx_x, **mx_w)),
+        (lambda v, **k: tw.linear_mx4(v["x"], v["w_codes"], v["w_scales"], out=v["y"], ws=v["ws"], **k),
+         dict(x=t(rows, cols), y=t(rows, units), ws=t(64, dtype=U8), **mx_w)),
+    ]
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_tensors_of_different_devices_are_refused(which, library):
+    call, tensors = _calls()[which]
+    call({n: make(0) for n, make in tensors.items()})
+    assert len(library.calls) == 1
+    for other in tensors:
+        with pytest.raises(ValueError, match="must be on cuda:"):
+            call({n: make(1 if n == other else 0) for n, make in tensors.items()})
+    assert len(library.calls) == 1
