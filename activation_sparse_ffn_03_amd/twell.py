@@ -8,6 +8,7 @@ built, loading it raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -404,12 +405,25 @@ def _on_gpu(t: torch.Tensor, what: str, device) -> None:
         raise ValueError(f"{what} must be on cuda:{device} like the other tensors, is on cuda:{t.get_device()}")
 
 
-def _queue(stream, t: torch.Tensor) -> int:
-    """Handle of `stream`, or of the current stream of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    # current_stream() makes a Stream object and takes 3 us; this is its handle alone
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+def _current(device: int):
+    """A context in which `device` is the current one: launches go to that, whatever their stream's."""
+    return _AS_IT_IS if torch._C._cuda_getDevice() == device else torch.cuda.device(device)
+
+
+_AS_IT_IS = contextlib.nullcontext()
+
+
+def _call(name: str, device: int, stream, *args) -> None:
+    """Calls an entry point with `device` current, on `stream` or on the current stream of `device`."""
+    if stream is None:
+        # current_stream() makes a Stream object and takes 3 us; this is its handle alone
+        queue = torch._C._cuda_getCurrentRawStream(device)
+    elif getattr(stream, "device_index", device) != device:
+        raise ValueError(f"stream must be one of cuda:{device}, where the tensors are, is one of cuda:{stream.device_index}")
+    else:
+        queue = stream.cuda_stream
+    with _current(device):
+        _check(getattr(lib(), name)(*args, queue), name)
 
 
 def _new(stream, make):
@@ -476,14 +490,13 @@ def add_rms_norm(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None
     if (out.codes is None) != (out.scale is None):
         raise ValueError("codes and scale go together")
     row, dev = shape[:1], residual.get_device()
-    _check(lib().twell_add_rms_norm(
-        rows, cols, rc, _addr(residual, "residual", shape), BF16 if delta is None else _code(delta, "delta"),
+    _call(
+        "twell_add_rms_norm", dev, stream, rows, cols, rc, _addr(residual, "residual", shape), BF16 if delta is None else _code(delta, "delta"),
         _addr(delta, "delta", shape, None, dev), _code(weight, "weight"), _addr(weight, "weight", shape[1:], None, dev), eps,
         _addr(out.residual, "out.residual", shape, residual.dtype, dev),
         F32 if out.out is None else _code(out.out, "out.out"), _addr(out.out, "out.out", shape, None, dev),
         _addr(out.codes, "out.codes", shape, torch.uint8, dev), _addr(out.scale, "out.scale", row, torch.float32, dev),
-        _addr(out.rstd, "out.rstd", row, torch.float32, dev),
-        _queue(stream, residual)), "twell_add_rms_norm")
+        _addr(out.rstd, "out.rstd", row, torch.float32, dev))
     return out
 
 
@@ -518,7 +531,7 @@ def add_rms_norm_bwd(d_out, residual, rstd, weight, d_residual=None, out=None, w
             _addr(rstd, "rstd", shape[:1], torch.float32, dev), wc, _addr(weight, "weight", shape[1:], None, dev),
             _addr(dr, "dr", shape, residual.dtype, dev), _addr(dw, "dw", shape[1:], torch.float32, dev))
     at, n, _keep = _workspace(ws, ws is None and add_rms_norm_bwd_ws(rows, cols), residual, stream)
-    _check(lib().twell_add_rms_norm_bwd(*args, at, n, _queue(stream, residual)), "twell_add_rms_norm_bwd")
+    _call("twell_add_rms_norm_bwd", dev, stream, *args, at, n)
     return dr, dw
 
 
@@ -545,8 +558,8 @@ def quantize_mx4(a, out=None, stream=None):
     q, s = _new(stream, lambda: alloc_mx4(rows, cols, a.device)) if out is None else out
     qs, ss = mx4_shapes(rows, cols)
     dev = a.get_device()
-    _check(lib().twell_quantize_mx4(rows, cols, dt, src, _addr(q, "codes", qs, torch.uint8, dev),
-                                    _addr(s, "scales", ss, torch.uint8, dev), _queue(stream, a)), "twell_quantize_mx4")
+    _call("twell_quantize_mx4", dev, stream, rows, cols, dt, src, _addr(q, "codes", qs, torch.uint8, dev),
+          _addr(s, "scales", ss, torch.uint8, dev))
     return q, s
 
 
@@ -558,8 +571,8 @@ def dequantize_mx4(codes, scales, cols: int, dtype=torch.bfloat16, out=None, str
     q, s = _addr(codes, "codes", qs, torch.uint8), _addr(scales, "scales", ss, torch.uint8, dev)
     if out is None:
         out = _new(stream, lambda: torch.empty((rows, cols), dtype=dtype, device=codes.device))
-    _check(lib().twell_dequantize_mx4(rows, cols, q, s, _code(out, "out"), _addr(out, "out", (rows, cols), None, dev),
-                                      _queue(stream, codes)), "twell_dequantize_mx4")
+    _call("twell_dequantize_mx4", dev, stream, rows, cols, q, s, _code(out, "out"),
+          _addr(out, "out", (rows, cols), None, dev))
     return out
 
 
@@ -584,9 +597,8 @@ def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bflo
     if out is None:
         out = _new(stream, lambda: torch.empty((n, units), dtype=dtype, device=x_codes.device))
     at, nbytes, _keep = _workspace(ws, ws is None and matmul_mx4_ws(n, cols, units), x_codes, stream)
-    _check(lib().twell_matmul_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units), None, dev),
-                                  at, nbytes, _queue(stream, x_codes)),
-           "twell_matmul_mx4")
+    _call("twell_matmul_mx4", dev, stream, n, cols, units, *args, _code(out, "out"),
+          _addr(out, "out", (n, units), None, dev), at, nbytes)
     return out
 
 
@@ -614,9 +626,8 @@ def linear_mx4(x, w_codes, w_scales, dtype=torch.bfloat16, out=None, ws=None, st
     if out is None:
         out = _new(stream, lambda: torch.empty((n, units), dtype=dtype, device=x.device))
     at, nbytes, _keep = _workspace(ws, ws is None and linear_mx4_ws(n, cols, units), x, stream)
-    _check(lib().twell_linear_mx4(n, cols, units, *args, _code(out, "out"), _addr(out, "out", (n, units), None, dev),
-                                  at, nbytes, _queue(stream, x)),
-           "twell_linear_mx4")
+    _call("twell_linear_mx4", dev, stream, n, cols, units, *args, _code(out, "out"),
+          _addr(out, "out", (n, units), None, dev), at, nbytes)
     return out
 
 
@@ -775,21 +786,27 @@ class TwellServe:
         then the block on its norm. Returns y [n_tokens, d_model] fp32, the
         delta of whatever comes next; the next call overwrites it, after it has
         read it where it is that call's delta."""
-        d, N, D, F = self.dims, self.dims.n_tokens, self.dims.d_model, self.dims.d_ff
+        N, D, F, dev = self.dims.n_tokens, self.dims.d_model, self.dims.d_ff, self.y.get_device()
         if residual.dtype != self.stream_dtype or tuple(residual.shape) != (N, D):
             raise ValueError(f"residual must be {self.stream_dtype} [{N}, {D}]")
-        _addr(w_up_t, "w_up_t", (F, D), torch.bfloat16)
-        _addr(w_down, "w_down", (F, D), torch.bfloat16)
-        _addr(t, "t", (N,), torch.float32)
+        _addr(w_up_t, "w_up_t", (F, D), torch.bfloat16, dev)
+        _addr(w_down, "w_down", (F, D), torch.bfloat16, dev)
+        _addr(t, "t", (N,), torch.float32, dev)
         if self.gate == "bf16":
-            _addr(w_gate, "w_gate", (F, D), torch.bfloat16)
+            _addr(w_gate, "w_gate", (F, D), torch.bfloat16, dev)
         elif self.gate == "fp8":
-            _addr(w_gate[0], "w_gate codes", (F, D), torch.uint8)
-            _addr(w_gate[1], "w_gate scales", (F,), torch.float32)
+            _addr(w_gate[0], "w_gate codes", (F, D), torch.uint8, dev)
+            _addr(w_gate[1], "w_gate scales", (F,), torch.float32, dev)
         else:
             wq, wsc = mx4_shapes(F, D)
-            _addr(w_gate[0], "w_gate codes", wq, torch.uint8)
-            _addr(w_gate[1], "w_gate scales", wsc, torch.uint8)
+            _addr(w_gate[0], "w_gate codes", wq, torch.uint8, dev)
+            _addr(w_gate[1], "w_gate scales", wsc, torch.uint8, dev)
+        with _current(dev):  # the block's calls go to the current device and its stream
+            self._run(residual, delta, norm_weight, w_gate, w_up_t, w_down, t, stream)
+        return self.y
+
+    def _run(self, residual, delta, norm_weight, w_gate, w_up_t, w_down, t, stream):
+        d = self.dims
         add_rms_norm(residual, norm_weight, delta, self.eps, stream=stream,
                      out=NormOut(None if delta is None else residual, self.x, self.x_q, self.x_scale, None))
         if self.gate == "bf16":
@@ -802,7 +819,6 @@ class TwellServe:
             linear_mx4(self.x, *w_gate, out=self.g, ws=self.ws_gate, stream=stream)
             pack_preact(d, BF16, self.g, t, self.pack, stream=stream)
             ffn_fwd(d, BF16, self.pack, self.x, w_up_t, w_down, self.y, ws=self.ws_fwd, stream=stream)
-        return self.y
 
     def capture_supported(self) -> bool:
         """False on the forwards whose graph capture is not cleared for
@@ -819,9 +835,10 @@ class TwellServe:
         if not self.capture_supported():
             raise TwellError(2, "TwellServe.capture", "graph capture of this forward (d_model > 2048 with possible "
                              "overflow rows) is disabled; call forward() eagerly")
-        self.forward(residual.clone(), delta, norm_weight, w_gate, w_up_t, w_down, t)
-        torch.cuda.synchronize()
-        graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(graph):
-            self.forward(residual, delta, norm_weight, w_gate, w_up_t, w_down, t)
+        with _current(self.y.get_device()):
+            self.forward(residual.clone(), delta, norm_weight, w_gate, w_up_t, w_down, t)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                self.forward(residual, delta, norm_weight, w_gate, w_up_t, w_down, t)
         return graph

@@ -120,3 +120,59 @@ def test_tensors_of_different_devices_are_refused(which, library):
         with pytest.raises(ValueError, match="must be on cuda:"):
             call({n: make(1 if n == other else 0) for n, make in tensors.items()})
     assert len(library.calls) == 1
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_calls_run_on_the_device_of_their_tensors(which, library):
+    """A launch goes to the current device, whatever its stream's: that of the tensors has to be current."""
+    call, tensors = _calls()[which]
+    for index in (0, 1):
+        call({n: make(index) for n, make in tensors.items()})
+        assert library.calls[-1][1:] == (index, 1000 + index)
+        assert library.current == [0]  # the caller's device is left as it was
+
+
+class _Stream:
+    def __init__(self, index):
+        self.device_index, self.cuda_stream = index, 77
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_a_stream_of_another_device_is_refused(which, library):
+    call, tensors = _calls()[which]
+    call({n: make(1) for n, make in tensors.items()}, stream=_Stream(1))
+    assert library.calls[-1][1:] == (1, 77)
+    with pytest.raises(ValueError, match="stream"):
+        call({n: make(1) for n, make in tensors.items()}, stream=_Stream(0))
+    assert len(library.calls) == 1
+
+
+def test_serving_block_runs_on_the_device_of_its_buffers(library):
+    """All launches of a forward, those of the gate and the projections among them, go to the device of the buffers."""
+    class _Serve(tw.TwellServe):
+        def __init__(self, gate, index):
+            N, D, F = 4, 64, 128
+            self.dims, self.gate, self.eps, self.stream_dtype = tw.make_dims(N, D, F, 64, 64), gate, 1e-6, BF
+            make = lambda *shape, dtype=F32: _OnGpu(shape, dtype, index)  # noqa: E731
+            self.x, self.y, self.g, self.ws_gate = make(N, D, dtype=BF), make(N, D), make(N, F), make(64, dtype=U8)
+            self.x_q, self.x_scale = (make(N, D, dtype=U8), make(N)) if gate == "fp8" else (None, None)
+            self.pack, self.ws_fwd = None, make(64, dtype=U8)
+
+    seen = []
+    note = lambda *a, **k: seen.append(library.current[0])  # noqa: E731
+    with pytest.MonkeyPatch.context() as mp:
+        for name in ("ffn_forward", "ffn_forward_fp8", "pack_preact", "ffn_fwd"):
+            mp.setattr(tw, name, note)
+        for index in (0, 1):
+            make = lambda *shape, dtype=F32: _OnGpu(shape, dtype, index)  # noqa: E731
+            gates = {"bf16": make(128, 64, dtype=BF), "fp8": (make(128, 64, dtype=U8), make(128)),
+                     "mx4": (make(128, 64, dtype=U8), make(128, 16, dtype=U8))}
+            for gate, w in gates.items():
+                first, before = len(seen), len(library.calls)
+                up = make(128, 64, dtype=BF)
+                _Serve(gate, index).forward(make(4, 64, dtype=BF), make(4, 64), make(64), w, up, up, make(4))
+                assert len(seen) > first and all(i == index for i in seen[first:])
+                assert [c[1] for c in library.calls[before:]] == [index] * (2 if gate == "mx4" else 1)
+                with pytest.raises(ValueError, match="must be on cuda:"):
+                    _Serve(gate, 1 - index).forward(make(4, 64, dtype=BF), make(4, 64), make(64), w, up, up, make(4))
+    assert library.current == [0]
