@@ -831,12 +831,15 @@ class TwellServe:
     def capture(self, residual, delta, norm_weight, w_gate, w_up_t, w_down, t) -> "torch.cuda.CUDAGraph":
         """Record forward() on these tensors into a HIP graph, after one eager
         call on a copy of the stream. A replay adds what delta holds then to
-        the stream and leaves the result in self.y."""
+        the stream and leaves the result in self.y; delta may be self.y, which
+        capture() leaves as it was."""
         if not self.capture_supported():
             raise TwellError(2, "TwellServe.capture", "graph capture of this forward (d_model > 2048 with possible "
                              "overflow rows) is disabled; call forward() eagerly")
         with _current(self.y.get_device()):
+            y = self.y.clone()
             self.forward(residual.clone(), delta, norm_weight, w_gate, w_up_t, w_down, t)
+            self.y.copy_(y)
             torch.cuda.synchronize()
             graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(graph):
