@@ -151,6 +151,13 @@ class TwellGatedFFN(torch.nn.Module):
         return y.reshape(*lead, y.shape[-1])
 
 
+def _packed(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy of it where it is not contiguous or does not begin at 16 bytes, as the library wants its arrays:
+    rows of an odd width behind the first, and the gradients that cat hands out, begin anywhere."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class AddRmsNormFunction(torch.autograd.Function):
     """r' = residual + delta and out = the RMS norm of r' times weight, through
     libtwell's kernels both ways. Inputs are [rows, cols]; returns (r', out),
@@ -159,9 +166,9 @@ class AddRmsNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, residual, delta, weight, eps: float, out_dtype):
         train = any(ctx.needs_input_grad[:3])
-        residual, weight = residual.contiguous(), weight.contiguous()
+        residual, weight = _packed(residual), _packed(weight)
         if delta is not None:
-            delta = delta.contiguous()
+            delta = _packed(delta)
         got = tw.alloc_norm(residual, out_dtype, rstd=train)
         if delta is None:
             got = got._replace(residual=None)
@@ -184,8 +191,8 @@ class AddRmsNormFunction(torch.autograd.Function):
         else:
             if d_out.dtype not in (torch.bfloat16, torch.float32):
                 d_out = d_out.float()
-            d_residual = None if d_residual is None else d_residual.contiguous()
-            dr, dw = tw.add_rms_norm_bwd(d_out.contiguous(), residual, rstd, weight, d_residual=d_residual)
+            d_residual = None if d_residual is None else _packed(d_residual)
+            dr, dw = tw.add_rms_norm_bwd(_packed(d_out), residual, rstd, weight, d_residual=d_residual)
             dw = dw.to(weight.dtype)
         return (dr if need[0] else None, dr.to(ctx.delta_dtype) if dr is not None and need[1] else None,
                 dw if need[2] else None, None, None)

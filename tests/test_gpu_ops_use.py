@@ -5,6 +5,7 @@ from __future__ import annotations
 import pytest
 import torch
 
+from activation_sparse_ffn_03_amd import autograd as ag
 from activation_sparse_ffn_03_amd import twell as tw
 from gpu_util import require_gpu
 
@@ -39,3 +40,48 @@ def test_capture_keeps_the_pending_delta(gate):
         want = eager.forward(want_stream, want, *weights)
         torch.cuda.synchronize()
         assert torch.equal(stream, want_stream) and torch.equal(y, want)
+
+
+def _norm64(r, w):
+    x = r.double()
+    return x / torch.sqrt((x * x).mean(-1, keepdim=True) + EPS) * w.double()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("cols", [1999, 1000, 5])
+def test_autograd_takes_views_that_begin_anywhere(cols, dtype):
+    """Slices of rows of an odd width, views into a flat buffer (of the weight, too), and the gradient that cat hands
+    to its second input: none begins at 16 bytes, values and gradients are those of the same rows alone."""
+    require_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(dtype)  # noqa: E731
+    rows = 5
+
+    def view(*shape):  # an element behind an aligned address
+        n = 1
+        for s in shape:
+            n *= s
+        return rnd(n + 1)[1:].view(shape)
+
+    r, d, w, top = view(rows, cols), rnd(rows + 1, cols)[1:], view(cols), rnd(1, cols)
+    assert any(t.data_ptr() % 16 for t in (r, d, w))
+
+    def run(make):
+        v = [make(t) for t in (r, d, w, top)]
+        for t in v:
+            t.requires_grad_()
+        st, out = ag.add_rms_norm(v[0], v[2], v[1], eps=EPS)
+        both = torch.cat([v[3], out]) * torch.cat([st, v[3]])
+        both.float().square().sum().backward()
+        return [st, out] + [t.grad for t in v]
+
+    for got, want in zip(run(lambda t: t.detach()), run(lambda t: t.detach().clone())):
+        assert torch.equal(got, want)
+    st, out = ag.add_rms_norm(r.detach(), w.detach(), d.detach(), eps=EPS)
+    assert torch.equal(st, (r.detach().float() + d.detach().float()).to(dtype))
+    n = _norm64(st, w.detach())
+    # the row's sum of squares: at most cols / 2 + 8 roundings of fp32 reach the norm, then its own
+    assert bool(((out.double() - n).abs() <= n.abs() * ((cols / 2 + 8) * 2.0 ** -24 + torch.finfo(dtype).eps / 2 * 1.01)).all())
+    alone = ag.add_rms_norm(r.detach(), w.detach(), eps=EPS)
+    assert alone[0].data_ptr() == r.data_ptr()  # nothing to add: the stream itself
+    assert torch.equal(alone[1], ag.add_rms_norm(r.detach().clone(), w.detach().clone(), eps=EPS)[1])
