@@ -16,6 +16,8 @@
 // Bound by memory: the stream and the addition are read once, the new stream,
 // out and the codes written once; the row stays in registers between its three
 // passes (sum of squares, largest magnitude, encoding).
+#include <cfloat>
+
 #include "chunk8.h"
 #include "ops_kernels.h"
 #include "../csrc/twell_trace.h"
@@ -49,6 +51,11 @@ __device__ __forceinline__ u32x2_t encode8(const float (&n)[8], float sc) {
   }
   return r;
 }
+
+// Where a row's sum of squares overflows its elements are scaled by this, so
+// that the sum is below their mean square.
+constexpr float kShrink = 1.f / 128;
+static_assert(kNormMaxCols <= 128 * 128, "the sum of the shrunk squares of a row");
 
 // 448 * 2^-126: from here the scale is a normal number.
 constexpr uint32_t kNormalScaleBits = 0x04E00000u;
@@ -103,21 +110,36 @@ __global__ __launch_bounds__(norm_threads<T>()) void add_rms_norm_kernel(NormArg
     for (int k = 0; k < 8; ++k)
       if (chunk_counts<KIND>(t + T * c, k, cols)) ss = fmaf(x[c][k], x[c][k], ss);
   }
-  __shared__ float red_sum[WPR];
+  __shared__ float red_sum[2][WPR];
   __shared__ uint32_t red_max[WPR];
-  ss = group_sum<G>(ss);
-  if constexpr (WPR > 1) {
-    if ((threadIdx.x & 63) == 0) red_sum[wave] = ss;
-    lds_barrier();
+  // The row's sum in every thread of it, the same bits in all.
+  auto row_sum = [&](float s, float* red) {
+    s = group_sum<G>(s);
+    if constexpr (WPR > 1) {
+      if ((threadIdx.x & 63) == 0) red[wave] = s;
+      lds_barrier();
+      s = 0.f;
+#pragma unroll
+      for (int i = 0; i < WPR; ++i) s += red[i];
+    }
+    return s;
+  };
+  ss = row_sum(ss, red_sum[0]);
+  float mean = ss / (float)cols;
+  if (ss > FLT_MAX) {  // all threads of the row or none
     ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < WPR; ++i) ss += red_sum[i];
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (chunk_counts<KIND>(t + T * c, k, cols)) ss = fmaf(x[c][k] * kShrink, x[c][k] * kShrink, ss);
+    mean = row_sum(ss, red_sum[1]) * (1.f / (kShrink * kShrink) / (float)cols);
   }
   if (a.residual_out != nullptr) {  // behind the sum: every thread has read its part of the row
 #pragma unroll
     for (int c = 0; c < C; ++c) store8<KIND>(static_cast<TR*>(a.residual_out) + off, t + T * c, cols, x[c]);
   }
-  const float rho = 1.0f / sqrtf(ss / (float)cols + a.eps);
+  const float rho = 1.0f / sqrtf(mean + a.eps);
   if (a.rstd != nullptr && t == 0) a.rstd[row] = rho;
 
   uint32_t mb = 0;

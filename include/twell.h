@@ -345,8 +345,8 @@ twell_status twell_ffn_bwd(const twell_dims* dims, twell_dtype dtype, const twel
  *   q[i,k]       = E4M3(n[i,k] / q_scale[i]), the rounding and the special
  *                  values of twell_quantize_e4m3.
  * The norm is that of r' as stored. The codes come from the fp32 n, so they
- * are those of twell_quantize_e4m3 on an fp32 out. A row whose fp32 sum of
- * squares overflows (elements above about 1.8e19) has rho = 0.
+ * are those of twell_quantize_e4m3 on an fp32 out. A row whose mean of squares
+ * is beyond fp32 (root mean square above about 1.8e19) has rho = 0.
  * residual [rows][cols] res_dtype; delta [rows][cols] delta_dtype or NULL (then
  * r' = residual); weight [cols] weight_dtype; eps > 0. residual_out, out, q
  * (with q_scale [rows]) and rstd [rows] may each be NULL, not all of them.

@@ -1,5 +1,5 @@
 """The operators around the block as programs use them: a captured step that adds its own y, views that begin
-anywhere."""
+anywhere, rows whose squares overflow a sum."""
 from __future__ import annotations
 
 import pytest
@@ -85,3 +85,45 @@ def test_autograd_takes_views_that_begin_anywhere(cols, dtype):
     alone = ag.add_rms_norm(r.detach(), w.detach(), eps=EPS)
     assert alone[0].data_ptr() == r.data_ptr()  # nothing to add: the stream itself
     assert torch.equal(alone[1], ag.add_rms_norm(r.detach().clone(), w.detach().clone(), eps=EPS)[1])
+
+
+@pytest.mark.parametrize("res", [F32, BF])
+@pytest.mark.parametrize("cols", [16, 95, 200, 509, 512, 1000, 2050, 4096, 8200, 16383, 16384])
+def test_norm_of_rows_whose_squares_overflow_a_sum(cols, res):
+    """Elements far below the root of the largest number, whose squares add up to more than it: the norm, its codes
+    and gradient are those of any other row. A mean of squares beyond fp32 still has rho = 0, and rows of ordinary
+    size next to such ones keep their bits."""
+    require_gpu()
+    gen = torch.Generator().manual_seed(cols)
+    rows = 19
+    r = 1 + torch.rand(rows, cols, generator=gen)
+    sizes = [1.0, 1e16, 1e17, 2e17, 5e17, 1e18, 3e18, 7e18, 8.5e18]  # rms up to 1.7e19
+    for i in range(rows):
+        r[i] *= sizes[i % len(sizes)]
+    r[rows - 1] = 1e20  # its mean of squares is beyond fp32
+    r = r.to(res)
+    w = 1 + 0.3 * torch.randn(cols, generator=gen)
+    got = tw.add_rms_norm(r.cuda(), w.cuda(), eps=EPS, out_dtype=F32, codes=True, rstd=True)
+    x = r.double()[:-1]
+    rho = 1 / torch.sqrt((x * x).mean(1, keepdim=True) + EPS)
+    # at most 32 squares a thread, 6 + 4 steps over lanes and 8 waves: 50 roundings of positive terms, which the root
+    # halves; then mean (two), eps, root and quotient
+    rel = (50 / 2 + 5) * 2.0 ** -24
+    assert bool(((got.rstd.cpu().double()[:-1, None] - rho).abs() <= rho * rel).all())
+    n = x * rho * w.double()
+    assert bool(((got.out.cpu().double()[:-1] - n).abs() <= n.abs() * (rel + 2.0 ** -23)).all())
+    q, s = tw.quantize_e4m3(got.out)
+    assert torch.equal(q, got.codes) and torch.equal(s, got.scale)
+    assert float(got.rstd[-1]) == 0 and bool((got.out[-1] == 0).all())
+    plain = [i for i in range(rows) if i % len(sizes) == 0 and i < rows - 1]
+    for a, b in zip(got, tw.add_rms_norm(r[plain].cuda(), w.cuda(), eps=EPS, out_dtype=F32, codes=True, rstd=True)):
+        assert torch.equal(a[plain], b)
+    g = torch.randn(rows, cols, generator=gen)
+    dr, dw = tw.add_rms_norm_bwd(g[:-1].cuda(), r[:-1].cuda(), got.rstd[:-1].contiguous(), w.cuda())
+    rs = got.rstd[:-1].cpu().double()[:, None]
+    u, xh = g[:-1].double() * w.double(), x * rs
+    size = rs * (u.abs() + xh.abs() * (u * xh).abs().mean(1, keepdim=True))
+    want = rs * (u - xh * (u * xh).mean(1, keepdim=True))
+    # the row's mean is off by at most 60 roundings of its absolute terms, the products by 6; then the type's own
+    err, step = (dr.cpu().double() - want).abs(), torch.finfo(res).eps / 2
+    assert bool((err <= size * (66 * 2.0 ** -24 + (step if res == BF else 0) * 1.01) + 2.0 ** -133).all())
