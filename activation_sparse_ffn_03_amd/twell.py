@@ -384,6 +384,13 @@ def _code(t: torch.Tensor, what: str) -> int:
     return c
 
 
+def _int32(where: str, *sizes: int) -> None:
+    """Refuses sizes that the library's 32-bit arguments would cut off."""
+    for n in sizes:
+        if not -(1 << 31) <= n < 1 << 31:
+            raise TwellError(2, where, f"{n} columns or units, above 2^31 - 1")
+
+
 def _addr(t: Optional[torch.Tensor], what: str, shape, dtype=None, device=None):
     """Device address of a contiguous tensor of the given shape (dtype, device index), None for None or an empty tensor."""
     if t is None:
@@ -482,6 +489,7 @@ def add_rms_norm(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None
         raise ValueError("residual must be [rows, cols]")
     shape = residual.shape
     rows, cols = shape
+    _int32("twell_add_rms_norm", cols)
     rc = _code(residual, "residual")
     if out is None:
         out = _new(stream, lambda: alloc_norm(residual, out_dtype, codes, rstd))
@@ -503,6 +511,7 @@ def add_rms_norm(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None
 @functools.lru_cache(maxsize=256)
 def add_rms_norm_bwd_ws(rows: int, cols: int) -> int:
     """Workspace bytes of add_rms_norm_bwd."""
+    _int32("twell_add_rms_norm_bwd_ws", cols)
     n = ctypes.c_size_t()
     _check(lib().twell_add_rms_norm_bwd_ws(rows, cols, ctypes.byref(n)), "twell_add_rms_norm_bwd_ws")
     return n.value
@@ -519,6 +528,7 @@ def add_rms_norm_bwd(d_out, residual, rstd, weight, d_residual=None, out=None, w
         raise ValueError("residual must be [rows, cols]")
     shape = residual.shape
     rows, cols = shape
+    _int32("twell_add_rms_norm_bwd", cols)
     gc, rc, wc = _code(d_out, "d_out"), _code(residual, "residual"), _code(weight, "weight")
     if out is None:
         dr, dw = _new(stream, lambda: (torch.empty_like(residual),
@@ -553,6 +563,7 @@ def quantize_mx4(a, out=None, stream=None):
     if a.dim() != 2:
         raise ValueError("quantize_mx4 takes a [rows, cols] tensor")
     rows, cols = a.shape
+    _int32("twell_quantize_mx4", cols)
     dt = _code(a, "a")
     src = _addr(a, "a", a.shape)
     q, s = _new(stream, lambda: alloc_mx4(rows, cols, a.device)) if out is None else out
@@ -566,6 +577,7 @@ def quantize_mx4(a, out=None, stream=None):
 def dequantize_mx4(codes, scales, cols: int, dtype=torch.bfloat16, out=None, stream=None):
     """The values MX4 rows stand for, [rows, cols] in bf16 or fp32 (twell_dequantize_mx4)."""
     rows = codes.shape[0]
+    _int32("twell_dequantize_mx4", cols)
     qs, ss = mx4_shapes(rows, cols)
     dev = codes.get_device()
     q, s = _addr(codes, "codes", qs, torch.uint8), _addr(scales, "scales", ss, torch.uint8, dev)
@@ -579,6 +591,7 @@ def dequantize_mx4(codes, scales, cols: int, dtype=torch.bfloat16, out=None, str
 @functools.lru_cache(maxsize=256)
 def matmul_mx4_ws(rows: int, cols: int, units: int) -> int:
     """Workspace bytes of matmul_mx4."""
+    _int32("twell_matmul_mx4_ws", cols, units)
     n = ctypes.c_size_t()
     _check(lib().twell_matmul_mx4_ws(rows, cols, units, ctypes.byref(n)), "twell_matmul_mx4_ws")
     return n.value
@@ -590,6 +603,7 @@ def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bflo
     rows of w] in bf16 or fp32, written into `out` when given; ws (bytes of
     matmul_mx4_ws) is allocated here when not."""
     n, units = x_codes.shape[0], w_codes.shape[0]
+    _int32("twell_matmul_mx4", cols, units)
     (xq, xs), (wq, wsc) = mx4_shapes(n, cols), mx4_shapes(units, cols)
     dev = x_codes.get_device()
     args = (_addr(x_codes, "x_codes", xq, torch.uint8), _addr(x_scales, "x_scales", xs, torch.uint8, dev),
@@ -605,6 +619,7 @@ def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bflo
 @functools.lru_cache(maxsize=256)
 def linear_mx4_ws(rows: int, cols: int, units: int) -> int:
     """Workspace bytes of linear_mx4."""
+    _int32("twell_linear_mx4_ws", cols, units)
     n = ctypes.c_size_t()
     _check(lib().twell_linear_mx4_ws(rows, cols, units, ctypes.byref(n)), "twell_linear_mx4_ws")
     return n.value
@@ -619,6 +634,7 @@ def linear_mx4(x, w_codes, w_scales, dtype=torch.bfloat16, out=None, ws=None, st
         raise ValueError("x must be [rows, cols]")
     n, cols = x.shape
     units = w_codes.shape[0]
+    _int32("twell_linear_mx4", cols, units)
     wq, wsc = mx4_shapes(units, cols)
     dev = x.get_device()
     args = (_code(x, "x"), _addr(x, "x", x.shape), _addr(w_codes, "w_codes", wq, torch.uint8, dev),

@@ -176,3 +176,32 @@ def test_serving_block_runs_on_the_device_of_its_buffers(library):
                 with pytest.raises(ValueError, match="must be on cuda:"):
                     _Serve(gate, 1 - index).forward(make(4, 64, dtype=BF), make(4, 64), make(64), w, up, up, make(4))
     assert library.current == [0]
+
+
+def test_sizes_beyond_32_bits_are_refused(library):
+    """The library takes columns and units as 32-bit numbers; 2^32 + 64 of them must not pass for 64."""
+    far = (1 << 32) + 64
+    t = lambda *shape, dtype=F32: _OnGpu(shape, dtype)  # noqa: E731
+    mx = lambda rows, cols: [t(*shape, dtype=U8) for shape in tw.mx4_shapes(rows, cols)]  # noqa: E731
+    long, short, y, ws = mx(2, far), mx(2, 64), t(2, 2), t(64, dtype=U8)
+    norm = [t(2, far), t(2, far), None, None, t(2)]
+    for call in (lambda: tw.add_rms_norm(t(2, far), t(far), out=norm),
+                 lambda: tw.add_rms_norm_bwd(t(2, far), t(2, far), t(2), t(far), out=(t(2, far), t(far)), ws=ws),
+                 lambda: tw.quantize_mx4(t(2, far), out=long),
+                 lambda: tw.dequantize_mx4(*long, far, out=t(2, far)),
+                 lambda: tw.matmul_mx4(*long, *long, far, out=y, ws=ws),
+                 lambda: tw.matmul_mx4(*short, *mx(far, 64), 64, out=t(2, far), ws=ws),
+                 lambda: tw.linear_mx4(t(2, far), *long, out=y, ws=ws),
+                 lambda: tw.linear_mx4(t(2, 64), *mx(far, 64), out=t(2, far), ws=ws)):
+        with pytest.raises(tw.TwellError, match="UNSUPPORTED"):
+            call()
+    assert not library.calls
+
+
+def test_workspaces_of_sizes_beyond_32_bits_are_refused():
+    far = (1 << 32) + 64
+    for call in (lambda: tw.add_rms_norm_bwd_ws(600, far), lambda: tw.matmul_mx4_ws(100, far, 64),
+                 lambda: tw.matmul_mx4_ws(100, 64, far), lambda: tw.linear_mx4_ws(100, far, 64),
+                 lambda: tw.linear_mx4_ws(100, 64, far)):
+        with pytest.raises(tw.TwellError, match="UNSUPPORTED"):
+            call()
