@@ -384,11 +384,12 @@ def _code(t: torch.Tensor, what: str) -> int:
     return c
 
 
-def _int32(where: str, *sizes: int) -> None:
-    """Refuses sizes that the library's 32-bit arguments would cut off."""
-    for n in sizes:
-        if not -(1 << 31) <= n < 1 << 31:
-            raise TwellError(2, where, f"{n} columns or units, above 2^31 - 1")
+_INT32 = (1 << 31) - 1
+
+
+def _too_large(where: str, n: int):
+    """A size that the library's 32-bit arguments would cut off."""
+    raise TwellError(2, where, f"{n} columns or units, above 2^31 - 1")
 
 
 def _addr(t: Optional[torch.Tensor], what: str, shape, dtype=None, device=None):
@@ -401,7 +402,9 @@ def _addr(t: Optional[torch.Tensor], what: str, shape, dtype=None, device=None):
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    _on_gpu(t, what, device)
+    at = t.get_device()  # one query where all is as it should be; -1 on the CPU
+    if at != device or at < 0:
+        _on_gpu(t, what, device)
     return t.data_ptr() or None
 
 
@@ -414,13 +417,10 @@ def _on_gpu(t: torch.Tensor, what: str, device) -> None:
 
 def _current(device: int):
     """A context in which `device` is the current one: launches go to that, whatever their stream's."""
-    return _AS_IT_IS if torch._C._cuda_getDevice() == device else torch.cuda.device(device)
+    return contextlib.nullcontext() if torch._C._cuda_getDevice() == device else torch.cuda.device(device)
 
 
-_AS_IT_IS = contextlib.nullcontext()
-
-
-def _call(name: str, device: int, stream, *args) -> None:
+def _call(entry, device: int, stream, *args) -> None:
     """Calls an entry point with `device` current, on `stream` or on the current stream of `device`."""
     if stream is None:
         # current_stream() makes a Stream object and takes 3 us; this is its handle alone
@@ -429,8 +429,13 @@ def _call(name: str, device: int, stream, *args) -> None:
         raise ValueError(f"stream must be one of cuda:{device}, where the tensors are, is one of cuda:{stream.device_index}")
     else:
         queue = stream.cuda_stream
-    with _current(device):
-        _check(getattr(lib(), name)(*args, queue), name)
+    if torch._C._cuda_getDevice() == device:
+        st = entry(*args, queue)
+    else:
+        with torch.cuda.device(device):
+            st = entry(*args, queue)
+    if st != 0:
+        _check(st, entry.__name__)
 
 
 def _new(stream, make):
@@ -489,7 +494,8 @@ def add_rms_norm(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None
         raise ValueError("residual must be [rows, cols]")
     shape = residual.shape
     rows, cols = shape
-    _int32("twell_add_rms_norm", cols)
+    if cols > _INT32:
+        _too_large("twell_add_rms_norm", cols)
     rc = _code(residual, "residual")
     if out is None:
         out = _new(stream, lambda: alloc_norm(residual, out_dtype, codes, rstd))
@@ -499,8 +505,9 @@ def add_rms_norm(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None
         raise ValueError("codes and scale go together")
     row, dev = shape[:1], residual.get_device()
     _call(
-        "twell_add_rms_norm", dev, stream, rows, cols, rc, _addr(residual, "residual", shape), BF16 if delta is None else _code(delta, "delta"),
-        _addr(delta, "delta", shape, None, dev), _code(weight, "weight"), _addr(weight, "weight", shape[1:], None, dev), eps,
+        lib().twell_add_rms_norm, dev, stream, rows, cols, rc, _addr(residual, "residual", shape),
+        BF16 if delta is None else _code(delta, "delta"), _addr(delta, "delta", shape, None, dev),
+        _code(weight, "weight"), _addr(weight, "weight", shape[1:], None, dev), eps,
         _addr(out.residual, "out.residual", shape, residual.dtype, dev),
         F32 if out.out is None else _code(out.out, "out.out"), _addr(out.out, "out.out", shape, None, dev),
         _addr(out.codes, "out.codes", shape, torch.uint8, dev), _addr(out.scale, "out.scale", row, torch.float32, dev),
@@ -511,7 +518,8 @@ def add_rms_norm(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None
 @functools.lru_cache(maxsize=256)
 def add_rms_norm_bwd_ws(rows: int, cols: int) -> int:
     """Workspace bytes of add_rms_norm_bwd."""
-    _int32("twell_add_rms_norm_bwd_ws", cols)
+    if cols > _INT32:
+        _too_large("twell_add_rms_norm_bwd_ws", cols)
     n = ctypes.c_size_t()
     _check(lib().twell_add_rms_norm_bwd_ws(rows, cols, ctypes.byref(n)), "twell_add_rms_norm_bwd_ws")
     return n.value
@@ -528,7 +536,8 @@ def add_rms_norm_bwd(d_out, residual, rstd, weight, d_residual=None, out=None, w
         raise ValueError("residual must be [rows, cols]")
     shape = residual.shape
     rows, cols = shape
-    _int32("twell_add_rms_norm_bwd", cols)
+    if cols > _INT32:
+        _too_large("twell_add_rms_norm_bwd", cols)
     gc, rc, wc = _code(d_out, "d_out"), _code(residual, "residual"), _code(weight, "weight")
     if out is None:
         dr, dw = _new(stream, lambda: (torch.empty_like(residual),
@@ -541,7 +550,7 @@ def add_rms_norm_bwd(d_out, residual, rstd, weight, d_residual=None, out=None, w
             _addr(rstd, "rstd", shape[:1], torch.float32, dev), wc, _addr(weight, "weight", shape[1:], None, dev),
             _addr(dr, "dr", shape, residual.dtype, dev), _addr(dw, "dw", shape[1:], torch.float32, dev))
     at, n, _keep = _workspace(ws, ws is None and add_rms_norm_bwd_ws(rows, cols), residual, stream)
-    _call("twell_add_rms_norm_bwd", dev, stream, *args, at, n)
+    _call(lib().twell_add_rms_norm_bwd, dev, stream, *args, at, n)
     return dr, dw
 
 
@@ -563,13 +572,14 @@ def quantize_mx4(a, out=None, stream=None):
     if a.dim() != 2:
         raise ValueError("quantize_mx4 takes a [rows, cols] tensor")
     rows, cols = a.shape
-    _int32("twell_quantize_mx4", cols)
+    if cols > _INT32:
+        _too_large("twell_quantize_mx4", cols)
     dt = _code(a, "a")
     src = _addr(a, "a", a.shape)
     q, s = _new(stream, lambda: alloc_mx4(rows, cols, a.device)) if out is None else out
     qs, ss = mx4_shapes(rows, cols)
     dev = a.get_device()
-    _call("twell_quantize_mx4", dev, stream, rows, cols, dt, src, _addr(q, "codes", qs, torch.uint8, dev),
+    _call(lib().twell_quantize_mx4, dev, stream, rows, cols, dt, src, _addr(q, "codes", qs, torch.uint8, dev),
           _addr(s, "scales", ss, torch.uint8, dev))
     return q, s
 
@@ -577,13 +587,14 @@ def quantize_mx4(a, out=None, stream=None):
 def dequantize_mx4(codes, scales, cols: int, dtype=torch.bfloat16, out=None, stream=None):
     """The values MX4 rows stand for, [rows, cols] in bf16 or fp32 (twell_dequantize_mx4)."""
     rows = codes.shape[0]
-    _int32("twell_dequantize_mx4", cols)
+    if cols > _INT32:
+        _too_large("twell_dequantize_mx4", cols)
     qs, ss = mx4_shapes(rows, cols)
     dev = codes.get_device()
     q, s = _addr(codes, "codes", qs, torch.uint8), _addr(scales, "scales", ss, torch.uint8, dev)
     if out is None:
         out = _new(stream, lambda: torch.empty((rows, cols), dtype=dtype, device=codes.device))
-    _call("twell_dequantize_mx4", dev, stream, rows, cols, q, s, _code(out, "out"),
+    _call(lib().twell_dequantize_mx4, dev, stream, rows, cols, q, s, _code(out, "out"),
           _addr(out, "out", (rows, cols), None, dev))
     return out
 
@@ -591,7 +602,8 @@ def dequantize_mx4(codes, scales, cols: int, dtype=torch.bfloat16, out=None, str
 @functools.lru_cache(maxsize=256)
 def matmul_mx4_ws(rows: int, cols: int, units: int) -> int:
     """Workspace bytes of matmul_mx4."""
-    _int32("twell_matmul_mx4_ws", cols, units)
+    if cols > _INT32 or units > _INT32:
+        _too_large("twell_matmul_mx4_ws", max(cols, units))
     n = ctypes.c_size_t()
     _check(lib().twell_matmul_mx4_ws(rows, cols, units, ctypes.byref(n)), "twell_matmul_mx4_ws")
     return n.value
@@ -603,7 +615,8 @@ def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bflo
     rows of w] in bf16 or fp32, written into `out` when given; ws (bytes of
     matmul_mx4_ws) is allocated here when not."""
     n, units = x_codes.shape[0], w_codes.shape[0]
-    _int32("twell_matmul_mx4", cols, units)
+    if cols > _INT32 or units > _INT32:
+        _too_large("twell_matmul_mx4", max(cols, units))
     (xq, xs), (wq, wsc) = mx4_shapes(n, cols), mx4_shapes(units, cols)
     dev = x_codes.get_device()
     args = (_addr(x_codes, "x_codes", xq, torch.uint8), _addr(x_scales, "x_scales", xs, torch.uint8, dev),
@@ -611,7 +624,7 @@ def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bflo
     if out is None:
         out = _new(stream, lambda: torch.empty((n, units), dtype=dtype, device=x_codes.device))
     at, nbytes, _keep = _workspace(ws, ws is None and matmul_mx4_ws(n, cols, units), x_codes, stream)
-    _call("twell_matmul_mx4", dev, stream, n, cols, units, *args, _code(out, "out"),
+    _call(lib().twell_matmul_mx4, dev, stream, n, cols, units, *args, _code(out, "out"),
           _addr(out, "out", (n, units), None, dev), at, nbytes)
     return out
 
@@ -619,7 +632,8 @@ def matmul_mx4(x_codes, x_scales, w_codes, w_scales, cols: int, dtype=torch.bflo
 @functools.lru_cache(maxsize=256)
 def linear_mx4_ws(rows: int, cols: int, units: int) -> int:
     """Workspace bytes of linear_mx4."""
-    _int32("twell_linear_mx4_ws", cols, units)
+    if cols > _INT32 or units > _INT32:
+        _too_large("twell_linear_mx4_ws", max(cols, units))
     n = ctypes.c_size_t()
     _check(lib().twell_linear_mx4_ws(rows, cols, units, ctypes.byref(n)), "twell_linear_mx4_ws")
     return n.value
@@ -634,7 +648,8 @@ def linear_mx4(x, w_codes, w_scales, dtype=torch.bfloat16, out=None, ws=None, st
         raise ValueError("x must be [rows, cols]")
     n, cols = x.shape
     units = w_codes.shape[0]
-    _int32("twell_linear_mx4", cols, units)
+    if cols > _INT32 or units > _INT32:
+        _too_large("twell_linear_mx4", max(cols, units))
     wq, wsc = mx4_shapes(units, cols)
     dev = x.get_device()
     args = (_code(x, "x"), _addr(x, "x", x.shape), _addr(w_codes, "w_codes", wq, torch.uint8, dev),
@@ -642,7 +657,7 @@ def linear_mx4(x, w_codes, w_scales, dtype=torch.bfloat16, out=None, ws=None, st
     if out is None:
         out = _new(stream, lambda: torch.empty((n, units), dtype=dtype, device=x.device))
     at, nbytes, _keep = _workspace(ws, ws is None and linear_mx4_ws(n, cols, units), x, stream)
-    _call("twell_linear_mx4", dev, stream, n, cols, units, *args, _code(out, "out"),
+    _call(lib().twell_linear_mx4, dev, stream, n, cols, units, *args, _code(out, "out"),
           _addr(out, "out", (n, units), None, dev), at, nbytes)
     return out
 
