@@ -10,8 +10,10 @@
 // reads the stored residual, differentiates exactly what was computed, and so
 // that adding first and norming later give the same. The codes come from the
 // fp32 n and not from the rounded out: one rounding, and for an fp32 out they
-// are bit for bit those of quantising it. The sum of squares is held in fp32
-// (rows with elements above 1.8e19 overflow it: their norm is 0).
+// are bit for bit those of quantising it. The sum of squares is held in fp32;
+// where it overflows (a row of 16384 equal elements from 1.5e17 on) it is taken
+// again over elements scaled down, so that only a mean of squares beyond fp32 (a
+// root mean square above 1.8e19) gives a norm of 0.
 //
 // Bound by memory: the stream and the addition are read once, the new stream,
 // out and the codes written once; the row stays in registers between its three

@@ -114,16 +114,25 @@ inline int mx4_direct_tile(int64_t n, int cols, int units) {  // f of the fastes
 }
 // A product that quantises x itself: one launch in place of two, and each
 // workgroup quantises the rows of its tile (16 tokens, or 32 where there are
-// more) into LDS, up to this many blocks (columns rounded up to 256).
+// more) into LDS, up to this many blocks (columns rounded up to 256). With the
+// waves' sums that is 58 KB, two workgroups a compute unit. The edge is a middle
+// between two shapes (us, one launch against two): long rows of up to 16 tokens
+// lose before it (5, 8, 12, 13, 16 x 4096 x 11008 10.2, 11.3, 13.4, 13.7, 15.0
+// against 11.7, 12.3, 13.0, 13.2, 13.7; 8, 12, 13, 16 x 4096 x 4096 6.7, 7.8,
+// 8.1, 8.6 against 7.0, 7.3, 7.3, 7.6: equal at about 1300 blocks), shorter rows
+// of more tokens win beyond it, too (17, 20, 24 x 2048 x 5632 6.0, 6.1, 6.8
+// against 7.2, 7.4, 7.5; 25, 28, 32, which take two launches, 7.0, 7.3, 7.7
+// against 7.4, 7.7, 7.8).
 constexpr int kMx4FusedBlocks = 1536;
 inline int mx4_fused_blocks(int64_t n, int cols) { return (int)(n < 32 ? n : 32) * ((cols + 255) / 256) * 8; }
-// Up to 16 tokens it wins wherever x fits (us, against two launches: 2, 4, 8 x
-// 4096 x 11008 6.7, 8.4, 10.6 against 10.4, 10.9, 11.6; 16 x 3000 x 5632 7.3
-// against 9.1; 12 x 4096 x 4096 7.9 against 7.7), above it by estimate: 512
-// blocks at a time, again and again where there are more workgroups than compute
-// units, against 2.5 for a launch (us, against two launches: 24 x 2048 x 5632
-// 7.2 : 8.0, 24 x 1024 x 4096 4.8 : 6.5, 60 x 1500 x 1500 7.0 : 7.4, 64 x 2048 x
-// 5632 12.0 : 10.7, 100 x 1024 x 4096 7.6 : 8.4, 200 x 512 x 1024 4.2 : 6.3).
+// Up to 16 tokens wherever x fits (us, against two launches: 2, 4 x 4096 x 11008
+// 6.7, 8.4 against 10.4, 10.9; 16 x 3000 x 5632 7.3 against 9.1; 16 x 2048 x 5632
+// 5.4 against 7.3; it loses up to 0.5 just below the edge, see there), above by
+// estimate: 512 blocks at a time, again and again where there are more workgroups
+// than compute units, against 2.5 for a launch (us, against two launches: 24 x
+// 1024 x 4096 4.5 : 6.2, 32 x 1024 x 4096 5.0 : 6.4, 60 x 1500 x 1500 7.0 : 7.4,
+// 64 x 2048 x 5632 12.0 : 10.7, 100 x 1024 x 4096 7.6 : 8.4, 200 x 512 x 1024
+// 4.2 : 6.3).
 inline bool mx4_fused(int64_t n, int cols, int units, double two_launches_us) {
   if (mx4_fused_blocks(n, cols) > kMx4FusedBlocks) return false;
   if (n <= 16) return true;

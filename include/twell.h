@@ -398,7 +398,8 @@ twell_status twell_quantize_mx4(int64_t rows, int32_t cols, twell_dtype dtype, c
                                 uint8_t* scale, void* stream);
 
 /* MX4 rows -> out [rows][cols] bf16 or fp32: the values the codes stand for,
- * exactly (NaN where the scale code is 255). */
+ * exactly (NaN where the scale code is 255; 253 and 254, which the quantisation
+ * never writes, may give infinity). */
 twell_status twell_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t* q, const uint8_t* scale,
                                   twell_dtype dtype, void* out, void* stream);
 
@@ -408,8 +409,9 @@ twell_status twell_matmul_mx4_ws(int64_t n, int32_t cols, int32_t units, size_t*
 
 /* y[i][c] = sum_k x[i,k] * w[c,k] for MX4 rows x ([n] rows of cols columns) and
  * w ([units] rows): the products of a block's codes are exact, their sums and
- * the scaled blocks' are held in fp32, y [n][units] is rounded once to
- * y_dtype. NaN scales make their row or column of y NaN. n == 0 is a no-op.
+ * the scaled blocks' are held in fp32 (subnormal numbers included, infinity
+ * above the largest), y [n][units] is rounded once to y_dtype. NaN scales make
+ * their row or column of y NaN. n == 0 is a no-op.
  * ws: at least the queried bytes (NULL allowed when that is 0). */
 twell_status twell_matmul_mx4(int64_t n, int32_t cols, int32_t units, const uint8_t* x_q, const uint8_t* x_scale,
                               const uint8_t* w_q, const uint8_t* w_scale, twell_dtype y_dtype, void* y, void* ws,
@@ -422,8 +424,9 @@ twell_status twell_linear_mx4_ws(int64_t n, int32_t cols, int32_t units, size_t*
 
 /* twell_quantize_mx4 of x [n][cols] (bf16 or fp32) and twell_matmul_mx4 in one
  * call: the gate's pre-activation for twell_pack_preact when w is the gate
- * weight. A serving operator: it has no backward. ws: at least the queried
- * bytes (NULL allowed when that is 0). */
+ * weight. Both operands then have four bits: a gate of it activates other units
+ * than the bf16 gate's near the threshold. A serving operator: it has no
+ * backward. ws: at least the queried bytes (NULL allowed when that is 0). */
 twell_status twell_linear_mx4(int64_t n, int32_t cols, int32_t units, twell_dtype x_dtype, const void* x,
                               const uint8_t* w_q, const uint8_t* w_scale, twell_dtype y_dtype, void* y, void* ws,
                               size_t ws_bytes, void* stream);
