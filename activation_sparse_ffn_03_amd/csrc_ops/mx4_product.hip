@@ -238,9 +238,11 @@ struct TileCfg {
 };
 
 // 16 bytes per lane from base + off straight into LDS, lane l's at lds + 16 l.
+// A load that takes M0 has to be one wait state behind its write; the compiler
+// does not see to that inside a statement.
 __device__ __forceinline__ void dma_16B(const uint8_t* base, uint32_t off, uint32_t lds) {
   const uint32_t m = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(m) : "memory");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(m) : "memory");
 }
 // vmcnt(M) if `many` (uniform) is not 0, else vmcnt(N). The branch is inside
 // the statement: one that the compiler sees would split the loop's body, and
