@@ -81,10 +81,12 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 
 // 16 bytes per lane from global memory straight into LDS
 // (global_load_lds_dwordx4): lane l's bytes land at lds_byte + 16 * l, where
-// lds_byte is the wave's base address (wave-uniform by construction).
+// lds_byte is the wave's base address (wave-uniform by construction). A load
+// that takes M0 has to be one wait state behind its write; the compiler does not
+// see to that inside a statement.
 __device__ __forceinline__ void dma_16B(const void* g, uint32_t lds_byte) {
   const uint32_t m = __builtin_amdgcn_readfirstlane(lds_byte);
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(m) : "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(m) : "memory");
 }
 // Wait until at most N of this wave's vector memory operations are outstanding.
 template <int N>

@@ -73,3 +73,27 @@ def _listing(path: str) -> str:
 def test_operators(source):
     loads, m0, base = hazards(_listing(os.path.join(b.CSRC_OPS, source)))
     assert loads > 0 and not m0 and not base, (loads, len(m0), len(base))
+
+
+@pytest.mark.parametrize("source", ["gate_pack.hip", "up_blocked.hip", "bwd_blocked.hip"])
+def test_block(source):
+    loads, m0, base = hazards(_listing(os.path.join(b.CSRC, source)))
+    assert loads > 0 and not m0 and not base, (loads, len(m0), len(base))
+
+
+def test_backward_uses_none_of_its_header():
+    assert hazards(_listing(os.path.join(b.CSRC, "bwd.hip")))[0] == 0
+
+
+def test_every_source_with_such_loads_is_listed():
+    """Sources that reach the statement, directly or through a header."""
+    def reaches(path):
+        text = open(path).read()
+        if re.search(r"\bdma_16B\(", text.split("dma_16B(const void", 1)[-1] if path.endswith("twell_device.h") else text):
+            return True
+        return any(reaches(h) for inc in re.findall(r'#include "([^"]+)"', text)
+                   if os.path.exists(h := os.path.join(os.path.dirname(path), inc)) and not h.endswith("twell_device.h"))
+
+    found = {s for d, names in ((b.CSRC, b.SOURCES), (b.CSRC_OPS, b.OPS_SOURCES)) for s in names
+             if reaches(os.path.join(d, s))}
+    assert found == {"mx4_product.hip", "gate_pack.hip", "up_blocked.hip", "bwd_blocked.hip", "bwd.hip"}
