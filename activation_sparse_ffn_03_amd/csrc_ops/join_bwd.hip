@@ -1,0 +1,310 @@
+// Backward of the join. With xh = r' * rho, yh = y * rho_y (or y itself) and m
+// what dropout multiplies with (0 or one over the share that is kept):
+//
+//   G     = d_residual + rho * (d_out * w - xh * c)       c  = mean(d_out * w * xh)
+//   dr    = alpha * G
+//   dv    = G * gate * m
+//   dy    = rho_y * (dv * post_w - yh * c2)               c2 = mean(dv * post_w * yh)
+//   dw    = sum of d_out * xh,  dpost = sum of dv * yh,  dgate = sum of G * m * yh * post_w over the rows that share it
+//
+// (without the norm behind the block dy = dv and dgate sums G * m * y). c2 needs
+// G, which needs c: it is taken apart into sums that do not,
+//   sum(dv post_w yh) = sum((d_residual + rho d_out w) k yh) - rho c sum(xh k yh),  k = gate m post_w,
+// so that a row is reduced once, three sums at a time.
+//
+// Bound by memory: one pass over d_out, d_residual, r' and y. A workgroup takes
+// rows that share one row of the gate, or all rows of several rows of it, keeps
+// its sums in registers (thread t owns the same columns in every row) and leaves
+// partial rows; a second launch adds them in a fixed order.
+#include "counter_rng.h"
+#include "ops_kernels.h"
+#include "../csrc/twell_trace.h"
+
+namespace twell {
+namespace {
+
+// Eight elements of either type (uniform over the launch).
+struct RawAny {
+  u32x4_t v[2];
+  template <int KIND>
+  __device__ __forceinline__ void load(const void* base, int is_bf16, int64_t off, int i, int cols) {
+    if (is_bf16) {
+      Raw8<uint16_t> r;
+      r.load<KIND>(static_cast<const uint16_t*>(base) + off, i, cols);
+      v[0] = r.v;
+    } else {
+      Raw8<float> r;
+      r.load<KIND>(static_cast<const float*>(base) + off, i, cols);
+      v[0] = r.v[0];
+      v[1] = r.v[1];
+    }
+  }
+  __device__ __forceinline__ float get(int k, int is_bf16) const {
+    const uint32_t b = k & 1 ? v[0][k >> 1] & 0xFFFF0000u : v[0][k >> 1] << 16;
+    return __uint_as_float(is_bf16 ? b : v[k >> 2][k & 3]);
+  }
+};
+
+// EACH: every row has a gate of its own, which is loaded with the row.
+template <typename TR, typename TY, int NT, int T, int C, int KIND, bool EACH>
+__global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdArgs a, int parts) {
+  constexpr int ROWS = NT / T;        // rows a workgroup takes at a time
+  constexpr int G = T < 64 ? T : 64;  // lanes of a wave that share a row
+  constexpr int WPR = T / G;          // waves of a row
+  const int wave = threadIdx.x >> 6, t = threadIdx.x % T, side = threadIdx.x / T;
+  const int cols = a.cols, b = blockIdx.x;
+  const bool has_stream = a.d_residual != nullptr, has_post = a.post_w != nullptr, has_gate = a.gate != nullptr;
+  const bool drops = a.drop != 0;
+
+  struct Row {
+    Raw8<TR> r[C], s[C];
+    Raw8<TY> y[C];
+    RawAny g[C], gate[EACH ? C : 1];
+    float rho, rho_y;
+  };
+  auto fetch = [&](int64_t row, Row& x) {
+    const int64_t off = row * cols;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      x.r[c].template load<KIND>(static_cast<const TR*>(a.residual) + off, t + T * c, cols);
+      x.y[c].template load<KIND>(static_cast<const TY*>(a.y) + off, t + T * c, cols);
+      x.g[c].template load<KIND>(a.d_out, a.g_bf16, off, t + T * c, cols);
+      if constexpr (EACH) x.gate[c].template load<KIND>(a.gate, a.gate_bf16, off, t + T * c, cols);
+    }
+    if (has_stream) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) x.s[c].template load<KIND>(static_cast<const TR*>(a.d_residual) + off, t + T * c, cols);
+    }
+    x.rho = a.rstd[row];
+    x.rho_y = has_post ? a.post_rstd[row] : 1.f;
+  };
+
+  float w[C][8], post[C][8], gate[EACH ? 1 : C][8];
+  load_weight<T, C, KIND>(a.w, a.w_bf16, t, cols, w);
+  if (has_post) {
+    load_weight<T, C, KIND>(a.post_w, a.post_bf16, t, cols, post);
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) post[c][k] = 1.f;
+  }
+  float dw[C][8], dpost[C][8], dgate[C][8];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dw[c][k] = dpost[c][k] = dgate[c][k] = 0.f;
+
+  // The sums of the rows taken side by side, added in their order, to `to`.
+  __shared__ float acc[ROWS > 1 ? ROWS : 1][ROWS > 1 ? 8 : 1][ROWS > 1 ? T : 1];
+  static_assert(ROWS == 1 || C == 1, "rows side by side have one chunk a thread");
+  auto put = [&](float (&sum)[C][8], float* to) {
+    if constexpr (ROWS > 1) {
+      __syncthreads();  // what was put before has been read
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[side][k][t] = sum[0][k];
+      __syncthreads();
+      if (side > 0) return;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        for (int i = 1; i < ROWS; ++i) sum[0][k] += acc[i][k][t];
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) store8<KIND>(to, t + T * c, cols, sum[c]);
+  };
+
+  const DropArgs drop_args{a.rng, a.site, a.drop, a.drop_scale};
+  DropBits bits = drops ? DropBits(drop_args) : DropBits();
+  __shared__ float red[2][3][ROWS][WPR];
+  int flip = 0;
+  constexpr bool AHEAD = C == 1;
+
+  // Rows of the gate of this workgroup; with EACH rows are dealt as they are.
+  const int64_t per = EACH ? a.rows : a.rows / a.gates;
+  const int64_t gates = EACH ? 1 : a.gates;
+  const bool shared = EACH || parts > 1;  // several workgroups for one row of the gate
+  const int n = EACH ? (int)gridDim.x : parts;
+  const int64_t first_gate = shared ? b / n : b * gates / gridDim.x;
+  const int64_t end_gate = shared ? first_gate + 1 : (b + 1) * gates / gridDim.x;
+  const int64_t slice = shared ? b % n : 0, slices = shared ? n : 1;
+  for (int64_t gr = first_gate; gr < end_gate; ++gr) {
+    const int64_t r0 = gr * per + slice * per / slices, r1 = gr * per + (slice + 1) * per / slices;
+    int64_t row = r0 + side;
+    Row now, next;
+    if (AHEAD && row < r1) fetch(row, now);
+    if constexpr (!EACH) {
+      if (has_gate) {
+        load_weight<T, C, KIND>(static_cast<const char*>(a.gate) + gr * cols * (a.gate_bf16 ? 2 : 4), a.gate_bf16, t,
+                                cols, gate);
+      } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) gate[c][k] = 1.f;
+      }
+    }
+    for (int64_t first = r0; first < r1; first += ROWS, row += ROWS) {  // the same number of times in every wave
+      const bool here = row < r1;
+      if constexpr (AHEAD) {
+        if (row + ROWS < r1) fetch(row + ROWS, next);
+      } else if (here) {
+        fetch(row, now);
+      }
+      uint32_t keep[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) keep[c] = drops ? bits.template chunk<KIND>((uint32_t)row, t + T * c, cols) : 0xFFu;
+      auto gate_at = [&](int c, int k) {
+        if constexpr (EACH) return now.gate[c].get(k, a.gate_bf16);
+        else return gate[c][k];
+      };
+      float s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float xh = now.r[c].get(k) * now.rho, g = now.g[c].get(k, a.g_bf16), u = g * w[c][k];
+          if (here) dw[c][k] = fmaf(g, xh, dw[c][k]);
+          const bool counts = chunk_counts<KIND>(t + T * c, k, cols);
+          if (counts) s1 = fmaf(u, xh, s1);
+          if (has_post && counts) {
+            float base = now.rho * u;
+            if (has_stream) base += now.s[c].get(k);
+            const float kyh = keep[c] >> k & 1 ? gate_at(c, k) * a.drop_scale * post[c][k] * (now.y[c].get(k) * now.rho_y) : 0.f;
+            s2 = fmaf(base, kyh, s2);
+            s3 = fmaf(xh, kyh, s3);
+          }
+        }
+      s1 = group_sum<G>(s1);
+      if (has_post) {
+        s2 = group_sum<G>(s2);
+        s3 = group_sum<G>(s3);
+      }
+      if constexpr (WPR > 1) {
+        // two buffers: a wave may write the next row's sums while another still
+        // reads this row's
+        if ((threadIdx.x & 63) == 0) {
+          red[flip][0][side][wave % WPR] = s1;
+          red[flip][1][side][wave % WPR] = s2;
+          red[flip][2][side][wave % WPR] = s3;
+        }
+        lds_barrier();
+        s1 = s2 = s3 = 0.f;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) {
+          s1 += red[flip][0][side][i];
+          s2 += red[flip][1][side][i];
+          s3 += red[flip][2][side][i];
+        }
+        flip ^= 1;
+      }
+      const float c1 = s1 / (float)cols, c2 = (s2 - now.rho * c1 * s3) / (float)cols;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float dr[8], dy[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float xh = now.r[c].get(k) * now.rho;
+          float d = now.rho * (now.g[c].get(k, a.g_bf16) * w[c][k] - xh * c1);
+          if (has_stream) d += now.s[c].get(k);
+          dr[k] = a.alpha * d;
+          const float yh = now.y[c].get(k) * now.rho_y;  // y itself without the norm: rho_y is 1 then
+          const bool kept = keep[c] >> k & 1;
+          const float dm = kept ? d * a.drop_scale : 0.f, dv = dm * gate_at(c, k);
+          const float u = kept ? yh * post[c][k] : 0.f;
+          if constexpr (EACH) {
+            dgate[c][k] = dm * u;
+          } else {
+            if (here) dgate[c][k] = fmaf(dm, u, dgate[c][k]);
+          }
+          if (has_post) {
+            if (here) dpost[c][k] = fmaf(dv, yh, dpost[c][k]);
+            dy[k] = now.rho_y * (dv * post[c][k] - yh * c2);
+          } else {
+            dy[k] = dv;
+          }
+        }
+        if (here) {
+          store8<KIND>(static_cast<TR*>(a.dr) + row * cols, t + T * c, cols, dr);
+          store8<KIND>(static_cast<TY*>(a.dy) + row * cols, t + T * c, cols, dy);
+          if constexpr (EACH) store8<KIND>(a.dgate + row * cols, t + T * c, cols, dgate[c]);
+        }
+      }
+      if constexpr (AHEAD) now = next;
+    }
+    if (!EACH && has_gate) {
+      const bool part = parts > 1;
+      put(dgate, part ? a.part + ((int64_t)gridDim.x * (has_post ? 2 : 1) + b) * cols : a.dgate + gr * cols);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dgate[c][k] = 0.f;
+    }
+  }
+  const bool alone = gridDim.x == 1;
+  put(dw, alone ? a.dw : a.part + (int64_t)b * cols);
+  if (has_post) put(dpost, alone ? a.dpost : a.part + ((int64_t)gridDim.x + b) * cols);
+}
+
+// Sums of partial rows: a workgroup takes 64 columns of one of them, each of its
+// 16 waves every 16th row in ascending order, then the 16 sums in order. Sum 0 is
+// dw, then dpost if it is there, then the rows of the gate, `parts` rows each.
+__global__ __launch_bounds__(1024) void join_bwd_sum(JoinBwdArgs a, int groups, int parts) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane, whole = a.post_w != nullptr ? 2 : 1, which = blockIdx.y;
+  const int rows = which < whole ? groups : parts;
+  const float* part = a.part + (which < whole ? (int64_t)which * groups : (int64_t)whole * groups + (int64_t)(which - whole) * parts) * a.cols;
+  float* out = which == 0 ? a.dw : which < whole ? a.dpost : a.dgate + (int64_t)(which - whole) * a.cols;
+  float s = 0.f;
+  if (col < a.cols) {
+#pragma unroll 8
+    for (int g = wave; g < rows; g += 16) s += part[(int64_t)g * a.cols + col];
+  }
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && col < a.cols) {
+    for (int i = 1; i < 16; ++i) s += red[i][lane];
+    out[col] = s;
+  }
+}
+
+template <typename TR, typename TY, int NT, int T, int C>
+hipError_t launch_cfg(const JoinBwdArgs& a, hipStream_t s) {
+  const JoinBwdPlan p = join_bwd_plan(a.rows, a.cols, a.gates);
+  const bool each = a.gate != nullptr && a.gates == a.rows && a.rows > 1;
+  row_kind(a.cols, [&](auto kind) {
+    constexpr int KIND = decltype(kind)::value;
+    if constexpr (KIND != ROWS_SHORT || T == 16) {
+      if (each)
+        TWELL_LAUNCH("join_rms_norm_bwd", (join_bwd_kernel<TR, TY, NT, T, C, KIND, true>), dim3(p.groups), NT, 0, s, a, p.parts);
+      else
+        TWELL_LAUNCH("join_rms_norm_bwd", (join_bwd_kernel<TR, TY, NT, T, C, KIND, false>), dim3(p.groups), NT, 0, s, a, p.parts);
+    }
+  });
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.groups == 1) return e;
+  const int sums = (a.post_w != nullptr ? 2 : 1) + (a.gate != nullptr && p.parts > 1 ? (int)a.gates : 0);
+  TWELL_LAUNCH("join_bwd_sum", join_bwd_sum, dim3((a.cols + 63) / 64, sums), 1024, 0, s, a, p.groups, p.parts);
+  return hipGetLastError();
+}
+
+template <typename TR, typename TY>
+hipError_t launch_typed(const JoinBwdArgs& a, hipStream_t s) {
+  if (a.cols <= 128) return launch_cfg<TR, TY, 512, 16, 1>(a, s);
+  if (a.cols <= 256) return launch_cfg<TR, TY, 512, 32, 1>(a, s);
+  if (a.cols <= 512) return launch_cfg<TR, TY, 512, 64, 1>(a, s);
+  if (a.cols <= 1024) return launch_cfg<TR, TY, 512, 128, 1>(a, s);
+  if (a.cols <= 2048) return launch_cfg<TR, TY, 512, 256, 1>(a, s);
+  if (a.cols <= 4096) return launch_cfg<TR, TY, 512, 512, 1>(a, s);
+  if (a.cols <= 8192) return launch_cfg<TR, TY, 512, 512, 2>(a, s);
+  return launch_cfg<TR, TY, 512, 512, 4>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_join_rms_norm_bwd(const JoinBwdArgs& a, hipStream_t s) {
+  if (a.res_bf16) return a.y_bf16 ? launch_typed<uint16_t, uint16_t>(a, s) : launch_typed<uint16_t, float>(a, s);
+  return a.y_bf16 ? launch_typed<float, uint16_t>(a, s) : launch_typed<float, float>(a, s);
+}
+
+}  // namespace twell

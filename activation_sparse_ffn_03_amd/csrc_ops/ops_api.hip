@@ -1,40 +1,12 @@
 // C ABI of the operators around the block: host-side validation, then kernel
 // launches on the caller's stream. See include/twell.h for the contract of
 // every call.
-#include <cstdio>
-
-#include "../csrc/twell_host.h"
-#include "../csrc/twell_internal.h"
+#include "ops_check.h"
 #include "ops_kernels.h"
 
+using namespace twell::check;
+
 namespace {
-
-twell_status fail(twell_status st, const char* why) { return twell::set_error(st, why); }
-
-twell_status hip_status(hipError_t e, const char* where) {
-  if (e == hipSuccess) return TWELL_OK;
-  char why[256];  // no allocation, nothing to throw
-  std::snprintf(why, sizeof why, "%s: %s", where, hipGetErrorString(e));
-  return twell::set_error(TWELL_ERR_HIP, why);
-}
-
-twell_status ok() {
-  twell::set_error(TWELL_OK, "");
-  return TWELL_OK;
-}
-
-bool bad_dtype(twell_dtype t) { return t != TWELL_BF16 && t != TWELL_F32; }
-size_t size_of(twell_dtype t) { return t == TWELL_BF16 ? 2 : 4; }
-
-#define OPS_CHECK_PTR(p, bytes, name)                                                            \
-  do {                                                                                           \
-    if (twell::bad_ptr((p), (bytes)))                                                            \
-      return fail(TWELL_ERR_INVALID_ARG, name " is NULL or not 16-byte aligned");                \
-  } while (0)
-#define OPS_CHECK_OPT(p, bytes, name)                                                            \
-  do {                                                                                           \
-    if ((p) != nullptr) OPS_CHECK_PTR(p, bytes, name);                                           \
-  } while (0)
 
 twell_status check_norm_shape(int64_t rows, int32_t cols) {
   if (rows < 0 || cols <= 0) return fail(TWELL_ERR_INVALID_ARG, "rows must be >= 0 and cols > 0");
@@ -121,12 +93,6 @@ twell_status product_ws(int64_t n, int32_t cols, int32_t units, bool quantise, s
   if (ws_bytes == nullptr) return fail(TWELL_ERR_INVALID_ARG, "ws_bytes is NULL");
   *ws_bytes = n == 0 ? 0 : product_layout(twell::mx4_plan(n, cols, units, !quantise), n, cols, units, quantise).total;
   twell::set_error(TWELL_OK, "");
-  return TWELL_OK;
-}
-
-twell_status check_ws(void* ws, size_t have, size_t need, const char* small) {
-  if (have < need) return fail(TWELL_ERR_WORKSPACE, small);
-  if (twell::bad_ptr(ws, need)) return fail(TWELL_ERR_WORKSPACE, "workspace is NULL or not 16-byte aligned");
   return TWELL_OK;
 }
 

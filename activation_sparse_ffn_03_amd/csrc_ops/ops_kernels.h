@@ -54,6 +54,102 @@ inline int norm_bwd_groups(int64_t rows, int cols) {
 }
 hipError_t launch_add_rms_norm_bwd(const NormBwdArgs& a, hipStream_t s);
 
+// The join of a block's output to the stream.
+struct JoinArgs {
+  int64_t rows;
+  int cols;
+  int res_bf16, y_bf16, w_bf16, post_bf16, gate_bf16, out_bf16;
+  const void* residual;  // [rows][cols]
+  const void* y;         // [rows][cols]
+  const void* w;         // [cols]
+  const void* post_w;    // [cols] or null: no norm behind the block
+  const void* gate;      // [rows / per_gate][cols] or null
+  uint32_t per_gate;     // rows that share a row of the gate
+  int64_t first_row;     // number of row 0 in the whole array (a launch may hold a part of it)
+  float alpha, eps;
+  const uint64_t* rng;   // seed and step
+  uint32_t site, drop;
+  float drop_scale;
+  void* residual_out;    // [rows][cols] or null; may be `residual` itself
+  void* out;             // [rows][cols] or null
+  uint8_t* q;            // [rows][cols] or null
+  float* q_scale;        // [rows], with q
+  float* rstd;           // [rows] or null
+  float* post_rstd;      // [rows] or null
+};
+hipError_t launch_join_rms_norm(const JoinArgs& a, hipStream_t s);
+
+struct JoinBwdArgs {
+  int64_t rows;
+  int cols;
+  int g_bf16, res_bf16, y_bf16, w_bf16, post_bf16, gate_bf16;
+  const void* d_out;       // [rows][cols]
+  const void* d_residual;  // [rows][cols], type of the residual, or null
+  const void* residual;    // [rows][cols], the new stream
+  const float* rstd;       // [rows]
+  const void* y;           // [rows][cols]
+  const float* post_rstd;  // [rows], with post_w
+  const void* w;           // [cols]
+  const void* post_w;      // [cols] or null
+  const void* gate;        // [gates][cols] or null
+  uint32_t gates;          // 1 without a gate
+  float alpha;
+  const uint64_t* rng;
+  uint32_t site, drop;
+  float drop_scale;
+  void* dr;                // [rows][cols], type of the residual
+  void* dy;                // [rows][cols], type of y
+  float* dw;               // [cols]
+  float* dpost;            // [cols], with post_w
+  float* dgate;            // [gates][cols], with gate
+  float* part;             // workspace: join_bwd_ws_floats
+};
+// How the rows are dealt to workgroups: `parts` workgroups for each row of the
+// gate, or several whole rows of the gate to a workgroup when there are more of
+// them than workgroups wanted.
+constexpr int kJoinBwdGroups = 256;
+inline int join_bwd_side(int cols) {  // rows that a workgroup takes side by side
+  return cols <= 128 ? 32 : cols <= 256 ? 16 : cols <= 512 ? 8 : cols <= 1024 ? 4 : cols <= 2048 ? 2 : 1;
+}
+struct JoinBwdPlan {
+  int groups;  // workgroups: gates * parts, or fewer than the gates
+  int parts;   // of a row of the gate's rows; 1 where a workgroup takes several
+};
+inline JoinBwdPlan join_bwd_plan(int64_t rows, int cols, uint32_t gates) {
+  if (rows == 0) return {1, 1};
+  if (gates == rows) {  // a gate a row (or one row): nothing is summed for it, and rows are dealt as without one
+    const int64_t need = (rows + join_bwd_side(cols) - 1) / join_bwd_side(cols);
+    return {(int)(need < kJoinBwdGroups ? need : kJoinBwdGroups), 1};
+  }
+  if (gates >= (uint32_t)kJoinBwdGroups) return {kJoinBwdGroups, 1};
+  const int64_t per = rows / gates, need = (per + join_bwd_side(cols) - 1) / join_bwd_side(cols);
+  const int most = kJoinBwdGroups / (int)gates;
+  const int parts = (int)(need < most ? need : most);
+  return {(int)gates * parts, parts};
+}
+// Partial rows: dw and dpost of every workgroup (unless there is one), and the
+// gate's where several workgroups share a row of it.
+inline size_t join_bwd_ws_floats(int64_t rows, int cols, uint32_t gates, bool post, bool gate) {
+  const JoinBwdPlan p = join_bwd_plan(rows, cols, gates);
+  const size_t sums = p.groups > 1 ? (size_t)p.groups * (post ? 2 : 1) : 0;
+  return (sums + (gate && p.parts > 1 ? p.groups : 0)) * (size_t)cols;
+}
+hipError_t launch_join_rms_norm_bwd(const JoinBwdArgs& a, hipStream_t s);
+
+constexpr int kDropoutMaxCols = 1 << 30;
+struct DropoutArgs {
+  int64_t rows;
+  int cols;
+  uint32_t first_row;  // number of row 0 in the whole array
+  int bf16;
+  const void* x;  // [rows][cols]
+  void* out;      // the same type; may be x
+  const uint64_t* rng;
+  uint32_t site, drop;
+  float drop_scale;
+};
+hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s);
+
 // MX4 rows: 64 bytes of codes for every 128 columns begun, 16 scale bytes for
 // every 512 begun.
 constexpr int kMx4MaxCols = 1 << 20;

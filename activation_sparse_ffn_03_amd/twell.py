@@ -35,7 +35,8 @@ EXPORTS = ("twell_status_str", "twell_last_error", "twell_n_tiles", "twell_query
            "twell_ffn_forward_noalloc", "twell_route_hybrid", "twell_ffn_bwd", "twell_add_rms_norm",
            "twell_add_rms_norm_bwd_ws", "twell_add_rms_norm_bwd", "twell_mx4_sizes", "twell_quantize_mx4",
            "twell_dequantize_mx4", "twell_matmul_mx4_ws", "twell_matmul_mx4", "twell_linear_mx4_ws",
-           "twell_linear_mx4", "twell_trace_start",
+           "twell_linear_mx4", "twell_dropout", "twell_join_rms_norm", "twell_join_rms_norm_bwd_ws",
+           "twell_join_rms_norm_bwd", "twell_trace_start",
            "twell_trace_stop", "twell_trace_count", "twell_trace_dropped", "twell_trace_get")
 
 # Bytes of the library's static scratch used by twell_ffn_forward_noalloc.
@@ -63,6 +64,12 @@ class Hybrid(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("ell_vals", "ell_cols", "ell_a", "row_nnz", "is_dense", "dense_rows", "dense_h", "n_dense",
                  "status")]
+
+
+class Join(ctypes.Structure):
+    _fields_ = [("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("rng", ctypes.c_void_p),
+                ("gate_rows", ctypes.c_int64), ("alpha", ctypes.c_float), ("p", ctypes.c_float),
+                ("site", ctypes.c_uint32), ("post_weight_dtype", ctypes.c_int), ("gate_dtype", ctypes.c_int)]
 
 
 _SIZE_FIELDS = ("vals", "cols", "counts", "ovf_flag", "ovf_rows", "ovf_h", "n_ovf", "status", "ell_vals",
@@ -142,6 +149,17 @@ def lib() -> ctypes.CDLL:
         L.twell_linear_mx4_ws.argtypes = [i64, i32, i32, psz]
         L.twell_linear_mx4.restype = ctypes.c_int
         L.twell_linear_mx4.argtypes = [i64, i32, i32, ctypes.c_int, vp, vp, vp, ctypes.c_int, vp, vp, sz, vp]
+        u32, pj = ctypes.c_uint32, ctypes.POINTER(Join)
+        L.twell_dropout.restype = ctypes.c_int
+        L.twell_dropout.argtypes = [i64, i32, ctypes.c_int, vp, f32, vp, u32, vp, vp]
+        L.twell_join_rms_norm.restype = ctypes.c_int
+        L.twell_join_rms_norm.argtypes = [i64, i32, ctypes.c_int, vp, ctypes.c_int, vp, ctypes.c_int, vp, pj, f32, vp,
+                                          ctypes.c_int, vp, vp, vp, vp, vp, vp]
+        L.twell_join_rms_norm_bwd_ws.restype = ctypes.c_int
+        L.twell_join_rms_norm_bwd_ws.argtypes = [i64, i32, i32, i64, psz]
+        L.twell_join_rms_norm_bwd.restype = ctypes.c_int
+        L.twell_join_rms_norm_bwd.argtypes = [i64, i32, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp, ctypes.c_int, vp, vp,
+                                              ctypes.c_int, vp, pj, vp, vp, vp, vp, vp, vp, sz, vp]
         L.twell_trace_start.restype = ctypes.c_int
         L.twell_trace_start.argtypes = [i32]
         L.twell_trace_stop.restype = ctypes.c_int
@@ -662,6 +680,176 @@ def linear_mx4(x, w_codes, w_scales, dtype=torch.bfloat16, out=None, ws=None, st
     at, nbytes, _keep = _workspace(ws, ws is None and linear_mx4_ws(n, cols, units), x, stream)
     _call(lib().twell_linear_mx4, dev, stream, n, cols, units, *args, _code(out, "out"),
           _addr(out, "out", (n, units), None, dev), at, nbytes)
+    return out
+
+
+# ---------------------------------------------------------------- from a block's output to the next block's input
+
+
+def make_rng(seed: int, step: int = 0, device="cuda") -> torch.Tensor:
+    """The generator's state that dropout takes: an int64 tensor of seed and step on the GPU. Advance the step
+    (rng[1] += 1) for each training step; a captured step may do so itself."""
+    return torch.tensor([seed, step], dtype=torch.int64, device=device)
+
+
+def _site(site: int) -> int:
+    if not 0 <= site < 1 << 32:
+        raise ValueError("site must be from 0 to 2^32 - 1")
+    return site
+
+
+def dropout(x, rng, p: float, site: int = 0, out=None, stream=None):
+    """x with a share p of its elements dropped and the others divided by the share that is kept (twell_dropout), in the
+    type of x [rows, cols], bf16 or fp32; written into `out` when given, which may be x. The mask depends on rng (int64
+    [2] on the GPU: seed and step, see make_rng), site, row and column alone: the gradient of the call is the same call
+    on the gradient."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    shape = x.shape
+    rows, cols = shape
+    if cols > _INT32:
+        _too_large("twell_dropout", cols)
+    dt, dev = _code(x, "x"), x.get_device()
+    src = _addr(x, "x", shape)
+    if out is None:
+        out = _new(stream, lambda: torch.empty_like(x))
+    _call(lib().twell_dropout, dev, stream, rows, cols, dt, src, p, _addr(rng, "rng", (2,), torch.int64, dev), _site(site),
+          _addr(out, "out", shape, x.dtype, dev))
+    return out
+
+
+class JoinOut(NamedTuple):
+    """What join_rms_norm puts out; fields that were not asked for are None."""
+    residual: Optional[torch.Tensor]   # [rows, cols] r', dtype of the residual
+    out: Optional[torch.Tensor]        # [rows, cols] the norm of it
+    codes: Optional[torch.Tensor]      # [rows, cols] uint8 E4M3 codes of the norm
+    scale: Optional[torch.Tensor]      # [rows] fp32 scales of the codes
+    rstd: Optional[torch.Tensor]       # [rows] fp32, for the backward
+    post_rstd: Optional[torch.Tensor]  # [rows] fp32, that of the norm behind the block
+
+
+def alloc_join(residual: torch.Tensor, out_dtype=None, codes: bool = False, stats: bool = False, post: bool = False) -> JoinOut:
+    """Output buffers of join_rms_norm for a [rows, cols] residual; stats for the backward, post with a norm behind the
+    block."""
+    n = alloc_norm(residual, out_dtype, codes, stats)
+    return JoinOut(*n, torch.empty_like(n.rstd) if stats and post else None)
+
+
+def _join(shape, dev, post_weight, gate, alpha, p, rng, site) -> Join:
+    """The library's struct of what lies between a block's output and the stream, checked."""
+    j = Join(alpha=alpha, p=p, site=_site(site))
+    if post_weight is not None:
+        j.post_weight = _addr(post_weight, "post_weight", shape[1:], None, dev)
+        j.post_weight_dtype = _code(post_weight, "post_weight")
+    if gate is not None:
+        if gate.dim() not in (1, 2):
+            raise ValueError("gate must be [cols] or [gate rows, cols]")
+        j.gate_rows = 1 if gate.dim() == 1 else gate.shape[0]
+        j.gate = _addr(gate, "gate", gate.shape[:-1] + shape[1:], None, dev)
+        j.gate_dtype = _code(gate, "gate")
+        if j.gate is None or shape[0] % j.gate_rows:
+            raise ValueError(f"gate must have a number of rows that divides {shape[0]}, has {j.gate_rows}")
+    if p != 0 and rng is None:
+        raise ValueError("dropout needs rng")
+    if p != 0:
+        j.rng = _addr(rng, "rng", (2,), torch.int64, dev)
+    return j
+
+
+def join_rms_norm(residual, y, weight, post_weight=None, gate=None, alpha: float = 1.0, eps: float = 1e-6, p: float = 0.0,
+                  rng=None, site: int = 0, out_dtype=None, codes: bool = False, stats: bool = False, out=None,
+                  stream=None) -> JoinOut:
+    """r' = alpha * residual + gate * dropout(norm(y) * post_weight), and the norm of r' times weight
+    (twell_join_rms_norm).
+
+    residual and y [rows, cols], weight [cols], each bf16 or fp32. post_weight [cols], or None: y is not normed; gate
+    [cols], or [gate rows, cols] where each serves rows / gate rows consecutive rows, or None; p, rng and site as in
+    dropout. Without `out` the new residual and the norm (out_dtype, default that of the residual) are returned, with
+    codes=True also its E4M3 codes and row scales, and with stats=True what join_rms_norm_bwd needs. `out`, a JoinOut or
+    six tensors in its order, each None where it is not wanted, says what to write and where; out.residual may be
+    `residual` itself."""
+    if residual.dim() != 2:
+        raise ValueError("residual must be [rows, cols]")
+    shape = residual.shape
+    rows, cols = shape
+    if cols > _INT32:
+        _too_large("twell_join_rms_norm", cols)
+    rc, dev = _code(residual, "residual"), residual.get_device()
+    if out is None:
+        out = _new(stream, lambda: alloc_join(residual, out_dtype, codes, stats, post_weight is not None))
+    elif not isinstance(out, JoinOut):
+        out = JoinOut(*out)
+    if (out.codes is None) != (out.scale is None):
+        raise ValueError("codes and scale go together")
+    row = shape[:1]
+    r = _addr(residual, "residual", shape)
+    j = _join(shape, dev, post_weight, gate, alpha, p, rng, site)
+    _call(
+        lib().twell_join_rms_norm, dev, stream, rows, cols, rc, r,
+        _code(y, "y"), _addr(y, "y", shape, None, dev), _code(weight, "weight"), _addr(weight, "weight", shape[1:], None, dev),
+        j, eps, _addr(out.residual, "out.residual", shape, residual.dtype, dev),
+        F32 if out.out is None else _code(out.out, "out.out"), _addr(out.out, "out.out", shape, None, dev),
+        _addr(out.codes, "out.codes", shape, torch.uint8, dev), _addr(out.scale, "out.scale", row, torch.float32, dev),
+        _addr(out.rstd, "out.rstd", row, torch.float32, dev), _addr(out.post_rstd, "out.post_rstd", row, torch.float32, dev))
+    return out
+
+
+class JoinGrads(NamedTuple):
+    """What join_rms_norm_bwd puts out; dpost and dgate are None without post_weight and gate."""
+    dr: torch.Tensor               # [rows, cols], dtype of the residual
+    dy: torch.Tensor               # [rows, cols], dtype of y
+    dw: torch.Tensor               # [cols] fp32
+    dpost: Optional[torch.Tensor]  # [cols] fp32
+    dgate: Optional[torch.Tensor]  # the gate's shape, fp32
+
+
+@functools.lru_cache(maxsize=256)
+def join_rms_norm_bwd_ws(rows: int, cols: int, post: bool, gate_rows: int) -> int:
+    """Workspace bytes of join_rms_norm_bwd; gate_rows is 0 without a gate."""
+    if cols > _INT32:
+        _too_large("twell_join_rms_norm_bwd_ws", cols)
+    n = ctypes.c_size_t()
+    _check(lib().twell_join_rms_norm_bwd_ws(rows, cols, int(post), gate_rows, ctypes.byref(n)), "twell_join_rms_norm_bwd_ws")
+    return n.value
+
+
+def join_rms_norm_bwd(d_out, residual, rstd, y, weight, post_weight=None, post_rstd=None, gate=None, alpha: float = 1.0,
+                      p: float = 0.0, rng=None, site: int = 0, d_residual=None, out=None, ws=None, stream=None) -> JoinGrads:
+    """Gradients of join_rms_norm (twell_join_rms_norm_bwd). residual, rstd and post_rstd are what the forward put out, y
+    and the options what it took (rng holding the same seed and step), d_out and d_residual the gradients of its norm
+    and of its new residual (None: nothing else reads that). Written into `out`, a JoinGrads, when given; ws (bytes of
+    join_rms_norm_bwd_ws) is allocated here when not."""
+    if residual.dim() != 2:
+        raise ValueError("residual must be [rows, cols]")
+    shape = residual.shape
+    rows, cols = shape
+    if cols > _INT32:
+        _too_large("twell_join_rms_norm_bwd", cols)
+    gc, rc, yc, wc = _code(d_out, "d_out"), _code(residual, "residual"), _code(y, "y"), _code(weight, "weight")
+    res, dev = _addr(residual, "residual", shape), residual.get_device()
+    j = _join(shape, dev, post_weight, gate, alpha, p, rng, site)
+    if post_weight is not None and post_rstd is None:
+        raise ValueError("post_weight needs post_rstd")
+    if out is None:
+        def make():
+            e = dict(dtype=torch.float32, device=residual.device)
+            return JoinGrads(torch.empty_like(residual), torch.empty_like(y), torch.empty(cols, **e),
+                             None if post_weight is None else torch.empty(cols, **e),
+                             None if gate is None else torch.empty(gate.shape, **e))
+        out = _new(stream, make)
+    elif not isinstance(out, JoinGrads):
+        out = JoinGrads(*out)
+    row, col, f32 = shape[:1], shape[1:], torch.float32
+    args = (rows, cols, gc, _addr(d_out, "d_out", shape, None, dev), rc,
+            _addr(d_residual, "d_residual", shape, residual.dtype, dev), res, _addr(rstd, "rstd", row, f32, dev), yc,
+            _addr(y, "y", shape, None, dev), None if post_weight is None else _addr(post_rstd, "post_rstd", row, f32, dev),
+            wc, _addr(weight, "weight", col, None, dev), j, _addr(out.dr, "dr", shape, residual.dtype, dev),
+            _addr(out.dy, "dy", shape, y.dtype, dev), _addr(out.dw, "dw", col, f32, dev),
+            _addr(out.dpost, "dpost", col, f32, dev),
+            None if gate is None else _addr(out.dgate, "dgate", gate.shape, f32, dev))
+    need = ws is None and join_rms_norm_bwd_ws(rows, cols, post_weight is not None, j.gate_rows)
+    at, n, _keep = _workspace(ws, need, residual, stream)
+    _call(lib().twell_join_rms_norm_bwd, dev, stream, *args, at, n)
     return out
 
 

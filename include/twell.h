@@ -432,6 +432,84 @@ twell_status twell_linear_mx4(int64_t n, int32_t cols, int32_t units, twell_dtyp
                               size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * From a block's output to the next block's input
+ * ------------------------------------------------------------------------- */
+
+/* Dropout from a counter-based generator: the mask is stored nowhere and made
+ * again wherever it is needed. With d = the integer nearest to 65536 p and B the
+ * Philox4x32-10 block (Salmon, Moraes, Dror, Shaw 2011) of
+ *   counter (col / 8, row, rng[1] mod 2^32, site), key rng[0] (low word first),
+ * taken as eight 16-bit numbers, the lower half of each word first, element
+ * (row, col) is dropped when number col % 8 is below d:
+ *   out = x * 65536 / (65536 - d) where it is kept (fp32, rounded once),
+ *   out = 0 where it is dropped, whatever x holds.
+ * rng: DEVICE [2] seed and step, 16-byte aligned. They are read when the kernel
+ * runs: a call recorded into a graph draws anew when the caller advances the
+ * step between replays. site tells apart the places of one network. The gradient
+ * is this call on the gradient, with the same p, rng and site.
+ * x, out: [rows][cols] bf16 or fp32; out may be x, otherwise they may not
+ * overlap. 0 <= p <= 1. Any cols from 1 to 2^30; rows == 0 is a no-op. */
+twell_status twell_dropout(int64_t rows, int32_t cols, twell_dtype dtype, const void* x, float p, const uint64_t* rng,
+                           uint32_t site, void* out, void* stream);
+
+/* What lies between a block's output and the stream. Host memory. */
+typedef struct twell_join {
+  const void* post_weight; /* [cols] weight of the norm behind the block, or NULL: no such norm */
+  const void* gate;        /* [gate_rows][cols] or NULL (then 1); row i of the stream uses row i / (rows / gate_rows) */
+  const uint64_t* rng;     /* DEVICE [2] seed and step of twell_dropout; NULL allowed when p rounds to 0 */
+  int64_t gate_rows;       /* divides rows: 1 a scale for each channel, a number of sequences, rows a gate for each token */
+  float alpha;             /* scale of the residual */
+  float p;                 /* dropped share of the normed output; 0: none */
+  uint32_t site;           /* as in twell_dropout */
+  twell_dtype post_weight_dtype, gate_dtype;
+} twell_join;
+
+/* The join of a block's output y to the residual stream, with norms before and
+ * after the block:
+ *   v    = y * rho_y * post_weight,  rho_y = 1 / sqrt(mean_k(y[i,k]^2) + eps)   (v = y without post_weight)
+ *   u    = dropout of v as in twell_dropout (rows and cols are those of the array)
+ *   r'   = alpha * residual + gate * u, fp32, rounded to res_dtype
+ *   rho  = 1 / sqrt(mean_k(r'[i,k]^2) + eps)
+ *   n    = r' * rho * weight
+ *   residual_out = r',  out = n rounded to out_dtype,  rstd = rho,  post_rstd = rho_y,
+ *   q and q_scale from n as in twell_add_rms_norm
+ * With alpha 1 and neither post_weight, gate nor dropout this is
+ * twell_add_rms_norm with delta = y, bit for bit. A row whose mean of squares is
+ * beyond fp32 has rho = 0 there, too. residual, y [rows][cols]; weight [cols].
+ * residual_out, out, q (with q_scale [rows]), rstd and post_rstd (with
+ * post_weight) may each be NULL, not all of them; residual_out may be
+ * `residual` itself, no other output may overlap an input. Any cols from 1 to
+ * 16384; rows == 0 is a no-op. */
+twell_status twell_join_rms_norm(int64_t rows, int32_t cols, twell_dtype res_dtype, const void* residual,
+                                 twell_dtype y_dtype, const void* y, twell_dtype weight_dtype, const void* weight,
+                                 const twell_join* join, float eps, void* residual_out, twell_dtype out_dtype,
+                                 void* out, uint8_t* q, float* q_scale, float* rstd, float* post_rstd, void* stream);
+
+/* Workspace bytes of twell_join_rms_norm_bwd (host-only query; may be 0): post
+ * says whether there is a post_weight, gate_rows is 0 without a gate. */
+twell_status twell_join_rms_norm_bwd_ws(int64_t rows, int32_t cols, int32_t post, int64_t gate_rows, size_t* ws_bytes);
+
+/* Backward of twell_join_rms_norm, from the stream it stored (r'), its rstd and
+ * post_rstd, y, and the same join (rng holding what it held then). With
+ * xh = r' * rho, yh = y * rho_y, m what dropout multiplies with:
+ *   G  = d_residual + rho * (d_out * weight - xh * mean_k(d_out * weight * xh))
+ *   dr = alpha * G
+ *   dv = G * gate * m
+ *   dy = rho_y * (dv * post_weight - yh * mean_k(dv * post_weight * yh))    (dy = dv without post_weight)
+ *   dw = sum_i d_out * xh,  dpost = sum_i dv * yh,  dgate[g] = sum over its rows of G * m * v
+ * dr is of res_dtype, dy of y_dtype; dw, dpost (with post_weight) [cols] and
+ * dgate (with gate) [gate_rows][cols] are fp32, summed in a fixed order. The
+ * codes have no gradient. d_residual may be NULL when nothing else reads the
+ * stream. All outputs are fully overwritten (rows == 0: the sums are 0); none may
+ * overlap an input. ws: at least the queried bytes. */
+twell_status twell_join_rms_norm_bwd(int64_t rows, int32_t cols, twell_dtype d_out_dtype, const void* d_out,
+                                     twell_dtype res_dtype, const void* d_residual, const void* residual,
+                                     const float* rstd, twell_dtype y_dtype, const void* y, const float* post_rstd,
+                                     twell_dtype weight_dtype, const void* weight, const twell_join* join, void* dr,
+                                     void* dy, float* dw, float* dpost, float* dgate, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/* ---------------------------------------------------------------------------
  * Tracing (diagnostics). When started, every kernel launched by the calls
  * above is bracketed by two HIP events recorded on the call's stream, so the
  * device time of each kernel can be read back afterwards. Events are created
