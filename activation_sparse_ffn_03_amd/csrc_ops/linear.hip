@@ -1,0 +1,171 @@
+// Around the linear layer's products: the order of their launches, the sums of
+// the splits of k, the gradient of the pre-activation with the bias's sums, and
+// copies with lines of whole 16 bytes. All of these are bound by memory.
+#include "linear_device.h"
+#include "../csrc/twell_trace.h"
+
+namespace twell {
+namespace {
+
+// Adds the splits' sums of eight neighbouring units in the splits' order, and
+// finishes them.
+template <int ACT>
+__global__ __launch_bounds__(256) void linear_join(LinearArgs a, int chunks) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / chunks;
+  if (row >= a.out.rows) return;
+  const int unit = 8 * (int)(i - row * chunks), have = a.out.units - unit;
+  const int64_t at = row * a.out.units + unit, plane = a.out.rows * a.out.units;
+  float bias[8], res[8], z[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) bias[k] = res[k] = 0.f;
+  if (a.out.bias != nullptr) load_some<8>(a.out.bias, a.out.bias_bf16, unit, have, bias);
+  if (a.out.residual != nullptr) load_some<8>(a.out.residual, a.out.res_bf16, at, have, res);
+  load_some<8>(a.part, 0, at, have, z);
+#pragma unroll 4
+  for (int s = 1; s < a.splits; ++s) {
+    float v[8];
+    load_some<8>(a.part, 0, s * plane + at, have, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) z[k] += v[k];
+  }
+  finish_units<ACT, 8>(a.out, row, unit, have, z, bias, res);
+}
+
+template <int ACT>
+hipError_t launch_join(const LinearArgs& a, hipStream_t s) {
+  const int chunks = (a.out.units + 7) / 8;
+  const dim3 grid((unsigned)((a.out.rows * chunks + 255) / 256));
+  TWELL_LAUNCH("linear_join", linear_join<ACT>, grid, 256, 0, s, a, chunks);
+  return hipGetLastError();
+}
+
+__global__ __launch_bounds__(256) void linear_pad_kernel(const uint16_t* __restrict__ in, int64_t rows, int cols,
+                                                         uint16_t* __restrict__ out, int64_t ld) {
+  const int chunks = (int)(ld / 8);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / chunks;
+  if (row >= rows) return;
+  const int col = 8 * (int)(i - row * chunks);
+  float v[8];
+  load_some<8>(in, 1, row * cols + col, cols - col, v);  // exact both ways
+  store_some<8>(out, 1, row * ld + col, 8, v);
+}
+
+// dz = d_out * act'(pre), and the sums of its columns over a run of rows: 64
+// threads side by side take 8 units each, four rows at a time.
+template <int ACT>
+__global__ __launch_bounds__(256) void linear_dz_kernel(LinearDzArgs a) {
+  const int t = threadIdx.x & 63, side = threadIdx.x >> 6;
+  const int unit = 8 * (blockIdx.x * 64 + t), have = a.units - unit;
+  const int64_t r0 = (int64_t)blockIdx.y * a.rows / gridDim.y, r1 = ((int64_t)blockIdx.y + 1) * a.rows / gridDim.y;
+  float sum[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sum[k] = 0.f;
+  if (have > 0) {
+#pragma unroll 2
+    for (int64_t row = r0 + side; row < r1; row += 4) {
+      const int64_t at = row * a.units + unit;
+      float g[8];
+      load_some<8>(a.d_out, a.g_bf16, at, have, g);
+      if constexpr (ACT != TWELL_ACT_NONE) {
+        float z[8];
+        load_some<8>(a.pre, 1, at, have, z);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] *= activate_slope<ACT>(z[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += g[k];
+      if (a.dz != nullptr) store_some<8>(a.dz, 1, row * a.ld + unit, 8, g);  // zeros behind the last unit
+    }
+  }
+  if (a.db == nullptr) return;
+  __shared__ float acc[4][8][64];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) acc[side][k][t] = sum[k];
+  __syncthreads();
+  if (side > 0 || have <= 0) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    for (int i = 1; i < 4; ++i) sum[k] += acc[i][k][t];
+  store_some<8>(gridDim.y == 1 ? a.db : a.part + (int64_t)blockIdx.y * a.units, 0, unit, have, sum);
+}
+
+// db[u] = sum over the partial rows, in their order.
+__global__ __launch_bounds__(256) void linear_db_sum(const float* __restrict__ part, int parts, int units,
+                                                     float* __restrict__ db) {
+  const int u = blockIdx.x * 256 + threadIdx.x;
+  if (u >= units) return;
+  float s = 0.f;
+#pragma unroll 8
+  for (int p = 0; p < parts; ++p) s += part[(int64_t)p * units + u];
+  db[u] = s;
+}
+
+template <int ACT>
+hipError_t launch_dz(const LinearDzArgs& a, hipStream_t s) {
+  const int parts = linear_db_parts(a.rows);
+  TWELL_LAUNCH("linear_dz", linear_dz_kernel<ACT>, dim3((a.units + 511) / 512, parts), 256, 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.db == nullptr || parts == 1) return e;
+  TWELL_LAUNCH("linear_db_sum", linear_db_sum, dim3((a.units + 255) / 256), 256, 0, s, a.part, parts, a.units, a.db);
+  return hipGetLastError();
+}
+
+__global__ __launch_bounds__(256) void linear_zero(LinearOut o, int chunks) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / chunks;
+  if (row >= o.rows) return;
+  const int unit = 8 * (int)(i - row * chunks);
+  const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  store_some<8>(o.y, o.y_bf16, row * o.units + unit, o.units - unit, z);
+}
+
+}  // namespace
+
+hipError_t launch_linear_zero(const LinearOut& o, hipStream_t s) {
+  const int chunks = (o.units + 7) / 8;
+  TWELL_LAUNCH("linear_zero", linear_zero, dim3((unsigned)((o.rows * chunks + 255) / 256)), 256, 0, s, o, chunks);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_join(const LinearArgs& a, hipStream_t s) {
+  switch (a.out.act) {
+    case TWELL_ACT_RELU: return launch_join<TWELL_ACT_RELU>(a, s);
+    case TWELL_ACT_SILU: return launch_join<TWELL_ACT_SILU>(a, s);
+    case TWELL_ACT_GELU: return launch_join<TWELL_ACT_GELU>(a, s);
+    default: return launch_join<TWELL_ACT_NONE>(a, s);
+  }
+}
+
+hipError_t launch_linear_pad(const void* in, int64_t rows, int cols, void* out, int64_t ld, hipStream_t s) {
+  const dim3 grid((unsigned)((rows * (ld / 8) + 255) / 256));
+  TWELL_LAUNCH("linear_pad", linear_pad_kernel, grid, 256, 0, s, static_cast<const uint16_t*>(in), rows, cols,
+               static_cast<uint16_t*>(out), ld);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_dz(const LinearDzArgs& a, hipStream_t s) {
+  switch (a.act) {
+    case TWELL_ACT_RELU: return launch_dz<TWELL_ACT_RELU>(a, s);
+    case TWELL_ACT_SILU: return launch_dz<TWELL_ACT_SILU>(a, s);
+    case TWELL_ACT_GELU: return launch_dz<TWELL_ACT_GELU>(a, s);
+    default: return launch_dz<TWELL_ACT_NONE>(a, s);
+  }
+}
+
+hipError_t launch_linear(LinearLayout layout, const LinearPlan& plan, const LinearArgs& all, hipStream_t s) {
+  LinearArgs a = all;
+  a.splits = plan.splits;
+  if (plan.tile == 0) return launch_linear_direct(a, s);
+  LinearArgs first = a;
+  if (a.splits > 1) {  // the sums alone; linear_join finishes them
+    first.out.bias = nullptr;
+    first.out.residual = nullptr;
+    first.out.pre = nullptr;
+    first.out.act = TWELL_ACT_NONE;
+  }
+  const hipError_t e = layout == LINEAR_ROWS    ? launch_linear_rows(plan.tile, first, s)
+                       : layout == LINEAR_MIXED ? launch_linear_mixed(plan.tile, first, s)
+                                                : launch_linear_cols(plan.tile, first, s);
+  return e != hipSuccess || a.splits == 1 ? e : launch_linear_join(a, s);
+}
+
+}  // namespace twell

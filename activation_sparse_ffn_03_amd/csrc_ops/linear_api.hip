@@ -1,0 +1,225 @@
+// C ABI of the linear layer and its backward: host-side validation, workspaces,
+// then the launches in their order on the caller's stream. See include/twell.h
+// for the contract of every call.
+#include "ops_check.h"
+#include "ops_kernels.h"
+
+using namespace twell::check;
+using twell::LinearLayout;
+using twell::LinearPlan;
+
+namespace {
+
+twell_status check_dims(int64_t n, int32_t cols, int32_t units) {
+  if (n < 0 || cols <= 0 || units <= 0) return fail(TWELL_ERR_INVALID_ARG, "n must be >= 0, cols and units > 0");
+  if (cols > twell::kLinearMaxCols || units > twell::kLinearMaxCols)
+    return fail(TWELL_ERR_UNSUPPORTED, "cols or units above 2^20");
+  // one launch of 256 threads a workgroup, each thread 8 elements of a row, less than 2^32 threads
+  const int64_t widest = ((cols > units ? cols : units) + 7) / 8;
+  if (n > 0x7FFFFFFFll || n * widest >= (1ll << 32) - 256)
+    return fail(TWELL_ERR_UNSUPPORTED, "2^32 pieces of 8 elements or more");
+  return TWELL_OK;
+}
+
+bool bad_act(int32_t a) { return (unsigned)a > (unsigned)TWELL_ACT_GELU; }
+
+// Pieces of the workspace, each on 256 bytes.
+struct Pieces {
+  size_t total = 0;
+  size_t take(size_t bytes) {
+    const size_t at = total;
+    total += (bytes + 255) / 256 * 256;
+    return at;
+  }
+};
+
+// twell_linear: x and w with padded lines where tiles need them, the splits' sums.
+struct ForwardLayout {
+  LinearPlan plan;
+  bool pad;
+  size_t x, w, part, total;
+};
+ForwardLayout forward_layout(int64_t n, int32_t cols, int32_t units) {
+  ForwardLayout L{};
+  L.plan = twell::linear_plan(twell::LINEAR_ROWS, n, cols, units);
+  L.pad = L.plan.tile != 0 && cols % 8 != 0;
+  const size_t ld = (size_t)twell::linear_pad(cols);
+  Pieces p;
+  L.x = p.take(L.pad ? (size_t)n * ld * 2 : 0);
+  L.w = p.take(L.pad ? (size_t)units * ld * 2 : 0);
+  L.part = p.take(twell::linear_part_bytes(L.plan, n, units));
+  L.total = n == 0 ? 0 : p.total;
+  return L;
+}
+
+// twell_linear_bwd: dz (unless d_out is it), x or w with padded lines, the
+// bias's partial sums, and the splits' sums of the two products, one after the
+// other in the same place.
+struct BackwardLayout {
+  LinearPlan dx, dw;
+  bool dz, pad_x, pad_w;
+  size_t dz_at, x, w, db, part, total;
+};
+BackwardLayout backward_layout(int64_t n, int32_t cols, int32_t units, bool d_out_bf16, int32_t act, uint32_t wanted) {
+  BackwardLayout L{};
+  const bool dx = wanted & TWELL_LINEAR_DX, dw = wanted & TWELL_LINEAR_DW;
+  L.dx = twell::linear_plan(twell::LINEAR_MIXED, n, units, cols);
+  L.dw = twell::linear_plan(twell::LINEAR_COLS, units, n, cols);
+  L.dz = (dx || dw) && (act != TWELL_ACT_NONE || !d_out_bf16 || units % 8 != 0);
+  L.pad_x = dw && cols % 8 != 0;
+  L.pad_w = dx && cols % 8 != 0;
+  const size_t ld = (size_t)twell::linear_pad(cols);
+  Pieces p;
+  L.dz_at = p.take(L.dz ? (size_t)n * twell::linear_pad(units) * 2 : 0);
+  L.x = p.take(L.pad_x ? (size_t)n * ld * 2 : 0);
+  L.w = p.take(L.pad_w ? (size_t)units * ld * 2 : 0);
+  const int parts = twell::linear_db_parts(n);
+  L.db = p.take(wanted & TWELL_LINEAR_DB && parts > 1 ? (size_t)parts * units * 4 : 0);
+  const size_t part_dx = dx ? twell::linear_part_bytes(L.dx, n, cols) : 0, part_dw = dw ? twell::linear_part_bytes(L.dw, units, cols) : 0;
+  L.part = p.take(part_dx > part_dw ? part_dx : part_dw);
+  L.total = n == 0 ? 0 : p.total;
+  return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+twell_status twell_linear_ws(int64_t n, int32_t cols, int32_t units, size_t* ws_bytes) {
+  const twell_status st = check_dims(n, cols, units);
+  if (st != TWELL_OK) return st;
+  if (ws_bytes == nullptr) return fail(TWELL_ERR_INVALID_ARG, "ws_bytes is NULL");
+  *ws_bytes = forward_layout(n, cols, units).total;
+  return ok();
+}
+
+twell_status twell_linear(int64_t n, int32_t cols, int32_t units, const void* x, const void* w,
+                          twell_dtype bias_dtype, const void* bias, int32_t act, twell_dtype res_dtype,
+                          const void* residual, void* pre, twell_dtype y_dtype, void* y, void* ws, size_t ws_bytes,
+                          void* stream) {
+  twell_status st = check_dims(n, cols, units);
+  if (st != TWELL_OK) return st;
+  if (bad_dtype(y_dtype) || (bias != nullptr && bad_dtype(bias_dtype)) || (residual != nullptr && bad_dtype(res_dtype)))
+    return fail(TWELL_ERR_INVALID_ARG, "dtypes must be bf16 or fp32");
+  if (bad_act(act)) return fail(TWELL_ERR_INVALID_ARG, "act is none of TWELL_ACT_*");
+  const size_t results = (size_t)n * units;
+  OPS_CHECK_PTR(x, (size_t)n * cols * 2, "x");
+  OPS_CHECK_PTR(w, (size_t)units * cols * 2, "w");
+  OPS_CHECK_OPT(bias, (size_t)units * size_of(bias_dtype), "bias");
+  OPS_CHECK_OPT(residual, results * size_of(res_dtype), "residual");
+  OPS_CHECK_OPT(pre, results * 2, "pre");
+  OPS_CHECK_PTR(y, results * size_of(y_dtype), "y");
+  if (residual == y && residual != nullptr && res_dtype != y_dtype)
+    return fail(TWELL_ERR_INVALID_ARG, "residual may be y itself only when both have one type");
+  if (n == 0) return ok();
+  const ForwardLayout L = forward_layout(n, cols, units);
+  if ((st = check_ws(ws, ws_bytes, L.total, "workspace smaller than twell_linear_ws says")) != TWELL_OK) return st;
+  ok();
+  char* base = static_cast<char*>(ws);
+  const hipStream_t s = (hipStream_t)stream;
+  twell::LinearArgs a{};
+  a.p = {static_cast<const uint16_t*>(w), cols};
+  a.q = {static_cast<const uint16_t*>(x), cols};
+  a.k = cols;
+  a.out = {n, units, bias, residual, pre, y, bias_dtype == TWELL_BF16, res_dtype == TWELL_BF16, y_dtype == TWELL_BF16, act};
+  if (L.pad) {
+    const int64_t ld = twell::linear_pad(cols);
+    hipError_t e = twell::launch_linear_pad(x, n, cols, base + L.x, ld, s);
+    if (e == hipSuccess) e = twell::launch_linear_pad(w, units, cols, base + L.w, ld, s);
+    if (e != hipSuccess) return hip_status(e, "twell_linear");
+    a.p = {reinterpret_cast<const uint16_t*>(base + L.w), ld};
+    a.q = {reinterpret_cast<const uint16_t*>(base + L.x), ld};
+    a.k = ld;  // zeros behind the last column
+  }
+  a.part = reinterpret_cast<float*>(base + L.part);
+  return hip_status(twell::launch_linear(twell::LINEAR_ROWS, L.plan, a, s), "twell_linear");
+}
+
+twell_status twell_linear_bwd_ws(int64_t n, int32_t cols, int32_t units, twell_dtype d_out_dtype, int32_t act,
+                                 uint32_t wanted, size_t* ws_bytes) {
+  const twell_status st = check_dims(n, cols, units);
+  if (st != TWELL_OK) return st;
+  if (bad_dtype(d_out_dtype)) return fail(TWELL_ERR_INVALID_ARG, "dtypes must be bf16 or fp32");
+  if (bad_act(act)) return fail(TWELL_ERR_INVALID_ARG, "act is none of TWELL_ACT_*");
+  if (ws_bytes == nullptr) return fail(TWELL_ERR_INVALID_ARG, "ws_bytes is NULL");
+  *ws_bytes = backward_layout(n, cols, units, d_out_dtype == TWELL_BF16, act, wanted).total;
+  return ok();
+}
+
+twell_status twell_linear_bwd(int64_t n, int32_t cols, int32_t units, twell_dtype d_out_dtype, const void* d_out,
+                              int32_t act, const void* pre, const void* x, const void* w, twell_dtype dx_dtype,
+                              void* dx, twell_dtype dw_dtype, void* dw, float* db, void* ws, size_t ws_bytes,
+                              void* stream) {
+  twell_status st = check_dims(n, cols, units);
+  if (st != TWELL_OK) return st;
+  if (bad_dtype(d_out_dtype) || (dx != nullptr && bad_dtype(dx_dtype)) || (dw != nullptr && bad_dtype(dw_dtype)))
+    return fail(TWELL_ERR_INVALID_ARG, "dtypes must be bf16 or fp32");
+  if (bad_act(act)) return fail(TWELL_ERR_INVALID_ARG, "act is none of TWELL_ACT_*");
+  const size_t results = (size_t)n * units;
+  OPS_CHECK_PTR(d_out, results * size_of(d_out_dtype), "d_out");
+  if (act != TWELL_ACT_NONE) OPS_CHECK_PTR(pre, results * 2, "pre");
+  if (dw != nullptr) OPS_CHECK_PTR(x, (size_t)n * cols * 2, "x");
+  if (dx != nullptr) OPS_CHECK_PTR(w, (size_t)units * cols * 2, "w");
+  OPS_CHECK_OPT(dx, (size_t)n * cols * size_of(dx_dtype), "dx");
+  OPS_CHECK_OPT(dw, (size_t)units * cols * size_of(dw_dtype), "dw");
+  OPS_CHECK_OPT(db, (size_t)units * 4, "db");
+  // an empty dx may have no address
+  if (dx == nullptr && dw == nullptr && db == nullptr) return n == 0 ? ok() : fail(TWELL_ERR_INVALID_ARG, "no output is given");
+  const uint32_t wanted = (dx != nullptr ? TWELL_LINEAR_DX : 0) | (dw != nullptr ? TWELL_LINEAR_DW : 0) |
+                          (db != nullptr ? TWELL_LINEAR_DB : 0);
+  const bool d_out_bf16 = d_out_dtype == TWELL_BF16;
+  const BackwardLayout L = backward_layout(n, cols, units, d_out_bf16, act, wanted);
+  if ((st = check_ws(ws, ws_bytes, L.total, "workspace smaller than twell_linear_bwd_ws says")) != TWELL_OK) return st;
+  ok();
+  char* base = static_cast<char*>(ws);
+  const hipStream_t s = (hipStream_t)stream;
+  hipError_t e = hipSuccess;
+  twell::LinearOperand dz{static_cast<const uint16_t*>(d_out), units};
+  if (L.dz || db != nullptr) {
+    twell::LinearDzArgs z{};
+    z.rows = n;
+    z.units = units;
+    z.act = act;
+    z.g_bf16 = d_out_bf16;
+    z.d_out = d_out;
+    z.pre = pre;
+    if (L.dz && n > 0) {
+      z.dz = reinterpret_cast<uint16_t*>(base + L.dz_at);
+      z.ld = twell::linear_pad(units);
+      dz = {z.dz, z.ld};
+    }
+    z.db = db;
+    z.part = reinterpret_cast<float*>(base + L.db);
+    if (n > 0 || db != nullptr) e = twell::launch_linear_dz(z, s);
+    if (e != hipSuccess) return hip_status(e, "twell_linear_bwd");
+  }
+  const int64_t ld = twell::linear_pad(cols);
+  twell::LinearArgs a{};
+  a.part = reinterpret_cast<float*>(base + L.part);
+  if (dx != nullptr && n > 0) {
+    a.p = {static_cast<const uint16_t*>(w), cols};
+    if (L.pad_w) {
+      if ((e = twell::launch_linear_pad(w, units, cols, base + L.w, ld, s)) != hipSuccess) return hip_status(e, "twell_linear_bwd");
+      a.p = {reinterpret_cast<const uint16_t*>(base + L.w), ld};
+    }
+    a.q = dz;
+    a.k = units;
+    a.out = {n, cols, nullptr, nullptr, nullptr, dx, 0, 0, dx_dtype == TWELL_BF16, TWELL_ACT_NONE};
+    if ((e = twell::launch_linear(twell::LINEAR_MIXED, L.dx, a, s)) != hipSuccess) return hip_status(e, "twell_linear_bwd");
+  }
+  if (dw != nullptr) {
+    a.out = {units, cols, nullptr, nullptr, nullptr, dw, 0, 0, dw_dtype == TWELL_BF16, TWELL_ACT_NONE};
+    if (n == 0) return hip_status(twell::launch_linear_zero(a.out, s), "twell_linear_bwd");
+    a.p = {static_cast<const uint16_t*>(x), cols};
+    if (L.pad_x) {
+      if ((e = twell::launch_linear_pad(x, n, cols, base + L.x, ld, s)) != hipSuccess) return hip_status(e, "twell_linear_bwd");
+      a.p = {reinterpret_cast<const uint16_t*>(base + L.x), ld};
+    }
+    a.q = dz;
+    a.k = n;
+    e = twell::launch_linear(twell::LINEAR_COLS, L.dw, a, s);
+  }
+  return hip_status(e, "twell_linear_bwd");
+}
+
+}  // extern "C"

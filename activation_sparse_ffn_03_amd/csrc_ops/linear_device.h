@@ -1,0 +1,129 @@
+// What the linear layer's kernels share on the device: activations, and the
+// epilogue of eight neighbouring results of one output row.
+#pragma once
+
+#include "chunk8.h"
+#include "ops_kernels.h"
+
+namespace twell {
+
+// e^x by the hardware's power of two (one last place): the product x log2(e) is
+// rounded, which makes the result off by |x| 2^-24 more, relative. 0 and infinity
+// beyond fp32's range.
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+__device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// The normal distribution function, and its density over sqrt(2 pi), by formula
+// 26.2.17 of Abramowitz and Stegun's Handbook of Mathematical Functions, which is
+// off by at most 7.5e-8: as exact as 1 + erf in fp32, without its two branches,
+// whose code an epilogue of 256 results a lane would hold 256 times.
+__device__ __forceinline__ float normal_cdf(float z, float& density) {
+  const float x = fabsf(z), t = rcp_fast(fmaf(0.2316419f, x, 1.f));
+  density = exp_fast(-0.5f * z * z) * 0.39894228f;
+  const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.330274429f, -1.821255978f), 1.781477937f), -0.356563782f), 0.319381530f);
+  const float tail = density * p;
+  return z < 0.f ? tail : 1.f - tail;  // NaN: 1 - NaN
+}
+
+// act(z), fp32.
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (ACT == TWELL_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
+  if constexpr (ACT == TWELL_ACT_SILU) return z * rcp_fast(1.f + exp_fast(-z));
+  if constexpr (ACT == TWELL_ACT_GELU) {
+    float density;
+    return z * normal_cdf(z, density);
+  }
+  return z;
+}
+// act'(z); ReLU's is 0 at 0.
+template <int ACT>
+__device__ __forceinline__ float activate_slope(float z) {
+  if constexpr (ACT == TWELL_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  if constexpr (ACT == TWELL_ACT_SILU) {
+    const float s = rcp_fast(1.f + exp_fast(-z));
+    return s * (1.f + z * (1.f - s));
+  }
+  if constexpr (ACT == TWELL_ACT_GELU) {
+    float density;
+    const float c = normal_cdf(z, density);
+    return fmaf(z, density, c);
+  }
+  return 1.f;
+}
+
+// N neighbouring elements at any element of an array, as floats, of which `have`
+// (N or more: all) are there.
+template <int N>
+__device__ __forceinline__ void load_some(const void* base, int is_bf16, int64_t at, int have, float (&v)[N]) {
+  if (is_bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    if (have >= N) {
+      uint32_t w[N / 2];
+      if constexpr (N == 8) *reinterpret_cast<u32x4_t*>(w) = *reinterpret_cast<const u32x4_a2_t*>(p);
+      else *reinterpret_cast<u32x2_t*>(w) = *reinterpret_cast<const u32x2_a2_t*>(p);
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = k & 1 ? bf16hi_to_f32(w[k >> 1]) : bf16lo_to_f32(w[k >> 1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = k < have ? bf16_to_f32(p[k]) : 0.f;
+    }
+  } else {
+    const float* p = static_cast<const float*>(base) + at;
+    if (have >= N) {
+#pragma unroll
+      for (int k = 0; k < N; k += 4) {
+        const f32x4_t q = *reinterpret_cast<const f32x4_a4_t*>(p + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[k + i] = q[i];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = k < have ? p[k] : 0.f;
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_some(void* base, int is_bf16, int64_t at, int have, const float (&v)[N]) {
+  if (is_bf16) {
+    uint16_t* p = static_cast<uint16_t*>(base) + at;
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int k = 0; k < N; k += 2) w[k >> 1] = pack_bf16(v[k], v[k + 1]);
+    if (have >= N) {
+      if constexpr (N == 8) *reinterpret_cast<u32x4_a2_t*>(p) = *reinterpret_cast<const u32x4_t*>(w);
+      else *reinterpret_cast<u32x2_a2_t*>(p) = *reinterpret_cast<const u32x2_t*>(w);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k < have) p[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+    }
+  } else {
+    float* p = static_cast<float*>(base) + at;
+    if (have >= N) {
+#pragma unroll
+      for (int k = 0; k < N; k += 4) *reinterpret_cast<f32x4_a4_t*>(p + k) = f32x4_t{v[k], v[k + 1], v[k + 2], v[k + 3]};
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k < have) p[k] = v[k];
+    }
+  }
+}
+
+// y = residual + act(z + bias) of N neighbouring units of an output row, where
+// z holds the product's sums; z as well where it is asked for. One rounding
+// each, at the stores.
+template <int ACT, int N>
+__device__ __forceinline__ void finish_units(const LinearOut& o, int64_t row, int unit, int have, float (&z)[N],
+                                             const float (&bias)[N], const float (&res)[N]) {
+  const int64_t at = row * o.units + unit;
+#pragma unroll
+  for (int k = 0; k < N; ++k) z[k] += bias[k];
+  if (o.pre != nullptr) store_some<N>(o.pre, 1, at, have, z);
+#pragma unroll
+  for (int k = 0; k < N; ++k) z[k] = activate<ACT>(z[k]) + res[k];
+  store_some<N>(o.y, o.y_bf16, at, have, z);
+}
+
+}  // namespace twell

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/twell.h"
+
 namespace twell {
 
 // Widest row the norm takes: a row is held in the registers of one workgroup.
@@ -274,5 +276,87 @@ struct Mx4ProductArgs {
   int y_bf16;
 };
 hipError_t launch_mx4_product(Mx4Plan plan, const Mx4ProductArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------- linear
+
+// Where a product's results go: [rows][units], units neighbouring.
+struct LinearOut {
+  int64_t rows;
+  int units;
+  const void* bias;      // [units] or null
+  const void* residual;  // [rows][units] or null; may be y
+  void* pre;             // bf16 [rows][units] or null
+  void* y;
+  int bias_bf16, res_bf16, y_bf16, act;
+};
+// An operand of a product: bf16, `ld` elements from one line to the next. Lines
+// are rows of the result's side with their k neighbouring, or k lines with the
+// side's elements neighbouring.
+struct LinearOperand {
+  const uint16_t* p;
+  int64_t ld;
+};
+// out[i][u] = sum_k q(i, k) p(u, k), what follows in LinearOut.
+struct LinearArgs {
+  LinearOperand p, q;
+  int64_t k;
+  LinearOut out;
+  int splits;   // of the stages of k; the sums of each go to `part` when there are several
+  float* part;  // [splits][rows][units]
+};
+enum LinearLayout {
+  LINEAR_ROWS,   // both operands with k neighbouring: y = x w^T
+  LINEAR_MIXED,  // p with its units neighbouring: dx = dz w
+  LINEAR_COLS    // both with k lines: dw = dz^T x
+};
+constexpr int kLinearMaxCols = 1 << 20;  // a line's bytes times a tile's lines stay below 2^32
+constexpr int kLinearStage = 64;         // k of a stage of the tiles
+// Elements that a line has at least when a tile reads it: whole 16 bytes.
+inline int64_t linear_pad(int64_t n) { return (n + 7) / 8 * 8; }
+
+// How a product of `rows` x `units` results over k runs.
+struct LinearPlan {
+  int tile;    // 0: straight from memory (LINEAR_ROWS only), 128 or 256: tiles of that size through LDS
+  int splits;  // of k; 1 straight from memory
+};
+inline LinearPlan linear_plan(LinearLayout layout, int64_t rows, int64_t k, int units) {
+  if (rows == 0 || k == 0) return {128, 1};  // nothing is launched
+  if (layout == LINEAR_ROWS && rows <= 64) return {0, 1};
+  const int64_t stages = (k + kLinearStage - 1) / kLinearStage;
+  const int64_t mid = ((rows + 127) / 128) * ((units + 127) / 128), big = ((rows + 255) / 256) * ((units + 255) / 256);
+  if (big >= 256) return {256, 1};
+  int64_t splits = 512 / mid;
+  if (splits > stages / 4) splits = stages / 4;
+  if (splits > 16) splits = 16;
+  return {128, (int)(splits < 1 ? 1 : splits)};
+}
+inline size_t linear_part_bytes(const LinearPlan& p, int64_t rows, int units) {
+  return p.splits > 1 ? (size_t)p.splits * rows * units * 4 : 0;
+}
+// Runs the product by its plan: tiles or straight from memory, and the splits' sums.
+hipError_t launch_linear(LinearLayout layout, const LinearPlan& plan, const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_rows(int tile, const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_mixed(int tile, const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_cols(int tile, const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_direct(const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_zero(const LinearOut& o, hipStream_t s);  // y = 0
+// Adds the splits' sums in their order and finishes them.
+hipError_t launch_linear_join(const LinearArgs& a, hipStream_t s);
+// rows x cols of bf16 to lines of ld elements, zeros behind the last column.
+hipError_t launch_linear_pad(const void* in, int64_t rows, int cols, void* out, int64_t ld, hipStream_t s);
+
+struct LinearDzArgs {
+  int64_t rows;
+  int units;
+  int act, g_bf16;
+  const void* d_out;  // [rows][units]
+  const void* pre;    // bf16 [rows][units], with an activation
+  uint16_t* dz;       // [rows][ld] or null
+  int64_t ld;
+  float* db;          // [units] or null
+  float* part;        // [linear_db_parts][units] when there are several
+};
+inline int linear_db_parts(int64_t rows) { return (int)(rows < 16 ? 1 : rows < 1024 ? (rows + 15) / 16 : 64); }
+hipError_t launch_linear_dz(const LinearDzArgs& a, hipStream_t s);
 
 }  // namespace twell

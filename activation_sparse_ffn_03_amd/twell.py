@@ -35,7 +35,7 @@ EXPORTS = ("twell_status_str", "twell_last_error", "twell_n_tiles", "twell_query
            "twell_ffn_forward_noalloc", "twell_route_hybrid", "twell_ffn_bwd", "twell_add_rms_norm",
            "twell_add_rms_norm_bwd_ws", "twell_add_rms_norm_bwd", "twell_mx4_sizes", "twell_quantize_mx4",
            "twell_dequantize_mx4", "twell_matmul_mx4_ws", "twell_matmul_mx4", "twell_linear_mx4_ws",
-           "twell_linear_mx4", "twell_dropout", "twell_join_rms_norm", "twell_join_rms_norm_bwd_ws",
+           "twell_linear_mx4", "twell_linear_ws", "twell_linear", "twell_linear_bwd_ws", "twell_linear_bwd", "twell_dropout", "twell_join_rms_norm", "twell_join_rms_norm_bwd_ws",
            "twell_join_rms_norm_bwd", "twell_trace_start",
            "twell_trace_stop", "twell_trace_count", "twell_trace_dropped", "twell_trace_get")
 
@@ -150,6 +150,16 @@ def lib() -> ctypes.CDLL:
         L.twell_linear_mx4.restype = ctypes.c_int
         L.twell_linear_mx4.argtypes = [i64, i32, i32, ctypes.c_int, vp, vp, vp, ctypes.c_int, vp, vp, sz, vp]
         u32, pj = ctypes.c_uint32, ctypes.POINTER(Join)
+        L.twell_linear_ws.restype = ctypes.c_int
+        L.twell_linear_ws.argtypes = [i64, i32, i32, psz]
+        L.twell_linear.restype = ctypes.c_int
+        L.twell_linear.argtypes = [i64, i32, i32, vp, vp, ctypes.c_int, vp, i32, ctypes.c_int, vp, vp, ctypes.c_int, vp, vp,
+                                   sz, vp]
+        L.twell_linear_bwd_ws.restype = ctypes.c_int
+        L.twell_linear_bwd_ws.argtypes = [i64, i32, i32, ctypes.c_int, i32, u32, psz]
+        L.twell_linear_bwd.restype = ctypes.c_int
+        L.twell_linear_bwd.argtypes = [i64, i32, i32, ctypes.c_int, vp, i32, vp, vp, vp, ctypes.c_int, vp, ctypes.c_int, vp,
+                                       vp, vp, sz, vp]
         L.twell_dropout.restype = ctypes.c_int
         L.twell_dropout.argtypes = [i64, i32, ctypes.c_int, vp, f32, vp, u32, vp, vp]
         L.twell_join_rms_norm.restype = ctypes.c_int
@@ -680,6 +690,112 @@ def linear_mx4(x, w_codes, w_scales, dtype=torch.bfloat16, out=None, ws=None, st
     at, nbytes, _keep = _workspace(ws, ws is None and linear_mx4_ws(n, cols, units), x, stream)
     _call(lib().twell_linear_mx4, dev, stream, n, cols, units, *args, _code(out, "out"),
           _addr(out, "out", (n, units), None, dev), at, nbytes)
+    return out
+
+
+# ---------------------------------------------------------------- linear layers beside the block
+
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+LINEAR_DX, LINEAR_DW, LINEAR_DB = 1, 2, 4
+
+
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(map(repr, ACTS))}, got {act!r}")
+    return ACTS[act]
+
+
+@functools.lru_cache(maxsize=256)
+def linear_ws(rows: int, cols: int, units: int) -> int:
+    """Workspace bytes of linear."""
+    if cols > _INT32 or units > _INT32:
+        _too_large("twell_linear_ws", max(cols, units))
+    n = ctypes.c_size_t()
+    _check(lib().twell_linear_ws(rows, cols, units, ctypes.byref(n)), "twell_linear_ws")
+    return n.value
+
+
+def linear(x, w, bias=None, act: str = "none", residual=None, dtype=torch.bfloat16, out=None, pre=None, ws=None,
+           stream=None):
+    """residual + act(x · w^T + bias) in one call (twell_linear): x [rows, cols] and w [units, cols] bf16, bias [units]
+    and residual [rows, units] bf16, fp32 or None, act "none", "relu", "silu" or "gelu" (with erf). Returns [rows,
+    units] in bf16 or fp32, written into `out` when given, which may be the residual itself. pre: a bf16 [rows, units]
+    tensor that is given x · w^T + bias, for linear_bwd. ws (bytes of linear_ws) is allocated here when not given."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [rows, cols] and w [units, cols]")
+    n, cols = x.shape
+    units = w.shape[0]
+    if cols > _INT32 or units > _INT32:
+        _too_large("twell_linear", max(cols, units))
+    dev, bf = x.get_device(), torch.bfloat16
+    shape = (n, units)
+    code = _act(act)
+    args = (_addr(x, "x", x.shape, bf), _addr(w, "w", (units, cols), bf, dev), BF16 if bias is None else _code(bias, "bias"),
+            _addr(bias, "bias", (units,), None, dev), code, BF16 if residual is None else _code(residual, "residual"),
+            _addr(residual, "residual", shape, None, dev), _addr(pre, "pre", shape, bf, dev))
+    if out is None:
+        out = _new(stream, lambda: torch.empty(shape, dtype=dtype, device=x.device))
+    yc, y = _code(out, "out"), _addr(out, "out", shape, None, dev)
+    at, nbytes, _keep = _workspace(ws, ws is None and linear_ws(n, cols, units), x, stream)
+    _call(lib().twell_linear, dev, stream, n, cols, units, *args, yc, y, at, nbytes)
+    return out
+
+
+class LinearGrads(NamedTuple):
+    """What linear_bwd puts out; fields that were not asked for are None."""
+    dx: Optional[torch.Tensor]  # [rows, cols]
+    dw: Optional[torch.Tensor]  # [units, cols]
+    db: Optional[torch.Tensor]  # [units] fp32
+
+
+@functools.lru_cache(maxsize=256)
+def linear_bwd_ws(rows: int, cols: int, units: int, d_out_dtype=torch.bfloat16, act: str = "none",
+                  wanted: int = LINEAR_DX | LINEAR_DW | LINEAR_DB) -> int:
+    """Workspace bytes of linear_bwd for the gradients in `wanted` (LINEAR_* bits)."""
+    if cols > _INT32 or units > _INT32:
+        _too_large("twell_linear_bwd_ws", max(cols, units))
+    n = ctypes.c_size_t()
+    _check(lib().twell_linear_bwd_ws(rows, cols, units, _CODES[d_out_dtype], _act(act), wanted, ctypes.byref(n)),
+           "twell_linear_bwd_ws")
+    return n.value
+
+
+def linear_bwd(d_out, x, w, act: str = "none", pre=None, bias: bool = True, dx_dtype=torch.bfloat16,
+               dw_dtype=torch.float32, out=None, ws=None, stream=None) -> LinearGrads:
+    """Gradients of linear (twell_linear_bwd): dx [rows, cols] and dw [units, cols] in bf16 or fp32, and with bias=True
+    db [units] in fp32, from that of its output, bf16 or fp32 (which is the residual's as well), and, with an
+    activation, the pre that the forward filled. With an activation or an fp32 d_out the gradient of the pre-activation
+    is rounded to bf16 for the two products. Written into `out`, a LinearGrads whose fields are None where a gradient is
+    not wanted, when given; ws (bytes of linear_bwd_ws) is allocated here when not."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [rows, cols] and w [units, cols]")
+    n, cols = x.shape
+    units = w.shape[0]
+    if cols > _INT32 or units > _INT32:
+        _too_large("twell_linear_bwd", max(cols, units))
+    dev, bf, code = x.get_device(), torch.bfloat16, _act(act)
+    shape = (n, units)
+    if code and pre is None:
+        raise ValueError("an activation needs the forward's pre")
+    args = (_code(d_out, "d_out"), _addr(d_out, "d_out", shape, None, dev), code,
+            _addr(pre, "pre", shape, bf, dev) if code else None, _addr(x, "x", x.shape, bf),
+            _addr(w, "w", (units, cols), bf, dev))
+    if out is None:
+        def make():
+            e = dict(device=x.device)
+            return LinearGrads(torch.empty((n, cols), dtype=dx_dtype, **e), torch.empty((units, cols), dtype=dw_dtype, **e),
+                               torch.empty(units, dtype=torch.float32, **e) if bias else None)
+        out = _new(stream, make)
+    elif not isinstance(out, LinearGrads):
+        out = LinearGrads(*out)
+    dx, dw, db = out
+    outs = (BF16 if dx is None else _code(dx, "dx"), _addr(dx, "dx", (n, cols), None, dev),
+            BF16 if dw is None else _code(dw, "dw"), _addr(dw, "dw", (units, cols), None, dev),
+            _addr(db, "db", (units,), torch.float32, dev))
+    wanted = (LINEAR_DX if dx is not None else 0) | (LINEAR_DW if dw is not None else 0) | (LINEAR_DB if db is not None else 0)
+    need = ws is None and linear_bwd_ws(n, cols, units, d_out.dtype, act, wanted)
+    at, nbytes, _keep = _workspace(ws, need, x, stream)
+    _call(lib().twell_linear_bwd, dev, stream, n, cols, units, *args, *outs, at, nbytes)
     return out
 
 

@@ -432,6 +432,60 @@ twell_status twell_linear_mx4(int64_t n, int32_t cols, int32_t units, twell_dtyp
                               size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Linear layers beside the block
+ * ------------------------------------------------------------------------- */
+
+/* Activations, the values of an int32_t `act`. */
+typedef enum twell_act {
+  TWELL_ACT_NONE = 0,
+  TWELL_ACT_RELU = 1, /* max(z, 0); slope 0 at 0 */
+  TWELL_ACT_SILU = 2, /* z / (1 + e^-z) */
+  TWELL_ACT_GELU = 3  /* z (1 + erf(z / sqrt 2)) / 2 */
+} twell_act;
+
+/* Workspace bytes of twell_linear (host-only query; may be 0). */
+twell_status twell_linear_ws(int64_t n, int32_t cols, int32_t units, size_t* ws_bytes);
+
+/* A linear layer with bias, activation and residual in the product's epilogue:
+ *   z[i,u] = sum_k x[i,k] * w[u,k] + bias[u],  y = residual + act(z)
+ * x [n][cols] and w [units][cols] bf16 (each row of w belongs to a unit, as in
+ * the block's weights); products are exact, sums and everything behind them fp32,
+ * y is rounded once to y_dtype. bias [units] of bias_dtype or NULL; residual
+ * [n][units] of res_dtype or NULL; pre: NULL, or bf16 [n][units] for z, which
+ * twell_linear_bwd takes. residual may be y itself when both have one type (the
+ * stream updated in place); otherwise outputs may not overlap inputs. Any cols
+ * and units from 1 to 2^20; n == 0 is a no-op. ws: at least the queried bytes
+ * (NULL allowed when that is 0). */
+twell_status twell_linear(int64_t n, int32_t cols, int32_t units, const void* x, const void* w,
+                          twell_dtype bias_dtype, const void* bias, int32_t act, twell_dtype res_dtype,
+                          const void* residual, void* pre, twell_dtype y_dtype, void* y, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* Which gradients a backward call writes. */
+#define TWELL_LINEAR_DX 1
+#define TWELL_LINEAR_DW 2
+#define TWELL_LINEAR_DB 4
+
+/* Workspace bytes of twell_linear_bwd for the gradients in `wanted`
+ * (TWELL_LINEAR_* bits; host-only query). */
+twell_status twell_linear_bwd_ws(int64_t n, int32_t cols, int32_t units, twell_dtype d_out_dtype, int32_t act,
+                                 uint32_t wanted, size_t* ws_bytes);
+
+/* Backward of twell_linear, from the pre-activation it stored:
+ *   dz = d_out * act'(pre),  dx = dz w,  dw = dz^T x,  db = sum_i dz
+ * d_out [n][units] of d_out_dtype (also the gradient of the residual); pre bf16
+ * [n][units] (not read with TWELL_ACT_NONE). dz is a bf16 operand of both
+ * products: it is rounded to bf16 unless it is a bf16 d_out itself (act NONE);
+ * db sums it unrounded. dx [n][cols] of dx_dtype, dw [units][cols] of dw_dtype, db
+ * [units] fp32, each NULL when it is not wanted; sums are fp32, in a fixed order.
+ * x and w may be NULL when the gradient that reads them is not wanted. Outputs
+ * are fully overwritten (n == 0: dw and db are 0) and may not overlap inputs. */
+twell_status twell_linear_bwd(int64_t n, int32_t cols, int32_t units, twell_dtype d_out_dtype, const void* d_out,
+                              int32_t act, const void* pre, const void* x, const void* w, twell_dtype dx_dtype,
+                              void* dx, twell_dtype dw_dtype, void* dw, float* db, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* ---------------------------------------------------------------------------
  * From a block's output to the next block's input
  * ------------------------------------------------------------------------- */
 

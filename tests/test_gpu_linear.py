@@ -1,0 +1,265 @@
+"""The linear layer with bias, activation and residual and its gradients on the GPU: products of small whole numbers bit for
+bit, others against float64 within bounds counted in roundings, at sizes that take every kernel; views, streams, graphs."""
+from __future__ import annotations
+
+import itertools
+
+import pytest
+import torch
+
+from activation_sparse_ffn_03_amd import twell as tw
+
+import linear_reference as lr
+from gpu_util import require_gpu
+from test_gpu_norm import _check_guards, _guarded
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(gen, *shape, scale=1.0, dtype=F32):
+    return (torch.randn(*shape, generator=gen, device="cuda") * scale).to(dtype)
+
+
+def _whole(gen, *shape, dtype=BF, top=2):
+    return torch.randint(-top, top + 1, shape, generator=gen, device="cuda").to(dtype)
+
+
+def _ws(need):
+    return _guarded((need,), torch.uint8)
+
+
+# rows, cols, units: few rows straight from memory (each tile, partial and whole, rows of any alignment), tiles of 128 (one
+# stage and more, whole and partial stages, edges both ways), of 256, k split over workgroups
+FEW = [(1, 1, 1), (1, 8, 8), (1, 64, 16), (1, 4096, 1000), (2, 7, 5), (3, 100, 33), (15, 513, 70), (16, 128, 16), (17, 72, 40),
+       (24, 1999, 130), (32, 1024, 256), (33, 640, 64), (47, 999, 257), (64, 520, 96)]
+TILES = [(65, 1, 1), (65, 8, 129), (100, 64, 100), (128, 128, 128), (129, 63, 127), (200, 72, 300), (256, 192, 256), (300, 1000, 77),
+         (130, 130, 640), (500, 4096, 200), (1000, 200, 1001), (513, 1990, 515)]
+BIG = [(4100, 64, 4200), (4096, 128, 4096), (4001, 137, 4111), (4353, 200, 4097)]
+
+
+def _exact_case(rows, cols, units, bias, res, y, pre, act="relu"):
+    print(f"[linear] {rows}x{cols}x{units} bias={bias} res={res} y={y} pre={pre}", flush=True)
+    gen = _gen(rows + cols + units)
+    x, w = _whole(gen, rows, cols), _whole(gen, units, cols)
+    b = None if bias is None else _whole(gen, units, dtype=bias, top=5)
+    r = None if res is None else _whole(gen, rows, units, dtype=res, top=100)
+    out, guard = _guarded((rows, units), y)
+    z, zguard = _guarded((rows, units), BF)
+    ws, wguard = _ws(tw.linear_ws(rows, cols, units))
+    got = tw.linear(x, w, bias=b, act=act, residual=r, out=out, pre=z if pre else None, ws=ws)
+    torch.cuda.synchronize()
+    assert got is out
+    _check_guards(guard, zguard, wguard)
+    want = x.double() @ w.double().t()
+    if b is not None:
+        want = want + b.double()
+    if pre:
+        assert torch.equal(z, want.to(BF))
+    if act == "relu":
+        want = want.clamp(min=0)
+    if r is not None:
+        want = want + r.double()
+    assert torch.equal(out, want.to(y))
+
+
+@pytest.mark.parametrize("rows,cols,units", FEW + TILES + BIG)
+def test_products_of_whole_numbers_are_exact(rows, cols, units):
+    require_gpu()
+    for k, (bias, res, y) in enumerate(((None, None, F32), (F32, BF, BF), (BF, F32, F32), (BF, None, BF))):
+        _exact_case(rows, cols, units, bias, res, y, k % 2 == 1, act="none" if k == 2 else "relu")
+
+
+@pytest.mark.parametrize("rows,cols,units", [(1, 1000, 257), (24, 5632, 200), (50, 999, 130), (200, 1990, 260), (300, 4096, 129), (4100, 72, 4200)])
+@pytest.mark.parametrize("act", list(tw.ACTS))
+def test_forward(rows, cols, units, act):
+    require_gpu()
+    for k, (bias, res, y) in enumerate(itertools.product((None, F32), (None, BF), (BF, F32))):
+        gen = _gen(k)
+        x, w = _randn(gen, rows, cols, dtype=BF), _randn(gen, units, cols, scale=2 / cols ** 0.5, dtype=BF)
+        b = None if bias is None else _randn(gen, units, scale=2, dtype=bias)
+        r = None if res is None else _randn(gen, rows, units, dtype=res)
+        pre = torch.empty(rows, units, dtype=BF, device="cuda")
+        got = tw.linear(x, w, bias=b, act=act, residual=r, dtype=y, pre=pre)
+        (z, tz), (want, tol) = lr.forward(x, w, b, act, r, y)
+        assert bool(((got.double() - want).abs() <= tol).all())
+        assert bool(((pre.double() - z).abs() <= lr.rounded(tz, z, BF)).all())
+        assert torch.equal(got, tw.linear(x, w, bias=b, act=act, residual=r, dtype=y))  # the same bits without pre, again
+
+
+@pytest.mark.parametrize("rows", [1, 40, 130])
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+def test_far_and_special_pre_activations(act, rows):
+    """Values that leave exp's range, infinities and NaN."""
+    require_gpu()
+    x = torch.ones(rows, 8, dtype=BF, device="cuda")
+    special = [0.0, -0.0, 1e-30, -1e-30, 5.0, -5.0, 30.0, -30.0, 90.0, -90.0, 200.0, -200.0, 1e20, -1e20, 3e38, -3e38]
+    b = torch.tensor(special + [float("inf"), float("nan")], device="cuda")
+    w = torch.zeros(len(b), 8, dtype=BF, device="cuda")
+    got = tw.linear(x, w, bias=b, act=act, dtype=F32)
+    z = b[:-2].double()
+    want, tol = lr.act64(z, act), lr.act_tol(z, act)
+    assert bool(((got[:, :-2].double() - want).abs() <= tol + (want.abs() * lr.U if act == "relu" else 0)).all())
+    assert bool((got[:, -2] == float("inf")).all()) and bool(got[:, -1].isnan().all())
+
+
+@pytest.mark.parametrize("rows,cols,units", [(1, 512, 1000), (24, 999, 200), (300, 256, 300), (300, 4096, 129), (4100, 128, 4200)])
+def test_residual_in_place(rows, cols, units):
+    require_gpu()
+    gen = _gen(3)
+    x, w = _randn(gen, rows, cols, dtype=BF), _randn(gen, units, cols, scale=0.1, dtype=BF)
+    for dt in (BF, F32):
+        r = _randn(gen, rows, units, dtype=dt)
+        want = tw.linear(x, w, act="silu", residual=r, dtype=dt)
+        assert tw.linear(x, w, act="silu", residual=r, out=r) is r and torch.equal(r, want)
+
+
+def _backward_case(rows, cols, units, act, g_t, dx_t, dw_t, whole):
+    print(f"[linear_bwd] {rows}x{cols}x{units} {act} {g_t} {dx_t} {dw_t}", flush=True)
+    gen = _gen(rows + 3 * cols + units)
+    make = _whole if whole else _randn
+    x, w, g = make(gen, rows, cols, dtype=BF), make(gen, units, cols, dtype=BF), make(gen, rows, units, dtype=g_t)
+    pre = None if act == "none" else make(gen, rows, units, dtype=BF)
+    bufs, guards = zip(_guarded((rows, cols), dx_t), _guarded((units, cols), dw_t), _guarded((units,), F32))
+    ws, wguard = _ws(tw.linear_bwd_ws(rows, cols, units, g_t, act))
+    got = tw.linear_bwd(g, x, w, act=act, pre=pre, out=bufs, ws=ws)
+    torch.cuda.synchronize()
+    _check_guards(*guards, wguard)
+    pairs = lr.backward(g, x, w, act, pre, dx_t, dw_t)
+    for name, a, (want, tol) in zip(got._fields, got, pairs):
+        if whole and act in ("none", "relu"):
+            assert torch.equal(a, want.to(a.dtype)), name
+        else:
+            err = (a.double() - want).abs()
+            assert bool((err <= tol).all()), (name, float((err / tol.clamp(min=1e-300)).max()))
+    return (g, x, w, pre), got
+
+
+@pytest.mark.parametrize("rows,cols,units", [(1, 1, 1), (1, 100, 64), (2, 64, 7), (16, 128, 128), (63, 72, 200), (64, 256, 129),
+                                             (65, 65, 65), (128, 1000, 256), (200, 1999, 130), (509, 1000, 1021), (1000, 136, 520),
+                                             (5000, 128, 96), (4100, 4200, 72), (72, 4104, 4100), (70, 4101, 4100)])
+def test_gradients_of_whole_numbers_are_exact(rows, cols, units):
+    require_gpu()
+    for act, g_t, dx_t, dw_t in (("none", BF, F32, F32), ("relu", F32, BF, BF), ("relu", BF, F32, BF)):
+        _backward_case(rows, cols, units, act, g_t, dx_t, dw_t, True)
+
+
+@pytest.mark.parametrize("rows,cols,units", [(1, 256, 300), (37, 1000, 257), (700, 520, 333), (2500, 128, 264)])
+@pytest.mark.parametrize("act", list(tw.ACTS))
+def test_gradients(rows, cols, units, act):
+    require_gpu()
+    for g_t, dx_t, dw_t in ((BF, BF, F32), (F32, F32, BF)):
+        _backward_case(rows, cols, units, act, g_t, dx_t, dw_t, False)
+
+
+def test_gradients_that_are_not_asked_for():
+    require_gpu()
+    (g, x, w, pre), full = _backward_case(300, 260, 129, "silu", F32, BF, F32, False)
+    for keep in itertools.product((False, True), repeat=3):
+        if any(keep):
+            bufs = [torch.empty_like(t) if k else None for t, k in zip(full, keep)]
+            for a, c in zip(tw.linear_bwd(g, x, w, act="silu", pre=pre, out=bufs), full):
+                assert a is None or torch.equal(a, c)
+    plain = tw.linear_bwd(g, x, w, act="silu", pre=pre, bias=False)
+    assert plain.db is None and torch.equal(plain.dw, full.dw) and plain.dx.dtype == BF
+
+
+def test_gradient_against_differences():
+    """(f(v + h) - f(v - h)) / 2h of a float64 sum of the layer's outputs' definition, and the kernel's gradients."""
+    require_gpu()
+    gen = _gen(11)
+    rows, cols, units, h = 5, 16, 24, 1e-5
+    x, w, b = _randn(gen, rows, cols, dtype=BF), _randn(gen, units, cols, scale=0.5, dtype=BF), _randn(gen, units)
+    g = _randn(gen, rows, units, dtype=BF)
+    for act in ("silu", "gelu"):
+        pre = torch.empty(rows, units, dtype=BF, device="cuda")
+        tw.linear(x, w, bias=b, act=act, pre=pre)
+        got = tw.linear_bwd(g, x, w, act=act, pre=pre, dx_dtype=F32)
+        f = lambda xx, ww, bb: float((lr.act64(xx @ ww.t() + bb, act) * g.double()).sum())  # noqa: E731
+        vals = [x.double(), w.double(), b.double()]
+        (_, tx), (_, tw_), (_, tb) = lr.backward(g, x, w, act, pre, F32, F32)
+        # the kernel's slope is that of z rounded to bf16: no second derivative above 1 (SiLU 0.5, GELU 0.8)
+        dz = (g.double().abs() * 2.0 ** -8 * pre.double().abs())
+        extra = [dz @ w.double().abs(), dz.t() @ x.double().abs(), dz.sum(0)]
+        for k, (a, t, e) in enumerate(zip(got, (tx, tw_, tb), extra)):
+            for i in range(0, vals[k].numel(), 7):
+                up, dn = [v.clone() for v in vals], [v.clone() for v in vals]
+                up[k].view(-1)[i] += h
+                dn[k].view(-1)[i] -= h
+                d = (f(*up) - f(*dn)) / (2 * h)
+                # differences: the third derivative's h^2 and cancellation's 1e-16 / h, both below 1e-8 here
+                assert abs(float(a.view(-1)[i]) - d) <= float((t + e).reshape(-1)[i]) + 1e-8
+
+
+@pytest.mark.parametrize("cols,units", [(64, 40), (65, 41)])
+def test_no_rows(cols, units):
+    require_gpu()
+    e = lambda *s: torch.empty(*s, dtype=BF, device="cuda")  # noqa: E731
+    assert tw.linear(e(0, cols), e(units, cols)).shape == (0, units)
+    out = [e(0, cols), torch.full((units, cols), 3.0, device="cuda"), torch.full((units,), 3.0, device="cuda")]
+    got = tw.linear_bwd(e(0, units), e(0, cols), e(units, cols), out=out)
+    torch.cuda.synchronize()
+    assert bool((got.dw == 0).all()) and bool((got.db == 0).all())
+
+
+@pytest.mark.parametrize("rows,cols,units", [(9, 300, 40), (140, 300, 40), (140, 303, 41)])
+def test_non_finite_operands_stay_in_their_rows(rows, cols, units):
+    """NaN and infinity in a row of x reach that row alone, in w that unit alone, k behind the last none."""
+    require_gpu()
+    gen = _gen(5)
+    x, w = _whole(gen, rows, cols), _whole(gen, units, cols)
+    want = tw.linear(x, w, dtype=F32)
+    x[4, cols - 1], x[7, 0], w[6, cols - 1] = float("nan"), float("inf"), float("nan")
+    got = tw.linear(x, w, dtype=F32)
+    bad = torch.zeros(rows, units, dtype=torch.bool, device="cuda")
+    bad[4], bad[7], bad[:, 6] = True, True, True
+    assert torch.equal(got[~bad], want[~bad]) and bool(got[4].isnan().all()) and bool(got[:, 6].isnan().all())
+    g = _whole(gen, rows, units)
+    clean = tw.linear_bwd(g, torch.where(x.isfinite(), x, 0), torch.where(w.isfinite(), w, 0), dx_dtype=F32)
+    g2 = tw.linear_bwd(g, x, torch.where(w.isfinite(), w, 0), dx_dtype=F32)
+    assert torch.equal(g2.dx, clean.dx)
+    keep = torch.ones(cols, dtype=torch.bool, device="cuda")
+    keep[0] = keep[cols - 1] = False
+    assert torch.equal(g2.dw[:, keep], clean.dw[:, keep])
+
+
+def test_streams_and_graphs():
+    """Two captured graphs with a workspace each, and eager calls on another stream, between replays of both."""
+    require_gpu()
+    gen = _gen(8)
+    sets = []
+    for rows, cols, units in ((300, 4096, 129), (24, 1000, 640)):
+        x, w = _randn(gen, rows, cols, dtype=BF), _randn(gen, units, cols, scale=0.05, dtype=BF)
+        sets.append((x, w, _randn(gen, units), _randn(gen, rows, units, dtype=BF)))
+
+    def step(x, w, b, r):
+        pre = torch.empty(x.shape[0], w.shape[0], dtype=BF, device="cuda")
+        y = tw.linear(x, w, bias=b, act="gelu", residual=r, pre=pre)
+        return [y, pre, *tw.linear_bwd(y, x, w, act="gelu", pre=pre)]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        first = [step(*t) for t in sets]
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for t in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(*t))
+        graphs.append(g)
+    for i in range(4):
+        for t in sets:
+            t[0].copy_(_randn(gen, *t[0].shape, dtype=BF))
+        for g in graphs:
+            g.replay()
+        for t, out in zip(sets, outs):
+            for a, c in zip(out, step(*t)):
+                assert torch.equal(a, c)
+    assert len(first) == 2
