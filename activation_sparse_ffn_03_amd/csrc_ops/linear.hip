@@ -154,7 +154,7 @@ hipError_t launch_linear_dz(const LinearDzArgs& a, hipStream_t s) {
 hipError_t launch_linear(LinearLayout layout, const LinearPlan& plan, const LinearArgs& all, hipStream_t s) {
   LinearArgs a = all;
   a.splits = plan.splits;
-  if (plan.tile == 0) return launch_linear_direct(a, s);
+  if (plan.tile == LINEAR_DIRECT) return launch_linear_direct(a, s);
   LinearArgs first = a;
   if (a.splits > 1) {  // the sums alone; linear_join finishes them
     first.out.bias = nullptr;
@@ -162,9 +162,13 @@ hipError_t launch_linear(LinearLayout layout, const LinearPlan& plan, const Line
     first.out.pre = nullptr;
     first.out.act = TWELL_ACT_NONE;
   }
-  const hipError_t e = layout == LINEAR_ROWS    ? launch_linear_rows(plan.tile, first, s)
-                       : layout == LINEAR_MIXED ? launch_linear_mixed(plan.tile, first, s)
-                                                : launch_linear_cols(plan.tile, first, s);
+  hipError_t e;
+  if (layout == LINEAR_MIXED) e = launch_linear_mixed(plan.tile, first, s);
+  else if (layout == LINEAR_COLS) e = launch_linear_cols(plan.tile, first, s);
+  else if (plan.tile == LINEAR_BIG) e = launch_linear_rows_big(first, s);
+  else if (plan.tile == LINEAR_WIDE) e = launch_linear_rows_wide(first, s);
+  else if (plan.tile == LINEAR_MID) e = launch_linear_rows_mid(first, s);
+  else e = launch_linear_rows_few(first, s);
   return e != hipSuccess || a.splits == 1 ? e : launch_linear_join(a, s);
 }
 

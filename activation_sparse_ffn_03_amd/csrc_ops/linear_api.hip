@@ -42,7 +42,7 @@ struct ForwardLayout {
 ForwardLayout forward_layout(int64_t n, int32_t cols, int32_t units) {
   ForwardLayout L{};
   L.plan = twell::linear_plan(twell::LINEAR_ROWS, n, cols, units);
-  L.pad = L.plan.tile != 0 && cols % 8 != 0;
+  L.pad = L.plan.tile != twell::LINEAR_DIRECT && cols % 8 != 0;
   const size_t ld = (size_t)twell::linear_pad(cols);
   Pieces p;
   L.x = p.take(L.pad ? (size_t)n * ld * 2 : 0);

@@ -30,9 +30,20 @@ struct LinearTile {
   static constexpr int UG = BU / 32, TG = BT / 32;  // 1 KB loads of a wave and stage
   static constexpr int LOADS = UG + TG;
   static constexpr int MIN_STORES = 2 * FU * FT;    // of a wave at the end of a whole tile: 16 bytes of bf16 a lane
-  static_assert(LOADS / 2 + MIN_STORES <= 63, "vmcnt");
+  static_assert(LOADS + MIN_STORES <= 63, "vmcnt");
   static_assert(OCC * LDS <= 160 * 1024, "LDS of a compute unit");
 };
+
+// f(0), .. f(N - 1) with constants: the compiler gives up unrolling a loop of
+// that much code, and results with a variable index would go to scratch memory.
+template <typename F, int... I>
+__device__ __forceinline__ void linear_each_of(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void linear_each(F f) {
+  linear_each_of(f, std::make_integer_sequence<int, N>{});
+}
 
 // What a lane reads in place of k behind the last.
 __device__ const u32x4_t linear_zeros = {0u, 0u, 0u, 0u};
@@ -76,7 +87,7 @@ __device__ __forceinline__ const char* linear_uniform(const void* p) {
 // apart and share their keys.
 //
 // LDS with k lines: 2 B bytes a k; the 64 bytes of a fragment's 32 elements are
-// moved to group g ^ (k & 3), so that the transposing read (ds_read_b64_tr_b16: 16
+// moved to group g ^ turn(k), so that the transposing read (ds_read_b64_tr_b16: 16
 // lanes read 4 k of 16 elements, lane j gets element j of the four; checked
 // with an in-bounds probe) of eight k by 64 bytes meets every bank twice, the
 // least for its 512 bytes.
@@ -84,20 +95,24 @@ template <int B, int F, bool KROWS>
 struct LinearSide {
   static constexpr int LOADS = B / 32;
   static constexpr int PER = KROWS ? 512 / B : 8;  // lines a load covers
+  // Four neighbouring k meet four parts of 64 bytes of the banks: k & 3, or with
+  // two groups a line, which reach half of the banks, k / 2 & 1.
+  static __device__ __forceinline__ int turn(int k) { return B >= 128 ? k & 3 : k >> 1 & 1; }
   int line, col;     // this lane's line in a load of g = 0, and its bytes in the line
   uint32_t at[KROWS ? F : 4];  // LDS bytes of this lane's operands (fragments, or steps)
   uint32_t ld2;      // bytes of a line
+  uint32_t off[LOADS];  // bytes from a stage's first line and k to what this lane loads
 
   __device__ __forceinline__ LinearSide(const LinearOperand& o, int lane, int wave, int w) : ld2((uint32_t)(2 * o.ld)) {
     if constexpr (KROWS) {
       constexpr int SLOTS = 64 / PER;
       line = wave * PER + lane / SLOTS;
       const int slot = lane % SLOTS;
-      col = 16 * ((((slot >> 2) ^ (line & 3)) << 2) + (slot & 3));
+      col = 16 * ((((slot >> 2) ^ turn(line)) << 2) + (slot & 3));
       const int i16 = lane & 15, k = 8 * (lane >> 5) + (i16 >> 2);
 #pragma unroll
       for (int i = 0; i < F; ++i)
-        at[i] = k * (2 * B) + (((w * F + i) ^ (i16 >> 2)) << 6) + 32 * ((lane >> 4) & 1) + 8 * (i16 & 3);
+        at[i] = k * (2 * B) + (((w * F + i) ^ turn(k)) << 6) + 32 * ((lane >> 4) & 1) + 8 * (i16 & 3);
     } else {
       line = 8 * wave + (lane >> 3);
       col = 16 * ((lane & 7) ^ ((lane >> 3) ^ wave));
@@ -106,25 +121,23 @@ struct LinearSide {
       for (int ks = 0; ks < 4; ++ks) at[ks] = w * F * 4096 + row * 128 + ((2 * ks + (lane >> 5)) ^ key) * 16;
     }
   }
-  // Load g of a stage from `base` (its first line and k): lines, or elements of a
-  // line, behind `last` read that one. With TAIL k from `k_left` on are zeros.
-  template <bool TAIL>
-  __device__ __forceinline__ void issue(const char* base, int last, int k_left, int g, uint32_t lds, int wave) const {
-    const uint32_t to = lds + (wave + 4 * g) * 1024;
-    uint32_t off;
-    bool in;
-    if constexpr (KROWS) {
-      base += (int64_t)(4 * PER * g) * ld2;
-      off = (uint32_t)line * ld2 + (uint32_t)min(col, 2 * last - 14);
-      in = line + 4 * PER * g < k_left;
-    } else {
-      off = (uint32_t)min(line + 32 * g, last) * ld2 + (uint32_t)col;
-      in = col < 2 * k_left;
-    }
-    if constexpr (TAIL)
-      linear_dma_at(in ? base + off : reinterpret_cast<const char*>(&linear_zeros), to);
-    else
-      linear_dma(base, off, to);
+  // Lines, or elements of a line, behind `last` read that one.
+  __device__ __forceinline__ uint32_t offset(int g, int last) const {
+    if constexpr (KROWS) return (uint32_t)(line + 4 * PER * g) * ld2 + (uint32_t)min(col, 2 * last - 14);
+    else return (uint32_t)min(line + 32 * g, last) * ld2 + (uint32_t)col;
+  }
+  __device__ __forceinline__ void offsets(int last) {
+#pragma unroll
+    for (int g = 0; g < LOADS; ++g) off[g] = offset(g, last);
+  }
+  // Load g of a stage from `base` (its first line and k), whose offsets are known and k all there ...
+  __device__ __forceinline__ void issue(const char* base, int g, uint32_t lds, int wave) const {
+    linear_dma(base, off[g], lds + (wave + 4 * g) * 1024);
+  }
+  // ... and of any stage: k from `k_left` on are zeros.
+  __device__ __forceinline__ void issue_any(const char* base, int last, int k_left, int g, uint32_t lds, int wave) const {
+    const bool in = KROWS ? line + 4 * PER * g < k_left : col < 2 * k_left;
+    linear_dma_at(in ? base + offset(g, last) : reinterpret_cast<const char*>(&linear_zeros), lds + (wave + 4 * g) * 1024);
   }
   __device__ __forceinline__ u32x4_t read(const char* stage, int i, int ks) const {
     if constexpr (KROWS) {
@@ -141,122 +154,132 @@ struct LinearSide {
   }
 };
 
-// f(0), .. f(N - 1) with constants: the compiler gives up unrolling a loop of
-// that much code, and results with a variable index would go to scratch memory.
-template <typename F, int... I>
-__device__ __forceinline__ void linear_each_of(F f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void linear_each(F f) {
-  linear_each_of(f, std::make_integer_sequence<int, N>{});
-}
-
 // A wave's results to memory, through LDS, TOK rows by 64 units at a time, so
 // that a store writes whole lines (8 rows, 128 bytes of bf16 each) and the
-// epilogue reads the residual that way. Rows may begin at any element.
-template <class C, int ACT>
+// residual is read that way, one turn ahead. Rows may begin at any element. All
+// of it is one straight piece of code for results that are all there: where loads
+// lie in branches the compiler waits for everything, the stores too (61000
+// cycles a tile of 256 x 256, a fifth of 8192 x 8192 x 8192). At the result's
+// edges each lane looks at what there is.
+template <class C, int ACT, bool RES, bool WHOLE>
 __device__ __forceinline__ void linear_store(const LinearOut& o, const f32x16_t (&acc)[C::FU][C::FT], int64_t row0,
                                              int unit0, char* out) {
   const int lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5;
   const int col = 8 * (lane & 7);
-  constexpr int TOK = C::TOK, PASSES = TOK / 8;
-  float bias[C::FU / 2][8];
+  constexpr int TOK = C::TOK, PASSES = TOK / 8, PAIRS = C::FU / 2, HALVES = 32 / TOK, TURNS = C::FT * HALVES * PAIRS;
+  float bias[PAIRS][8];
 #pragma unroll
-  for (int i = 0; i < C::FU / 2; ++i) {
+  for (int i = 0; i < PAIRS; ++i) {
     const int unit = unit0 + 64 * i + col;
-    if (o.bias != nullptr) {
-      load_some<8>(o.bias, o.bias_bf16, unit, o.units - unit, bias[i]);
-    } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) bias[i][k] = 0.f;
-    }
+    for (int k = 0; k < 8; ++k) bias[i][k] = 0.f;
+    if (o.bias != nullptr && (WHOLE || unit < o.units)) load_some<8>(o.bias, o.bias_bf16, unit, WHOLE ? 8 : o.units - unit, bias[i]);
   }
-  linear_each<C::FT>([&](auto J) __attribute__((always_inline)) {
-    linear_each<32 / TOK>([&](auto H) __attribute__((always_inline)) {  // lanes of TOK rows write, all read
-      constexpr int j = decltype(J)::value, h = decltype(H)::value;
-      const bool mine = row / TOK == h;
+  // Turn t: rows [32 j + TOK h, + TOK), units [64 i, + 64), and its residual: 16
+  // bytes of bf16 or 32 of fp32 (of bf16 the same 16 twice).
+  u32x4_t res[2][PASSES][2];
+  auto fetch = [&](auto T) __attribute__((always_inline)) {
+    constexpr int t = decltype(T)::value, i = t % PAIRS, jh = t / PAIRS;
+    if constexpr (WHOLE && RES && t < TURNS) {
+#pragma unroll
+      for (int r = 0; r < PASSES; ++r) {
+        const int64_t at = (row0 + TOK * jh + 8 * r + (lane >> 3)) * o.units + unit0 + 64 * i + col;
+        const char* p = static_cast<const char*>(o.residual) + at * (o.res_bf16 ? 2 : 4);
+        res[t & 1][r][0] = *reinterpret_cast<const u32x4_a2_t*>(p);
+        res[t & 1][r][1] = *reinterpret_cast<const u32x4_a2_t*>(p + (o.res_bf16 ? 0 : 16));
+      }
+    }
+  };
+  fetch(std::integral_constant<int, 0>{});
+  linear_each<TURNS>([&](auto T) __attribute__((always_inline)) {
+    constexpr int t = decltype(T)::value, i = t % PAIRS, jh = t / PAIRS, j = jh / HALVES, h = jh % HALVES;
+    fetch(std::integral_constant<int, t + 1>{});
+    if (row / TOK == h) {  // lanes of TOK rows write, all read
       char* line = out + row % TOK * C::LINE;
-      const int64_t first = row0 + 32 * j + TOK * h + (lane >> 3);
-      float res[C::FU / 2][PASSES][8];
 #pragma unroll
-      for (int i = 0; i < C::FU / 2; ++i)
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int r = 0; r < PASSES; ++r) {
-          const int unit = unit0 + 64 * i + col;
-          if (o.residual != nullptr && first + 8 * r < o.rows) {
-            load_some<8>(o.residual, o.res_bf16, (first + 8 * r) * o.units + unit, o.units - unit, res[i][r]);
-          } else {
+        for (int q = 0; q < 4; ++q) {
+          const f32x16_t& v = acc[2 * i + k][j];
+          *reinterpret_cast<f32x4_t*>(line + 128 * k + 32 * q + 16 * half) =
+              f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        }
+    }
+    // A wave's LDS operations are done in their order; the statements around the
+    // reads keep the compiler to it, which sees no lane's write of what another
+    // reads.
+    asm volatile("" ::: "memory");
+    const int64_t first = row0 + TOK * jh;
+    if constexpr (WHOLE) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) res[i][r][k] = 0.f;
+      for (int r = 0; r < PASSES; ++r) {
+        float z[8], add[8];
+        const char* at = out + (8 * r + (lane >> 3)) * C::LINE + 4 * col;
+#pragma unroll
+        for (int k = 0; k < 8; k += 4) {
+          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(at + 4 * k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[k + e] = v[e];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          add[k] = 0.f;
+          if constexpr (RES) {
+            const u32x4_t* raw = res[t & 1][r];
+            const uint32_t b = k & 1 ? raw[0][k >> 1] & 0xFFFF0000u : raw[0][k >> 1] << 16;
+            add[k] = __uint_as_float(o.res_bf16 ? b : raw[k >> 2][k & 3]);
           }
         }
-      linear_each<C::FU / 2>([&](auto I) __attribute__((always_inline)) {
-        constexpr int i = decltype(I)::value;
-        if (mine) {
+        finish_units<ACT, 8, true>(o, first + 8 * r + (lane >> 3), unit0 + 64 * i + col, 8, z, bias[i], add);
+      }
+    } else {
+      const int unit = unit0 + 64 * i + col;
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+      for (int r = 0; r < PASSES; ++r) {
+        const int64_t at = first + 8 * r + (lane >> 3);
+        if (at >= o.rows || unit >= o.units) continue;
+        float z[8], add[8];
+        const char* from = out + (8 * r + (lane >> 3)) * C::LINE + 4 * col;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const f32x16_t& v = acc[2 * i + k][j];
-              *reinterpret_cast<f32x4_t*>(line + 128 * k + 32 * q + 16 * half) =
-                  f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-            }
+        for (int k = 0; k < 8; k += 4) {
+          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(from + 4 * k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[k + e] = v[e], add[k + e] = 0.f;
         }
-        // A wave's LDS operations are done in their order; the statements around
-        // the reads keep the compiler to it, which sees no lane's write of what
-        // another reads.
-        asm volatile("" ::: "memory");
-#pragma unroll
-        for (int r = 0; r < PASSES; ++r) {
-          float z[8];
-          const char* at = out + (8 * r + (lane >> 3)) * C::LINE + 4 * col;
-#pragma unroll
-          for (int k = 0; k < 8; k += 4) {
-            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(at + 4 * k);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[k + e] = v[e];
-          }
-          const int unit = unit0 + 64 * i + col;
-          if (first + 8 * r < o.rows && unit < o.units)
-            finish_units<ACT, 8>(o, first + 8 * r, unit, o.units - unit, z, bias[i], res[i][r]);
-        }
-        asm volatile("" ::: "memory");
-      });
-    });
+        if constexpr (RES) load_some<8>(o.residual, o.res_bf16, at * o.units + unit, o.units - unit, add);
+        finish_units<ACT, 8, true>(o, at, unit, o.units - unit, z, bias[i], add);
+      }
+    }
+    asm volatile("" ::: "memory");
   });
 }
 
 // Workgroup -> tile: each XCD takes a contiguous run of tiles, walked in
 // groups of 4 row blocks so that the tiles in flight share lines in L2.
-__device__ __forceinline__ void linear_tile_of(int64_t L, int64_t tb, int ub, int64_t& t, int& u) {
-  constexpr int kGroup = 4;
-  const int64_t per = (int64_t)kGroup * ub, first = L / per * kGroup;
-  const int g = (int)min(tb - first, (int64_t)kGroup), in = (int)(L % per);
-  t = first + in % g;
+__device__ __forceinline__ void linear_tile_of(uint32_t L, uint32_t tb, uint32_t ub, uint32_t& t, uint32_t& u) {
+  constexpr uint32_t kGroup = 4;
+  const uint32_t per = kGroup * ub, group = L / per, in = L - group * per;
+  const uint32_t g = min(tb - group * kGroup, kGroup);
   u = in / g;
+  t = group * kGroup + in - u * g;
 }
 
-// TAIL: k is not a whole number of stages, or there is one stage: loads run two
-// ahead, and the second one's k are zeros then.
-template <class C, bool PK, bool QK, bool TAIL, int ACT>
-__global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, int64_t tb, int ub) {
+template <class C, bool PK, bool QK, int ACT, bool RES>
+__global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32_t tb, uint32_t ub) {
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
   constexpr int FU = C::FU, FT = C::FT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wu = wave >> 1, wt = wave & 1;
-  const LinearSide<C::BU, FU, PK> P(a.p, lane, wave, wu);
-  const LinearSide<C::BT, FT, QK> Q(a.q, lane, wave, wt);
+  LinearSide<C::BU, FU, PK> P(a.p, lane, wave, wu);
+  LinearSide<C::BT, FT, QK> Q(a.q, lane, wave, wt);
   const int stages = (int)((a.k + 63) / 64);
 
   // This workgroup's items (tiles, for each split): every n-th (n workgroups on
-  // the XCD) of its XCD's run.
-  const int64_t tiles = tb * ub, items = tiles * a.splits;
-  const int xcd = blockIdx.x % 8;
-  const int64_t run = items / 8, extra = items % 8;
-  const int64_t end = (xcd + 1) * run + min((int64_t)xcd + 1, extra);
-  const int64_t stride = (gridDim.x + 7 - xcd) / 8;
-  int64_t L = xcd * run + min((int64_t)xcd, extra) + blockIdx.x / 8;
+  // the XCD) of its XCD's run. There are less than 2^24 of them.
+  const uint32_t tiles = tb * ub, items = tiles * a.splits;
+  const uint32_t xcd = blockIdx.x % 8, run = items / 8, extra = items % 8;
+  const uint32_t end = (xcd + 1) * run + min(xcd + 1, extra), stride = (gridDim.x + 7 - xcd) / 8;
+  uint32_t L = xcd * run + min(xcd, extra) + blockIdx.x / 8;
   if (L >= end) return;
 
   struct Item {
@@ -265,15 +288,15 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, int64_
     int64_t row0, k0;
     int unit0, count, split;  // stages: two at least
   };
-  auto item_at = [&](int64_t l) {
+  auto item_at = [&](uint32_t l) {
     Item r;
-    r.split = __builtin_amdgcn_readfirstlane((int)(l / tiles));
-    int64_t t;
-    int u;
+    r.split = a.splits == 1 ? 0 : __builtin_amdgcn_readfirstlane(l / tiles);
+    uint32_t t, u;
     linear_tile_of(l - r.split * tiles, tb, ub, t, u);
-    r.row0 = t * C::BT;
+    r.row0 = (int64_t)t * C::BT;
     r.unit0 = u * C::BU;
-    const int s0 = (int)((int64_t)r.split * stages / a.splits), s1 = (int)((int64_t)(r.split + 1) * stages / a.splits);
+    const int share = stages / a.splits, longer = stages % a.splits;  // the first splits have one stage more
+    const int s0 = r.split * share + min(r.split, longer), s1 = s0 + share + (r.split < longer ? 1 : 0);
     r.k0 = (int64_t)s0 * 64;
     r.count = __builtin_amdgcn_readfirstlane(max(s1 - s0, 2));
     r.p = linear_uniform(a.p.p + (PK ? r.k0 * a.p.ld + r.unit0 : r.unit0 * a.p.ld + r.k0));
@@ -296,14 +319,19 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, int64_
     r.q = (in ? c.q : n.q) + 128 * k * (QK ? a.q.ld : 1);
     r.p_last = in ? c.p_last : n.p_last;
     r.q_last = in ? c.q_last : n.q_last;
-    r.k_left = TAIL ? (int)min(a.k - (in ? c.k0 : n.k0) - 64 * k, (int64_t)64) : 64;
+    r.k_left = (int)min(a.k - (in ? c.k0 : n.k0) - 64 * k, (int64_t)64);
     return r;
   };
   const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(smem));
-  auto issue = [&](const Stage& s, uint32_t buf, int g) {
+  auto issue_any = [&](const Stage& s, uint32_t buf, int g) {
     const uint32_t at = lds0 + buf * C::STAGE;
-    if (g < C::UG) P.template issue<TAIL>(s.p, s.p_last, s.k_left, g, at, wave);
-    else Q.template issue<TAIL>(s.q, s.q_last, s.k_left, g - C::UG, at + C::BU * 128, wave);
+    if (g < C::UG) P.issue_any(s.p, s.p_last, s.k_left, g, at, wave);
+    else Q.issue_any(s.q, s.q_last, s.k_left, g - C::UG, at + C::BU * 128, wave);
+  };
+  auto issue = [&](const char* p, const char* q, uint32_t buf, int g) {
+    const uint32_t at = lds0 + buf * C::STAGE;
+    if (g < C::UG) P.issue(p, g, at, wave);
+    else Q.issue(q, g - C::UG, at + C::BU * 128, wave);
   };
 
   f32x16_t acc[FU][FT];
@@ -320,9 +348,9 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, int64_
   {
     const Stage s0 = stage_at(cur, cur, 0), s1 = stage_at(cur, cur, 1);
 #pragma unroll
-    for (int g = 0; g < C::LOADS; ++g) issue(s0, 0, g);
+    for (int g = 0; g < C::LOADS; ++g) issue_any(s0, 0, g);
 #pragma unroll
-    for (int g = 0; g < C::LOADS; ++g) issue(s1, 1, g);
+    for (int g = 0; g < C::LOADS; ++g) issue_any(s1, 1, g);
   }
   wait_vmcnt<C::LOADS>();
   lds_barrier();
@@ -342,14 +370,16 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, int64_
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
 
-    for (int kt = 0; kt < cur.count; ++kt) {
-      // Four steps of 16 k. All operands of the stage are in registers when the
-      // second step ends, so that its LDS can be filled again during the third
-      // and fourth; the next stage's first operands are read in the fourth.
-      // Loads are spread over two steps: a wave that issues them at once waits
-      // for the address unit and keeps its matrix core waiting.
-      const Stage ahead = stage_at(cur, next, kt + 2);
-      constexpr int OPS = FU + FT, M = FU * FT;  // operands and matrix instructions of a step
+    // Stage kt. Its four steps of 16 k are M matrix instructions each, with other
+    // work dealt to them: first the reads of what the first step has not got, then
+    // (barrier: every wave has read all of this stage) the loads of the stage
+    // after next into its place, spread because a wave that issues them at once
+    // waits for the address unit and keeps its matrix core waiting; last (wait and
+    // barrier: the next stage has landed) the next stage's first operands. `load`
+    // is called with the number of a load.
+    auto stage = [&](int kt, auto load) __attribute__((always_inline)) {
+      constexpr int OPS = FU + FT, M = FU * FT, S = 4 * M;  // operands and matrix instructions of a step, of the stage
+      constexpr int READ = S * 17 / 64, FREE = S * 24 / 64, LOAD = S * 56 / 64, NEXT = S * 48 / 64, DONE = S * 57 / 64;
       auto read = [&](int r) {  // read r of the 3 OPS behind the first step's operands
         const int ks = 1 + r / OPS, k = r % OPS;
         if (k < FU) av[ks][k] = read_a(k, ks, buf);
@@ -359,43 +389,50 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, int64_
         if (r < FU) av[0][r] = read_a(r, 0, buf ^ 1);
         else bv[0][r - FU] = read_b(r - FU, 0, buf ^ 1);
       };
-      // Operation k of n that are dealt to slots [0, m): those of slot s.
-      auto first_of = [](int s, int n, int m) { return s >= m ? n : s * n / m; };
-      auto step = [&](auto KS) {
-        constexpr int ks = decltype(KS)::value;
-#pragma unroll
-        for (int s = 0; s < M; ++s) {
-          const int i = s / FT, j = s % FT;
-          acc[i][j] = mfma(av[ks][i], bv[ks][j], acc[i][j]);
-          if constexpr (ks < 2) {  // done half a step before the barrier
-#pragma unroll
-            for (int r = first_of(ks * M + s, 3 * OPS, M + M / 2); r < first_of(ks * M + s + 1, 3 * OPS, M + M / 2); ++r)
-              read(r);
-          } else {
-#pragma unroll
-            for (int g = first_of((ks - 2) * M + s, C::LOADS, 2 * M); g < first_of((ks - 2) * M + s + 1, C::LOADS, 2 * M); ++g)
-              issue(ahead, buf, g);
-          }
-          if constexpr (ks == 3) {
-#pragma unroll
-            for (int r = first_of(s, OPS, M / 2 + 1); r < first_of(s + 1, OPS, M / 2 + 1); ++r) read_next(r);
-          }
+      // Of n operations that are dealt to slots [from, to): those before slot s.
+      constexpr auto before = [](int s, int n, int from, int to) { return s <= from ? 0 : s >= to ? n : (s - from) * n / (to - from); };
+      linear_each<S>([&](auto T) __attribute__((always_inline)) {
+        constexpr int t = decltype(T)::value, ks = t / M, i = t % M / FT, j = t % FT;
+        if constexpr (t == FREE) {
+          lds_barrier();
           __builtin_amdgcn_sched_barrier(0);
         }
-      };
-      step(std::integral_constant<int, 0>{});
-      step(std::integral_constant<int, 1>{});
-      lds_barrier();  // every wave has read all of this stage
-      __builtin_amdgcn_sched_barrier(0);
-      step(std::integral_constant<int, 2>{});
-      // The next stage has landed once only this step's loads are pending, and
-      // in an item's first stage the stores of the one before, which were
-      // asked for later than it.
-      linear_wait_either<C::LOADS / 2 + C::MIN_STORES, C::LOADS / 2>(stores & (uint32_t)(kt == 0));
-      lds_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-      step(std::integral_constant<int, 3>{});
+        if constexpr (t == NEXT) {
+          // only this stage's loads may be pending, and in an item's first stage
+          // the stores of the one before, which were asked for later than the next's
+          constexpr int pending = before(NEXT, C::LOADS, FREE, LOAD);
+          linear_wait_either<pending + C::MIN_STORES, pending>(stores & (uint32_t)(kt == 0));
+          lds_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        acc[i][j] = mfma(av[ks][i], bv[ks][j], acc[i][j]);
+#pragma unroll
+        for (int r = before(t, 3 * OPS, 0, READ); r < before(t + 1, 3 * OPS, 0, READ); ++r) read(r);
+#pragma unroll
+        for (int g = before(t, C::LOADS, FREE, LOAD); g < before(t + 1, C::LOADS, FREE, LOAD); ++g) load(g);
+        if constexpr (t >= NEXT) {
+#pragma unroll
+          for (int r = before(t, OPS, NEXT, DONE); r < before(t + 1, OPS, NEXT, DONE); ++r) read_next(r);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
       buf ^= 1;
+    };
+    // While the stage after next is one of this item's, and not its last, which
+    // may have fewer k, its loads' offsets do not change and cost nothing.
+    P.offsets(cur.p_last);
+    Q.offsets(cur.q_last);
+    const char *p = linear_uniform(cur.p + 256 * (PK ? a.p.ld : 1)), *q = linear_uniform(cur.q + 256 * (QK ? a.q.ld : 1));
+    int kt = 0;
+    for (; kt < cur.count - 3; ++kt) {
+      stage(kt, [&](int g) { issue(p, q, buf, g); });
+      p += 128 * (PK ? a.p.ld : 1);
+      q += 128 * (QK ? a.q.ld : 1);
+    }
+#pragma unroll 1
+    for (; kt < cur.count; ++kt) {
+      const Stage ahead = stage_at(cur, next, kt + 2);
+      stage(kt, [&](int g) { issue_any(ahead, buf, g); });
     }
 
     LinearOut o = a.out;
@@ -405,10 +442,13 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, int64_
     }
     const int64_t row0 = cur.row0 + wt * FT * 32;
     const int unit0 = cur.unit0 + wu * FU * 32;
-    linear_store<C, ACT>(o, acc, row0, unit0, smem + 2 * C::STAGE + wave * C::OUT);
+    char* out = smem + 2 * C::STAGE + wave * C::OUT;
+    const bool whole = row0 + FT * 32 <= a.out.rows && unit0 + FU * 32 <= a.out.units;
+    if (whole) linear_store<C, ACT, RES, true>(o, acc, row0, unit0, out);
+    else linear_store<C, ACT, RES, false>(o, acc, row0, unit0, out);
     if (!more) break;
     // at the result's edges some have nothing to store, and may not have been issued
-    stores = row0 + FT * 32 <= a.out.rows && unit0 + FU * 32 <= a.out.units;
+    stores = whole;
     cur = next;
     L += stride;
   }
@@ -417,18 +457,33 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, int64_
 
 using LinearBig = LinearTile<4, 4, 1>;
 using LinearMid = LinearTile<2, 2, 2>;
+using LinearWide = LinearTile<4, 2, 1>;
+using LinearFew = LinearTile<2, 1, 2>;
 
-template <class C, bool PK, bool QK, int ACT>
+template <class C, bool PK, bool QK, int ACT, bool RES>
 hipError_t launch_linear_tile(const LinearArgs& a, hipStream_t s) {
-  const int64_t tb = (a.out.rows + C::BT - 1) / C::BT;
-  const int ub = (a.out.units + C::BU - 1) / C::BU;
+  const int64_t tb = (a.out.rows + C::BT - 1) / C::BT, ub = (a.out.units + C::BU - 1) / C::BU;
   const int64_t items = tb * ub * a.splits, fit = 256 * C::OCC;  // workgroups that run at a time
+  if (items >= kLinearMaxItems) return hipErrorInvalidValue;
   const dim3 grid((unsigned)(items < fit ? items : fit));
-  if (a.k % 64 == 0 && a.k > 64)
-    TWELL_LAUNCH("linear_tiled", (linear_tiled<C, PK, QK, false, ACT>), grid, 256, 0, s, a, tb, ub);
-  else
-    TWELL_LAUNCH("linear_tiled", (linear_tiled<C, PK, QK, true, ACT>), grid, 256, 0, s, a, tb, ub);
+  TWELL_LAUNCH("linear_tiled", (linear_tiled<C, PK, QK, ACT, RES>), grid, 256, 0, s, a, (uint32_t)tb, (uint32_t)ub);
   return hipGetLastError();
+}
+
+// y = x w^T with the epilogue that the call asks for.
+template <class C, int ACT>
+hipError_t launch_linear_res(const LinearArgs& a, hipStream_t s) {
+  return a.out.residual != nullptr ? launch_linear_tile<C, false, false, ACT, true>(a, s)
+                                   : launch_linear_tile<C, false, false, ACT, false>(a, s);
+}
+template <class C>
+hipError_t launch_linear_act(const LinearArgs& a, hipStream_t s) {
+  switch (a.splits > 1 ? TWELL_ACT_NONE : a.out.act) {
+    case TWELL_ACT_RELU: return launch_linear_res<C, TWELL_ACT_RELU>(a, s);
+    case TWELL_ACT_SILU: return launch_linear_res<C, TWELL_ACT_SILU>(a, s);
+    case TWELL_ACT_GELU: return launch_linear_res<C, TWELL_ACT_GELU>(a, s);
+    default: return launch_linear_res<C, TWELL_ACT_NONE>(a, s);
+  }
 }
 
 }  // namespace twell

@@ -310,34 +310,94 @@ enum LinearLayout {
   LINEAR_COLS    // both with k lines: dw = dz^T x
 };
 constexpr int kLinearMaxCols = 1 << 20;  // a line's bytes times a tile's lines stay below 2^32
+constexpr int64_t kLinearMaxItems = 1 << 24;  // tiles times splits of a launch
 constexpr int kLinearStage = 64;         // k of a stage of the tiles
 // Elements that a line has at least when a tile reads it: whole 16 bytes.
 inline int64_t linear_pad(int64_t n) { return (n + 7) / 8 * 8; }
 
-// How a product of `rows` x `units` results over k runs.
+// How a product of `rows` x `units` results over k runs: straight from memory
+// (LINEAR_ROWS only), or in tiles through LDS.
+enum LinearTileSize {
+  LINEAR_DIRECT,
+  LINEAR_FEW,   // 64 rows x 128 units, two workgroups a compute unit
+  LINEAR_MID,   // 128 x 128, two workgroups a compute unit
+  LINEAR_WIDE,  // 128 rows x 256 units
+  LINEAR_BIG    // 256 x 256
+};
 struct LinearPlan {
-  int tile;    // 0: straight from memory (LINEAR_ROWS only), 128 or 256: tiles of that size through LDS
+  LinearTileSize tile;
   int splits;  // of k; 1 straight from memory
 };
+// Estimates (us). Tiles: 3.5 a launch, for each item of the busiest compute unit
+// its stages and an end, and where k is split another launch and the partial sums
+// written and read. A stage takes longer when all compute units are at it.
+// Measured, splits : us (bf16 results; rows x k x units; ROWS, then MIXED and COLS):
+//                        FEW               MID          WIDE           BIG
+//   128 x 1024 x 1024    1: 8.5            1: 11.2      1: 15.5        1: 29.4
+//   64 x 5632 x 2048     1: 24.5 10: 13.5  10: 15.9     10: 20.9       10: 43.2
+//   64 x 4096 x 11008    1: 28.8 2: 23.0   2: 25.0      2: 29.6        5: 31.1
+//   300 x 8192 x 700     1: 47.8 8: 16.6   10: 17.6     10: 21.2       16: 28.4
+//   1000 x 512 x 1000    1: 7.5 2: 12.3    1: 9.6       1: 12.5        1: 20.1
+//   512 x 4096 x 4096    1: 28.9           1: 30.9 2: 27.1  2: 32.4    4: 35.4
+//   1024 x 4096 x 4096   1: 41.0           1: 34.8 2: 43.0  1: 44.4    3: 49.6
+//   2048 x 4096 x 4096   1: 77.2           1: 60.7      1: 54.7 2: 80.6  1: 73.9
+//   4096 x 4096 x 4096   1: 149            1: 116       1: 107         1: 94.8
+//   5000 x 256 x 5001    1: 35.0           1: 31.9      1: 42.6        1: 41.3
+//   8192 x 5632 x 2048   1: 241            1: 165       1: 145         1: 128
+//   1000 x 8192 x 1024   1: 48.8 4: 30.1   4: 31.7      6: 41.3        10: 64.1
+//   1021 x 509 x 1000    1: 8.2 2: 13.0    1: 10.0      1: 14.4        1: 22.5
+//   512 x 8192 x 512     6: 16.9           6: 19.0      10: 22.4       12: 28.7
+//   5632 x 8192 x 2048   1: 284            1: 173       1: 188 2: 182  1: 151
+inline double linear_tile_us(LinearTileSize tile, int64_t rows, int64_t k, int units, int splits) {
+  const int64_t br = tile == LINEAR_BIG ? 256 : tile == LINEAR_FEW ? 64 : 128;
+  const int64_t bu = tile == LINEAR_BIG || tile == LINEAR_WIDE ? 256 : 128;
+  const int64_t items = ((rows + br - 1) / br) * ((units + bu - 1) / bu) * splits, n = (items + 255) / 256;
+  const double load = items < 256 ? items / 256.0 : 1.0;
+  const double stage = tile == LINEAR_BIG    ? 1.0 + 0.32 * load
+                       : tile == LINEAR_WIDE ? 0.57 + 0.15 * load
+                       : tile == LINEAR_MID  ? 0.38 + 0.05 * load
+                       : n == 1              ? 0.35
+                                             : 0.28;
+  const double end = tile == LINEAR_BIG ? 9.0 : tile == LINEAR_WIDE ? 4.5 : tile == LINEAR_MID ? 2.0 : 1.2;
+  const int64_t stages = ((k + kLinearStage - 1) / kLinearStage + splits - 1) / splits;
+  const double body = n * stages * stage, reads = 2.0 * k * (rows + units) / 6.5e6;
+  const double join = splits > 1 ? 2.5 + 8.0 * splits * rows * units / 5.5e6 : 0;
+  return 3.5 + (body > reads ? body : reads) + n * end + join;
+}
+// Straight from memory: w once, and 8 lines of x for every 8 rows and 16 units
+// (measured: 8, 16, 24, 32 x 4096 x 11008 16.6, 20.5, 23.3, 26.8; x 5632 x 2048
+// 6.1, 7.6, 8.7, 9.8; the tiles of few rows take 22 and 13).
+inline double linear_direct_us(int64_t rows, int64_t k, int units) {
+  const double groups = (units + 15) / 16 / 256.0, steps = (double)((k + 63) / 64);
+  return 2.5 + 2.0 * k * units / 8.6e6 + (groups > 1 ? groups : 1) * steps * 8 * ((rows + 7) / 8) * 0.0022;
+}
 inline LinearPlan linear_plan(LinearLayout layout, int64_t rows, int64_t k, int units) {
-  if (rows == 0 || k == 0) return {128, 1};  // nothing is launched
-  if (layout == LINEAR_ROWS && rows <= 64) return {0, 1};
+  if (rows == 0 || k == 0) return {LINEAR_FEW, 1};  // nothing is launched
   const int64_t stages = (k + kLinearStage - 1) / kLinearStage;
-  const int64_t mid = ((rows + 127) / 128) * ((units + 127) / 128), big = ((rows + 255) / 256) * ((units + 255) / 256);
-  if (big >= 256) return {256, 1};
-  int64_t splits = 512 / mid;
-  if (splits > stages / 4) splits = stages / 4;
-  if (splits > 16) splits = 16;
-  return {128, (int)(splits < 1 ? 1 : splits)};
+  const bool direct = layout == LINEAR_ROWS && rows <= 32;
+  LinearPlan best{LINEAR_DIRECT, 1};
+  double least = direct ? linear_direct_us(rows, k, units) : 1e30;
+  for (int t = LINEAR_FEW; t <= LINEAR_BIG; ++t)
+    for (int s = 1; s <= 16 && (s == 1 || 2 * s <= stages); ++s) {  // two stages at least
+      const double us = linear_tile_us((LinearTileSize)t, rows, k, units, s);
+      if (us < least) {
+        least = us;
+        best = {(LinearTileSize)t, s};
+      }
+    }
+  return best;
 }
 inline size_t linear_part_bytes(const LinearPlan& p, int64_t rows, int units) {
   return p.splits > 1 ? (size_t)p.splits * rows * units * 4 : 0;
 }
 // Runs the product by its plan: tiles or straight from memory, and the splits' sums.
 hipError_t launch_linear(LinearLayout layout, const LinearPlan& plan, const LinearArgs& a, hipStream_t s);
-hipError_t launch_linear_rows(int tile, const LinearArgs& a, hipStream_t s);
-hipError_t launch_linear_mixed(int tile, const LinearArgs& a, hipStream_t s);
-hipError_t launch_linear_cols(int tile, const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_rows_big(const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_rows_wide(const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_rows_mid(const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_rows_few(const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_mixed(LinearTileSize tile, const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_cols(LinearTileSize tile, const LinearArgs& a, hipStream_t s);
 hipError_t launch_linear_direct(const LinearArgs& a, hipStream_t s);
 hipError_t launch_linear_zero(const LinearOut& o, hipStream_t s);  // y = 0
 // Adds the splits' sums in their order and finishes them.
