@@ -41,8 +41,8 @@ struct ForwardLayout {
 };
 ForwardLayout forward_layout(int64_t n, int32_t cols, int32_t units) {
   ForwardLayout L{};
-  L.plan = twell::linear_plan(twell::LINEAR_ROWS, n, cols, units);
-  L.pad = L.plan.tile != twell::LINEAR_DIRECT && cols % 8 != 0;
+  L.plan = twell::linear_plan(twell::LINEAR_ROWS, n, cols, units, cols % 8 != 0);
+  L.pad = L.plan.pad;
   const size_t ld = (size_t)twell::linear_pad(cols);
   Pieces p;
   L.x = p.take(L.pad ? (size_t)n * ld * 2 : 0);
@@ -63,11 +63,11 @@ struct BackwardLayout {
 BackwardLayout backward_layout(int64_t n, int32_t cols, int32_t units, bool d_out_bf16, int32_t act, uint32_t wanted) {
   BackwardLayout L{};
   const bool dx = wanted & TWELL_LINEAR_DX, dw = wanted & TWELL_LINEAR_DW;
-  L.dx = twell::linear_plan(twell::LINEAR_MIXED, n, units, cols);
-  L.dw = twell::linear_plan(twell::LINEAR_COLS, units, n, cols);
+  L.dx = twell::linear_plan(twell::LINEAR_MIXED, n, units, cols, cols % 8 != 0);
+  L.dw = twell::linear_plan(twell::LINEAR_COLS, units, n, cols, cols % 8 != 0);
   L.dz = (dx || dw) && (act != TWELL_ACT_NONE || !d_out_bf16 || units % 8 != 0);
-  L.pad_x = dw && cols % 8 != 0;
-  L.pad_w = dx && cols % 8 != 0;
+  L.pad_x = dw && L.dw.pad;
+  L.pad_w = dx && L.dx.pad;
   const size_t ld = (size_t)twell::linear_pad(cols);
   Pieces p;
   L.dz_at = p.take(L.dz ? (size_t)n * twell::linear_pad(units) * 2 : 0);
@@ -122,6 +122,7 @@ twell_status twell_linear(int64_t n, int32_t cols, int32_t units, const void* x,
   a.q = {static_cast<const uint16_t*>(x), cols};
   a.k = cols;
   a.out = {n, units, bias, residual, pre, y, bias_dtype == TWELL_BF16, res_dtype == TWELL_BF16, y_dtype == TWELL_BF16, act};
+  a.any = cols % 8 != 0 && !L.pad;
   if (L.pad) {
     const int64_t ld = twell::linear_pad(cols);
     hipError_t e = twell::launch_linear_pad(x, n, cols, base + L.x, ld, s);
@@ -202,6 +203,7 @@ twell_status twell_linear_bwd(int64_t n, int32_t cols, int32_t units, twell_dtyp
       if ((e = twell::launch_linear_pad(w, units, cols, base + L.w, ld, s)) != hipSuccess) return hip_status(e, "twell_linear_bwd");
       a.p = {reinterpret_cast<const uint16_t*>(base + L.w), ld};
     }
+    a.any = cols % 8 != 0 && !L.pad_w;
     a.q = dz;
     a.k = units;
     a.out = {n, cols, nullptr, nullptr, nullptr, dx, 0, 0, dx_dtype == TWELL_BF16, TWELL_ACT_NONE};
@@ -215,6 +217,7 @@ twell_status twell_linear_bwd(int64_t n, int32_t cols, int32_t units, twell_dtyp
       if ((e = twell::launch_linear_pad(x, n, cols, base + L.x, ld, s)) != hipSuccess) return hip_status(e, "twell_linear_bwd");
       a.p = {reinterpret_cast<const uint16_t*>(base + L.x), ld};
     }
+    a.any = cols % 8 != 0 && !L.pad_x;
     a.q = dz;
     a.k = n;
     e = twell::launch_linear(twell::LINEAR_COLS, L.dw, a, s);

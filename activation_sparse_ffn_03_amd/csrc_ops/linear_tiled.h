@@ -121,9 +121,12 @@ struct LinearSide {
       for (int ks = 0; ks < 4; ++ks) at[ks] = w * F * 4096 + row * 128 + ((2 * ks + (lane >> 5)) ^ key) * 16;
     }
   }
-  // Lines, or elements of a line, behind `last` read that one.
+  // Lines, or elements of a line, behind `last` read that one. 16 bytes of a
+  // line that begin before its end may reach into the next line: there they are
+  // the result's columns that are not stored.
+  __device__ __forceinline__ int reach(int last) const { return min(col, last / 8 * 16); }
   __device__ __forceinline__ uint32_t offset(int g, int last) const {
-    if constexpr (KROWS) return (uint32_t)(line + 4 * PER * g) * ld2 + (uint32_t)min(col, 2 * last - 14);
+    if constexpr (KROWS) return (uint32_t)(line + 4 * PER * g) * ld2 + (uint32_t)reach(last);
     else return (uint32_t)min(line + 32 * g, last) * ld2 + (uint32_t)col;
   }
   __device__ __forceinline__ void offsets(int last) {
@@ -138,6 +141,34 @@ struct LinearSide {
   __device__ __forceinline__ void issue_any(const char* base, int last, int k_left, int g, uint32_t lds, int wave) const {
     const bool in = KROWS ? line + 4 * PER * g < k_left : col < 2 * k_left;
     linear_dma_at(in ? base + offset(g, last) : reinterpret_cast<const char*>(&linear_zeros), lds + (wave + 4 * g) * 1024);
+  }
+  // Operands whose lines begin at any element go through registers: load g of a
+  // stage whose offsets are known and k all there, ...
+  __device__ __forceinline__ u32x4_t fetch(const char* base, int g) const {
+    return *reinterpret_cast<const u32x4_a2_t*>(base + off[g]);
+  }
+  // ... of any stage. Where 16 bytes would reach behind the operand (a line's last
+  // k; with k lines the elements behind the last, in k's last stage) they are
+  // the 16 that end there, and fix() moves them down; k behind the last are
+  // zeros then.
+  __device__ __forceinline__ u32x4_t fetch_any(const char* base, int last, int k_left, int g) const {
+    int64_t at;
+    if constexpr (KROWS) at = (int64_t)min(line + 4 * PER * g, k_left - 1) * ld2 + (k_left > 64 ? reach(last) : min(col, 2 * last - 14));
+    else at = (int64_t)min(line + 32 * g, last) * ld2 + min(col, 2 * k_left - 16);
+    return *reinterpret_cast<const u32x4_a2_t*>(base + at);
+  }
+  __device__ __forceinline__ u32x4_t fix(u32x4_t v, int last, int k_left, int g) const {
+    const int s = KROWS ? k_left > 64 ? 0 : col / 2 + 7 - last : col / 2 + 8 - k_left;  // elements behind the last
+    if (s > 0 && s < 8) {
+      if (s & 4) v = u32x4_t{v[2], v[3], 0u, 0u};
+      if (s & 2) v = u32x4_t{v[1], v[2], v[3], 0u};
+      if (s & 1) v = u32x4_t{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+    }
+    const bool none = KROWS ? line + 4 * PER * g >= k_left : s >= 8;
+    return none ? u32x4_t{0u, 0u, 0u, 0u} : v;
+  }
+  __device__ __forceinline__ void put(const u32x4_t& v, char* side, int g, int wave, int lane) const {
+    *reinterpret_cast<u32x4_t*>(side + (wave + 4 * g) * 1024 + 16 * lane) = v;
   }
   __device__ __forceinline__ u32x4_t read(const char* stage, int i, int ks) const {
     if constexpr (KROWS) {
@@ -264,7 +295,8 @@ __device__ __forceinline__ void linear_tile_of(uint32_t L, uint32_t tb, uint32_t
   t = group * kGroup + in - u * g;
 }
 
-template <class C, bool PK, bool QK, int ACT, bool RES>
+// PA, QA: the operand's lines begin at any element (and hold 8 or more).
+template <class C, bool PK, bool QK, bool PA, bool QA, int ACT, bool RES>
 __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32_t tb, uint32_t ub) {
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
   constexpr int FU = C::FU, FT = C::FT;
@@ -286,8 +318,9 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32
     const char *p, *q;   // first line and k
     int p_last, q_last;  // lines (or elements of a line) that there are, less one
     int64_t row0, k0;
-    int unit0, count, split;  // stages: two at least
+    int unit0, count, split;  // stages: LEAST at least, behind the last k's of zeros
   };
+  constexpr int LEAST = PA || QA ? 3 : 2;
   auto item_at = [&](uint32_t l) {
     Item r;
     r.split = a.splits == 1 ? 0 : __builtin_amdgcn_readfirstlane(l / tiles);
@@ -298,13 +331,11 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32
     const int share = stages / a.splits, longer = stages % a.splits;  // the first splits have one stage more
     const int s0 = r.split * share + min(r.split, longer), s1 = s0 + share + (r.split < longer ? 1 : 0);
     r.k0 = (int64_t)s0 * 64;
-    r.count = __builtin_amdgcn_readfirstlane(max(s1 - s0, 2));
+    r.count = __builtin_amdgcn_readfirstlane(max(s1 - s0, LEAST));
     r.p = linear_uniform(a.p.p + (PK ? r.k0 * a.p.ld + r.unit0 : r.unit0 * a.p.ld + r.k0));
     r.q = linear_uniform(a.q.p + (QK ? r.k0 * a.q.ld + r.row0 : r.row0 * a.q.ld + r.k0));
-    // with k lines whole 16 bytes are read: to the next multiple of 8
-    r.p_last = PK ? ((min(C::BU, a.out.units - r.unit0) + 7) & ~7) - 1 : min(C::BU, a.out.units - r.unit0) - 1;
-    const int rows = (int)min((int64_t)C::BT, a.out.rows - r.row0);
-    r.q_last = QK ? ((rows + 7) & ~7) - 1 : rows - 1;
+    r.p_last = min(C::BU, a.out.units - r.unit0) - 1;
+    r.q_last = (int)min((int64_t)C::BT, a.out.rows - r.row0) - 1;
     return r;
   };
   struct Stage {
@@ -319,19 +350,48 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32
     r.q = (in ? c.q : n.q) + 128 * k * (QK ? a.q.ld : 1);
     r.p_last = in ? c.p_last : n.p_last;
     r.q_last = in ? c.q_last : n.q_last;
-    r.k_left = (int)min(a.k - (in ? c.k0 : n.k0) - 64 * k, (int64_t)64);
+    r.k_left = (int)min(a.k - (in ? c.k0 : n.k0) - 64 * k, (int64_t)128);
     return r;
   };
   const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(smem));
-  auto issue_any = [&](const Stage& s, uint32_t buf, int g) {
-    const uint32_t at = lds0 + buf * C::STAGE;
-    if (g < C::UG) P.issue_any(s.p, s.p_last, s.k_left, g, at, wave);
-    else Q.issue_any(s.q, s.q_last, s.k_left, g - C::UG, at + C::BU * 128, wave);
+  u32x4_t sp[PA ? C::UG : 1], sq[QA ? C::TG : 1];  // the stage after those in LDS
+  auto side_p = [&](uint32_t buf) { return smem + buf * C::STAGE; };
+  auto side_q = [&](uint32_t buf) { return smem + buf * C::STAGE + C::BU * 128; };
+  // Load g of stage `s` into LDS; through registers: of `s`, which they hold, and
+  // of the one behind it, `after`, into them.
+  auto fetch_any = [&](const Stage& s, int g) __attribute__((always_inline)) {
+    if (g < C::UG) {
+      if constexpr (PA) sp[g] = P.fetch_any(s.p, s.p_last, s.k_left, g);
+    } else {
+      if constexpr (QA) sq[g - C::UG] = Q.fetch_any(s.q, s.q_last, s.k_left, g - C::UG);
+    }
   };
-  auto issue = [&](const char* p, const char* q, uint32_t buf, int g) {
-    const uint32_t at = lds0 + buf * C::STAGE;
-    if (g < C::UG) P.issue(p, g, at, wave);
-    else Q.issue(q, g - C::UG, at + C::BU * 128, wave);
+  auto issue_any = [&](const Stage& s, const Stage& after, uint32_t buf, int g) __attribute__((always_inline)) {
+    if (g < C::UG) {
+      if constexpr (PA) P.put(P.fix(sp[g], s.p_last, s.k_left, g), side_p(buf), g, wave, lane);
+      else P.issue_any(s.p, s.p_last, s.k_left, g, lds0 + buf * C::STAGE, wave);
+    } else {
+      if constexpr (QA) Q.put(Q.fix(sq[g - C::UG], s.q_last, s.k_left, g - C::UG), side_q(buf), g - C::UG, wave, lane);
+      else Q.issue_any(s.q, s.q_last, s.k_left, g - C::UG, lds0 + buf * C::STAGE + C::BU * 128, wave);
+    }
+    fetch_any(after, g);
+  };
+  auto issue = [&](const char* p, const char* q, const char* p_after, const char* q_after, uint32_t buf, int g) __attribute__((always_inline)) {
+    if (g < C::UG) {
+      if constexpr (PA) {
+        P.put(sp[g], side_p(buf), g, wave, lane);
+        sp[g] = P.fetch(p_after, g);
+      } else {
+        P.issue(p, g, lds0 + buf * C::STAGE, wave);
+      }
+    } else {
+      if constexpr (QA) {
+        Q.put(sq[g - C::UG], side_q(buf), g - C::UG, wave, lane);
+        sq[g - C::UG] = Q.fetch(q_after, g - C::UG);
+      } else {
+        Q.issue(q, g - C::UG, lds0 + buf * C::STAGE + C::BU * 128, wave);
+      }
+    }
   };
 
   f32x16_t acc[FU][FT];
@@ -346,13 +406,16 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32
   // last one they read it again, unused.
   Item cur = item_at(L);
   {
-    const Stage s0 = stage_at(cur, cur, 0), s1 = stage_at(cur, cur, 1);
+    const Stage s0 = stage_at(cur, cur, 0), s1 = stage_at(cur, cur, 1), s2 = stage_at(cur, cur, 2);
 #pragma unroll
-    for (int g = 0; g < C::LOADS; ++g) issue_any(s0, 0, g);
+    for (int g = 0; g < C::LOADS; ++g) fetch_any(s0, g);
 #pragma unroll
-    for (int g = 0; g < C::LOADS; ++g) issue_any(s1, 1, g);
+    for (int g = 0; g < C::LOADS; ++g) issue_any(s0, s1, 0, g);
+#pragma unroll
+    for (int g = 0; g < C::LOADS; ++g) issue_any(s1, s2, 1, g);
   }
-  wait_vmcnt<C::LOADS>();
+  if constexpr (PA != QA) wait_vmcnt<0>();
+  else if constexpr (!PA) wait_vmcnt<C::LOADS>();
   lds_barrier();
 #pragma unroll
   for (int i = 0; i < FU; ++i) av[0][i] = read_a(i, 0, 0);
@@ -398,10 +461,11 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32
           __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (t == NEXT) {
-          // only this stage's loads may be pending, and in an item's first stage
-          // the stores of the one before, which were asked for later than the next's
+          // only this stage's loads may be pending (one each, into LDS or registers),
+          // and in an item's first stage the stores of the one before, which were
+          // asked for later than the next's
           constexpr int pending = before(NEXT, C::LOADS, FREE, LOAD);
-          linear_wait_either<pending + C::MIN_STORES, pending>(stores & (uint32_t)(kt == 0));
+          if constexpr (!(PA && QA)) linear_wait_either<pending + C::MIN_STORES, pending>(stores & (uint32_t)(kt == 0));
           lds_barrier();
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -418,21 +482,22 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32
       });
       buf ^= 1;
     };
-    // While the stage after next is one of this item's, and not its last, which
-    // may have fewer k, its loads' offsets do not change and cost nothing.
+    // While the stages to be loaded are this item's, and not its last, which may
+    // have fewer k, their offsets do not change and cost nothing.
     P.offsets(cur.p_last);
     Q.offsets(cur.q_last);
     const char *p = linear_uniform(cur.p + 256 * (PK ? a.p.ld : 1)), *q = linear_uniform(cur.q + 256 * (QK ? a.q.ld : 1));
     int kt = 0;
-    for (; kt < cur.count - 3; ++kt) {
-      stage(kt, [&](int g) { issue(p, q, buf, g); });
-      p += 128 * (PK ? a.p.ld : 1);
-      q += 128 * (QK ? a.q.ld : 1);
+    for (; kt < cur.count - LEAST - 1; ++kt) {
+      const char *p_after = p + 128 * (PK ? a.p.ld : 1), *q_after = q + 128 * (QK ? a.q.ld : 1);
+      stage(kt, [&](int g) __attribute__((always_inline)) { issue(p, q, p_after, q_after, buf, g); });
+      p = p_after;
+      q = q_after;
     }
 #pragma unroll 1
     for (; kt < cur.count; ++kt) {
-      const Stage ahead = stage_at(cur, next, kt + 2);
-      stage(kt, [&](int g) { issue_any(ahead, buf, g); });
+      const Stage ahead = stage_at(cur, next, kt + 2), after = stage_at(cur, next, kt + 3);
+      stage(kt, [&](int g) __attribute__((always_inline)) { issue_any(ahead, after, buf, g); });
     }
 
     LinearOut o = a.out;
@@ -466,8 +531,17 @@ hipError_t launch_linear_tile(const LinearArgs& a, hipStream_t s) {
   const int64_t items = tb * ub * a.splits, fit = 256 * C::OCC;  // workgroups that run at a time
   if (items >= kLinearMaxItems) return hipErrorInvalidValue;
   const dim3 grid((unsigned)(items < fit ? items : fit));
-  TWELL_LAUNCH("linear_tiled", (linear_tiled<C, PK, QK, ACT, RES>), grid, 256, 0, s, a, (uint32_t)tb, (uint32_t)ub);
-  return hipGetLastError();
+  auto go = [&](auto pa, auto qa) {
+    TWELL_LAUNCH("linear_tiled", (linear_tiled<C, PK, QK, decltype(pa)::value, decltype(qa)::value, ACT, RES>), grid, 256, 0,
+                 s, a, (uint32_t)tb, (uint32_t)ub);
+    return hipGetLastError();
+  };
+  if (a.any) {
+    // in tiles of 256 x 256 there are no registers for it
+    if constexpr (C::FU * C::FT < 16) return go(std::true_type{}, std::bool_constant<!PK>{});
+    else return hipErrorInvalidValue;
+  }
+  return go(std::false_type{}, std::false_type{});
 }
 
 // y = x w^T with the epilogue that the call asks for.

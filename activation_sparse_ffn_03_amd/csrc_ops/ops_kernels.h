@@ -301,6 +301,7 @@ struct LinearArgs {
   LinearOperand p, q;
   int64_t k;
   LinearOut out;
+  bool any;     // lines of p (of both with LINEAR_ROWS) begin at any element, and hold 8 or more
   int splits;   // of the stages of k; the sums of each go to `part` when there are several
   float* part;  // [splits][rows][units]
 };
@@ -327,6 +328,7 @@ enum LinearTileSize {
 struct LinearPlan {
   LinearTileSize tile;
   int splits;  // of k; 1 straight from memory
+  bool pad;    // lines at any element are copied to lines of whole 16 bytes first
 };
 // Estimates (us). Tiles: 3.5 a launch, for each item of the busiest compute unit
 // its stages and an end, and where k is split another launch and the partial sums
@@ -371,18 +373,27 @@ inline double linear_direct_us(int64_t rows, int64_t k, int units) {
   const double groups = (units + 15) / 16 / 256.0, steps = (double)((k + 63) / 64);
   return 2.5 + 2.0 * k * units / 8.6e6 + (groups > 1 ? groups : 1) * steps * 8 * ((rows + 7) / 8) * 0.0022;
 }
-inline LinearPlan linear_plan(LinearLayout layout, int64_t rows, int64_t k, int units) {
-  if (rows == 0 || k == 0) return {LINEAR_FEW, 1};  // nothing is launched
+// Lines that begin at any element (`any`; of p, with LINEAR_ROWS of both
+// operands) go through registers on their way to LDS, or are copied first, which
+// lines of less than 8 elements need, and the tiles of 256 x 256.
+inline LinearPlan linear_plan(LinearLayout layout, int64_t rows, int64_t k, int units, bool any) {
+  if (rows == 0 || k == 0) return {LINEAR_FEW, 1, false};  // nothing is launched
   const int64_t stages = (k + kLinearStage - 1) / kLinearStage;
-  const bool direct = layout == LINEAR_ROWS && rows <= 32;
-  LinearPlan best{LINEAR_DIRECT, 1};
-  double least = direct ? linear_direct_us(rows, k, units) : 1e30;
+  LinearPlan best{LINEAR_DIRECT, 1, false};
+  double least = layout == LINEAR_ROWS && rows <= 32 ? linear_direct_us(rows, k, units) : 1e30;
+  const double copied = layout == LINEAR_ROWS ? (double)k * (rows + units) : (double)k * units;
+  const double pad_us = any ? (layout == LINEAR_ROWS ? 5 : 2.5) + 4 * copied / 5e6 : 0;
+  const bool short_lines = (layout == LINEAR_ROWS ? k : units) < 8;
   for (int t = LINEAR_FEW; t <= LINEAR_BIG; ++t)
-    for (int s = 1; s <= 16 && (s == 1 || 2 * s <= stages); ++s) {  // two stages at least
-      const double us = linear_tile_us((LinearTileSize)t, rows, k, units, s);
-      if (us < least) {
-        least = us;
-        best = {(LinearTileSize)t, s};
+    for (int pad = any ? 0 : 1; pad < 2; ++pad) {
+      if (pad == 0 && (short_lines || t == LINEAR_BIG)) continue;
+      const int fewest = pad == 0 ? 3 : 2;  // stages of a split
+      for (int s = 1; s <= 16 && (s == 1 || fewest * s <= stages); ++s) {
+        const double us = linear_tile_us((LinearTileSize)t, rows, k, units, s) * (pad ? 1 : 1.1) + (pad ? pad_us : 0);
+        if (us < least) {
+          least = us;
+          best = {(LinearTileSize)t, s, any && pad == 1};
+        }
       }
     }
   return best;
