@@ -224,18 +224,197 @@ class TwellRMSNorm(torch.nn.Module):
         return add_rms_norm(residual, self.weight, delta, self.eps, self.out_dtype)
 
 
+def _grad(t: torch.Tensor) -> torch.Tensor:
+    """A gradient as the library takes it: bf16 or fp32, packed."""
+    return _packed(t if t.dtype in (torch.bfloat16, torch.float32) else t.float())
+
+
+class LinearFunction(torch.autograd.Function):
+    """y = residual + act(x · w^T + bias) through libtwell's kernels both ways. x [rows, cols] and w [units, cols] bf16,
+    bias [units] and residual [rows, units] bf16, fp32 or None."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, act: str, out_dtype):
+        x, w = _packed(x), _packed(w)
+        bias = None if bias is None else _packed(bias)
+        residual = None if residual is None else _packed(residual)
+        train = any(ctx.needs_input_grad[:3])
+        pre = None
+        if train and act != "none":
+            pre = torch.empty((x.shape[0], w.shape[0]), dtype=torch.bfloat16, device=x.device)
+        y = tw.linear(x, w, bias=bias, act=act, residual=residual, dtype=out_dtype or torch.bfloat16, pre=pre)
+        if train:
+            ctx.save_for_backward(x, w, pre)
+        ctx.act, ctx.bias_dtype, ctx.res_dtype = act, bias is not None and bias.dtype, residual is not None and residual.dtype
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_out):
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        if any(need[:3]):
+            x, w, pre = ctx.saved_tensors
+            g = _grad(d_out)
+            e = dict(device=x.device)
+            dx = torch.empty_like(x) if need[0] else None
+            dw = torch.empty_like(w) if need[1] else None
+            db = torch.empty(w.shape[0], dtype=torch.float32, **e) if need[2] else None
+            tw.linear_bwd(g, x, w, act=ctx.act, pre=pre, out=(dx, dw, db))
+            db = None if db is None else db.to(ctx.bias_dtype)
+        return dx, dw, db, d_out.to(ctx.res_dtype) if need[3] else None, None, None
+
+
+def linear(x, w, bias=None, act: str = "none", residual=None, out_dtype=None):
+    """Functional form for any leading dimensions: residual + act(x · w^T + bias), bf16 unless out_dtype says fp32."""
+    shape = x.shape[:-1] + w.shape[:1]
+    if residual is not None:
+        if residual.shape != shape:
+            raise ValueError(f"residual must have shape {tuple(shape)}, got {tuple(residual.shape)}")
+        residual = residual.reshape(-1, shape[-1])
+    return LinearFunction.apply(x.reshape(-1, x.shape[-1]), w, bias, residual, act, out_dtype).reshape(shape)
+
+
+class TwellLinear(torch.nn.Module):
+    """A linear layer with bias, activation and residual in one kernel: weight [units, cols] as the block's, initialised
+    N(0, 1 / cols), bias fp32 zeros. forward(x, residual=None)."""
+
+    def __init__(self, cols: int, units: int, bias: bool = True, act: str = "none", out_dtype=None, device="cuda"):
+        super().__init__()
+        tw._act(act)
+        self.act, self.out_dtype = act, out_dtype
+        self.weight = torch.nn.Parameter((torch.randn(units, cols, device=device) / math.sqrt(cols)).to(torch.bfloat16))
+        self.bias = torch.nn.Parameter(torch.zeros(units, device=device)) if bias else None
+
+    def forward(self, x, residual=None):
+        return linear(x, self.weight, self.bias, self.act, residual, self.out_dtype)
+
+
+class TwellDenseFFN(torch.nn.Module):
+    """The dense counterpart of TwellGatedFFN, for layers whose activations are not sparse: down(act(up(x))), with
+    forward(x, residual=None) the residual added in the second product."""
+
+    def __init__(self, d_model: int, d_ff: int, act: str = "silu", bias: bool = True, out_dtype=None, device="cuda"):
+        super().__init__()
+        self.up = TwellLinear(d_model, d_ff, bias, act, device=device)
+        self.down = TwellLinear(d_ff, d_model, bias, out_dtype=out_dtype, device=device)
+
+    def forward(self, x, residual=None):
+        return self.down(self.up(x), residual)
+
+
+class DropoutFunction(torch.autograd.Function):
+    """Dropout of [rows, cols] whose mask is made again in the backward, from a copy of rng (16 bytes), so that the
+    caller may advance the step in between."""
+
+    @staticmethod
+    def forward(ctx, x, rng, p: float, site: int):
+        ctx.p, ctx.site = p, site
+        if ctx.needs_input_grad[0]:
+            ctx.save_for_backward(rng.clone())
+        return tw.dropout(_packed(x), rng, p, site=site)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_out):
+        rng, = ctx.saved_tensors
+        return tw.dropout(_grad(d_out), rng, ctx.p, site=ctx.site), None, None, None
+
+
+def dropout(x, rng, p: float, site: int = 0):
+    """Functional form for any leading dimensions (rows of the mask are those of x as [rows, cols]). rng: see
+    twell.make_rng."""
+    return DropoutFunction.apply(x.reshape(-1, x.shape[-1]), rng, p, site).reshape(x.shape)
+
+
+class JoinRmsNormFunction(torch.autograd.Function):
+    """r' = alpha * residual + gate * dropout(norm(y) * post_weight) and out = the RMS norm of r' times weight, through
+    libtwell's kernels both ways. residual and y are [rows, cols]; returns (r', out)."""
+
+    @staticmethod
+    def forward(ctx, residual, y, weight, post_weight, gate, alpha: float, eps: float, p: float, rng, site: int, out_dtype):
+        train = any(ctx.needs_input_grad[:5])
+        residual, y, weight = _packed(residual), _packed(y), _packed(weight)
+        post_weight = None if post_weight is None else _packed(post_weight)
+        gate = None if gate is None else _packed(gate)
+        got = tw.join_rms_norm(residual, y, weight, post_weight=post_weight, gate=gate, alpha=alpha, eps=eps, p=p, rng=rng,
+                               site=site, out_dtype=out_dtype, stats=train)
+        ctx.set_materialize_grads(False)
+        if train:
+            ctx.save_for_backward(got.residual, got.rstd, y, got.post_rstd, weight, post_weight, gate,
+                                  rng.clone() if p != 0 else None)
+        ctx.alpha, ctx.p, ctx.site, ctx.out_dtype = alpha, p, site, got.out.dtype
+        return got.residual, got.out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_residual, d_out):
+        r, rstd, y, post_rstd, weight, post_weight, gate, rng = ctx.saved_tensors
+        if d_out is None:  # only the stream was used
+            d_out = torch.zeros(r.shape, dtype=ctx.out_dtype, device=r.device)
+        d_residual = None if d_residual is None else _packed(d_residual)
+        g = tw.join_rms_norm_bwd(_grad(d_out), r, rstd, y, weight, post_weight=post_weight, post_rstd=post_rstd, gate=gate,
+                                 alpha=ctx.alpha, p=ctx.p, rng=rng, site=ctx.site, d_residual=d_residual)
+        need = ctx.needs_input_grad
+        return (g.dr if need[0] else None, g.dy if need[1] else None, g.dw.to(weight.dtype) if need[2] else None,
+                g.dpost.to(post_weight.dtype) if need[3] else None, g.dgate.to(gate.dtype) if need[4] else None,
+                None, None, None, None, None, None)
+
+
+def join_rms_norm(residual, y, weight, post_weight=None, gate=None, alpha: float = 1.0, eps: float = 1e-6, p: float = 0.0,
+                  rng=None, site: int = 0, out_dtype=None):
+    """Functional form for any leading dimensions: (alpha * residual + gate * dropout(norm(y) * post_weight), its RMS
+    norm times weight). gate is [cols], or [gate rows, cols] where each serves as many consecutive rows (a batch's
+    sequences, or as many as there are rows)."""
+    shape = residual.shape
+    if y.shape != shape:
+        raise ValueError("y must have the shape of the residual")
+    r, out = JoinRmsNormFunction.apply(residual.reshape(-1, shape[-1]), y.reshape(-1, shape[-1]), weight, post_weight, gate,
+                                       alpha, eps, p, rng, site, out_dtype)
+    return r.reshape(shape), out.reshape(shape)
+
+
+class TwellJoin(torch.nn.Module):
+    """The join of a block's output to the stream in front of the next block: forward(residual, y, rng=None) returns
+    (stream, norm). post_norm: a norm behind the block, weight ones; gate: a channel scale initialised with that value,
+    or None; alpha scales the residual; p is the dropped share in training (rng then says which)."""
+
+    def __init__(self, d_model: int, post_norm: bool = True, gate=None, alpha: float = 1.0, p: float = 0.0, site: int = 0,
+                 eps: float = 1e-6, dtype=torch.bfloat16, out_dtype=None, device="cuda"):
+        super().__init__()
+        self.alpha, self.p, self.site, self.eps, self.out_dtype = float(alpha), float(p), int(site), float(eps), out_dtype
+        e = dict(dtype=dtype, device=device)
+        self.weight = torch.nn.Parameter(torch.ones(d_model, **e))
+        self.post_weight = torch.nn.Parameter(torch.ones(d_model, **e)) if post_norm else None
+        self.gate = None if gate is None else torch.nn.Parameter(torch.full((d_model,), float(gate), **e))
+
+    def forward(self, residual, y, rng=None):
+        p = self.p if self.training else 0.0
+        return join_rms_norm(residual, y, self.weight, self.post_weight, self.gate, self.alpha, self.eps, p, rng, self.site,
+                             self.out_dtype)
+
+
 class TwellBlock(torch.nn.Module):
     """The feed-forward half of a transformer layer: TwellRMSNorm in front of
     TwellGatedFFN. forward(residual, delta=None, t=None) adds delta (what the
     layer's attention put out, or the block before) to the stream and returns
-    (stream, y) with y in fp32, to be added by the next norm."""
+    (stream, y) with y in fp32, to be added by the next norm. With `join`, a
+    TwellJoin, delta is joined by that in place of the plain addition (it may be
+    None only without) and rng goes to its dropout."""
 
     def __init__(self, d_model: int, d_ff: int, l1_lambda: float = 0.0, cfg: TwellConfig = TwellConfig(),
-                 eps: float = 1e-6, dtype=torch.bfloat16, device="cuda"):
+                 eps: float = 1e-6, dtype=torch.bfloat16, device="cuda", join=None):
         super().__init__()
-        self.norm = TwellRMSNorm(d_model, eps, dtype, out_dtype=dtype, device=device)
+        self.norm = TwellRMSNorm(d_model, eps, dtype, out_dtype=dtype, device=device) if join is None else join
         self.ffn = TwellGatedFFN(d_model, d_ff, l1_lambda, cfg, dtype, device)
 
-    def forward(self, residual, delta=None, t=None):
-        residual, x = self.norm(residual, delta)
+    def forward(self, residual, delta=None, t=None, rng=None):
+        if isinstance(self.norm, TwellJoin):
+            if delta is None:
+                raise ValueError("a block with a join needs what it joins to the stream")
+            residual, x = self.norm(residual, delta, rng)
+            if x.dtype != self.ffn.w_gate_t.dtype:
+                x = x.to(self.ffn.w_gate_t.dtype)
+        else:
+            residual, x = self.norm(residual, delta)
         return residual, self.ffn(x, t)

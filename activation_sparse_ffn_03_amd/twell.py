@@ -1123,11 +1123,15 @@ class TwellServe:
         else:
             self.ws_gate = alloc_workspace(self.sizes["ws_gate"], device) if self.sizes["ws_gate"] else None
 
-    def forward(self, residual, delta, norm_weight, w_gate, w_up_t, w_down, t, stream=None):
+    def forward(self, residual, delta, norm_weight, w_gate, w_up_t, w_down, t, stream=None, post_weight=None,
+                layer_gate=None, alpha: float = 1.0):
         """residual += delta in place (delta None: the stream stays as it is),
         then the block on its norm. Returns y [n_tokens, d_model] fp32, the
         delta of whatever comes next; the next call overwrites it, after it has
-        read it where it is that call's delta."""
+        read it where it is that call's delta. With post_weight (a norm behind
+        what put delta out), layer_gate or alpha the stream becomes
+        alpha * residual + layer_gate * norm(delta) * post_weight, by
+        join_rms_norm (its gate and alpha) in place of add_rms_norm."""
         N, D, F, dev = self.dims.n_tokens, self.dims.d_model, self.dims.d_ff, self.y.get_device()
         if residual.dtype != self.stream_dtype or tuple(residual.shape) != (N, D):
             raise ValueError(f"residual must be {self.stream_dtype} [{N}, {D}]")
@@ -1143,14 +1147,20 @@ class TwellServe:
             wq, wsc = mx4_shapes(F, D)
             _addr(w_gate[0], "w_gate codes", wq, torch.uint8, dev)
             _addr(w_gate[1], "w_gate scales", wsc, torch.uint8, dev)
+        if delta is None and (post_weight is not None or layer_gate is not None or alpha != 1.0):
+            raise ValueError("post_weight, layer_gate and alpha need a delta")
         with _current(dev):  # the block's calls go to the current device and its stream
-            self._run(residual, delta, norm_weight, w_gate, w_up_t, w_down, t, stream)
+            self._run(residual, delta, norm_weight, w_gate, w_up_t, w_down, t, stream, post_weight, layer_gate, alpha)
         return self.y
 
-    def _run(self, residual, delta, norm_weight, w_gate, w_up_t, w_down, t, stream):
+    def _run(self, residual, delta, norm_weight, w_gate, w_up_t, w_down, t, stream, post_weight, layer_gate, alpha):
         d = self.dims
-        add_rms_norm(residual, norm_weight, delta, self.eps, stream=stream,
-                     out=NormOut(None if delta is None else residual, self.x, self.x_q, self.x_scale, None))
+        if post_weight is not None or layer_gate is not None or alpha != 1.0:
+            join_rms_norm(residual, delta, norm_weight, post_weight=post_weight, gate=layer_gate, alpha=alpha, eps=self.eps,
+                          stream=stream, out=JoinOut(residual, self.x, self.x_q, self.x_scale, None, None))
+        else:
+            add_rms_norm(residual, norm_weight, delta, self.eps, stream=stream,
+                         out=NormOut(None if delta is None else residual, self.x, self.x_q, self.x_scale, None))
         if self.gate == "bf16":
             ffn_forward(d, BF16, self.x, w_gate, t, self.pack, w_up_t, w_down, self.y, ws=self.ws_fwd,
                         gate_ws=self.ws_gate, stream=stream)
@@ -1170,7 +1180,8 @@ class TwellServe:
         heavy = self.gate != "fp8" and not self.sizes["ws_gate"] and d.d_model > 2048
         return not (heavy and d.slots < d.tile_n and d.ovf_cap > 0)
 
-    def capture(self, residual, delta, norm_weight, w_gate, w_up_t, w_down, t) -> "torch.cuda.CUDAGraph":
+    def capture(self, residual, delta, norm_weight, w_gate, w_up_t, w_down, t, post_weight=None, layer_gate=None,
+                alpha: float = 1.0) -> "torch.cuda.CUDAGraph":
         """Record forward() on these tensors into a HIP graph, after one eager
         call on a copy of the stream. A replay adds what delta holds then to
         the stream and leaves the result in self.y; delta may be self.y, which
@@ -1180,10 +1191,11 @@ class TwellServe:
                              "overflow rows) is disabled; call forward() eagerly")
         with _current(self.y.get_device()):
             y = self.y.clone()
-            self.forward(residual.clone(), delta, norm_weight, w_gate, w_up_t, w_down, t)
+            join = dict(post_weight=post_weight, layer_gate=layer_gate, alpha=alpha)
+            self.forward(residual.clone(), delta, norm_weight, w_gate, w_up_t, w_down, t, **join)
             self.y.copy_(y)
             torch.cuda.synchronize()
             graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(graph):
-                self.forward(residual, delta, norm_weight, w_gate, w_up_t, w_down, t)
+                self.forward(residual, delta, norm_weight, w_gate, w_up_t, w_down, t, **join)
         return graph
