@@ -122,7 +122,7 @@ twell_status twell_linear(int64_t n, int32_t cols, int32_t units, const void* x,
   a.q = {static_cast<const uint16_t*>(x), cols};
   a.k = cols;
   a.out = {n, units, bias, residual, pre, y, bias_dtype == TWELL_BF16, res_dtype == TWELL_BF16, y_dtype == TWELL_BF16, act};
-  a.any = cols % 8 != 0 && !L.pad;
+  a.any = cols % 8 != 0 && !L.pad && L.plan.tile != twell::LINEAR_DIRECT;
   if (L.pad) {
     const int64_t ld = twell::linear_pad(cols);
     hipError_t e = twell::launch_linear_pad(x, n, cols, base + L.x, ld, s);
