@@ -46,8 +46,9 @@ struct RawAny {
 };
 
 // EACH: every row has a gate of its own, which is loaded with the row.
-template <typename TR, typename TY, int NT, int T, int C, int KIND, bool EACH>
+template <typename TR, typename TY, int NT, int T, int KIND, bool EACH>
 __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdArgs a, int parts) {
+  constexpr int C = 1;                // chunks of a thread
   constexpr int ROWS = NT / T;        // rows a workgroup takes at a time
   constexpr int G = T < 64 ? T : 64;  // lanes of a wave that share a row
   constexpr int WPR = T / G;          // waves of a row
@@ -71,9 +72,12 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdArgs a, int parts) 
       x.g[c].template load<KIND>(a.d_out, a.g_bf16, off, t + T * c, cols);
       if constexpr (EACH) x.gate[c].template load<KIND>(a.gate, a.gate_bf16, off, t + T * c, cols);
     }
-    if (has_stream) {
+    // zeros without a gradient of the stream, and below ones without a weight or
+    // gate: branches over whole rows would keep their terms in registers
 #pragma unroll
-      for (int c = 0; c < C; ++c) x.s[c].template load<KIND>(static_cast<const TR*>(a.d_residual) + off, t + T * c, cols);
+    for (int c = 0; c < C; ++c) {
+      if (has_stream) x.s[c].template load<KIND>(static_cast<const TR*>(a.d_residual) + off, t + T * c, cols);
+      else x.s[c] = {};
     }
     x.rho = a.rstd[row];
     x.rho_y = has_post ? a.post_rstd[row] : 1.f;
@@ -97,7 +101,6 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdArgs a, int parts) 
 
   // The sums of the rows taken side by side, added in their order, to `to`.
   __shared__ float acc[ROWS > 1 ? ROWS : 1][ROWS > 1 ? 8 : 1][ROWS > 1 ? T : 1];
-  static_assert(ROWS == 1 || C == 1, "rows side by side have one chunk a thread");
   auto put = [&](float (&sum)[C][8], float* to) {
     if constexpr (ROWS > 1) {
       __syncthreads();  // what was put before has been read
@@ -117,8 +120,6 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdArgs a, int parts) 
   DropBits bits = drops ? DropBits(drop_args) : DropBits();
   __shared__ float red[2][3][ROWS][WPR];
   int flip = 0;
-  constexpr bool AHEAD = C == 1;
-
   // Rows of the gate of this workgroup; with EACH rows are dealt as they are.
   const int64_t per = EACH ? a.rows : a.rows / a.gates;
   const int64_t gates = EACH ? 1 : a.gates;
@@ -131,7 +132,7 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdArgs a, int parts) 
     const int64_t r0 = gr * per + slice * per / slices, r1 = gr * per + (slice + 1) * per / slices;
     int64_t row = r0 + side;
     Row now, next;
-    if (AHEAD && row < r1) fetch(row, now);
+    if (row < r1) fetch(row, now);
     if constexpr (!EACH) {
       if (has_gate) {
         load_weight<T, C, KIND>(static_cast<const char*>(a.gate) + gr * cols * (a.gate_bf16 ? 2 : 4), a.gate_bf16, t,
@@ -145,11 +146,7 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdArgs a, int parts) 
     }
     for (int64_t first = r0; first < r1; first += ROWS, row += ROWS) {  // the same number of times in every wave
       const bool here = row < r1;
-      if constexpr (AHEAD) {
-        if (row + ROWS < r1) fetch(row + ROWS, next);
-      } else if (here) {
-        fetch(row, now);
-      }
+      if (row + ROWS < r1) fetch(row + ROWS, next);
       uint32_t keep[C];
 #pragma unroll
       for (int c = 0; c < C; ++c) keep[c] = drops ? bits.template chunk<KIND>((uint32_t)row, t + T * c, cols) : 0xFFu;
@@ -165,20 +162,17 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdArgs a, int parts) 
           const float xh = now.r[c].get(k) * now.rho, g = now.g[c].get(k, a.g_bf16), u = g * w[c][k];
           if (here) dw[c][k] = fmaf(g, xh, dw[c][k]);
           const bool counts = chunk_counts<KIND>(t + T * c, k, cols);
-          if (counts) s1 = fmaf(u, xh, s1);
-          if (has_post && counts) {
-            float base = now.rho * u;
-            if (has_stream) base += now.s[c].get(k);
-            const float kyh = keep[c] >> k & 1 ? gate_at(c, k) * a.drop_scale * post[c][k] * (now.y[c].get(k) * now.rho_y) : 0.f;
+          const float base = fmaf(now.rho, u, now.s[c].get(k));
+          const float kyh = keep[c] >> k & 1 ? gate_at(c, k) * a.drop_scale * post[c][k] * (now.y[c].get(k) * now.rho_y) : 0.f;
+          if (counts) {
+            s1 = fmaf(u, xh, s1);
             s2 = fmaf(base, kyh, s2);
             s3 = fmaf(xh, kyh, s3);
           }
         }
       s1 = group_sum<G>(s1);
-      if (has_post) {
-        s2 = group_sum<G>(s2);
-        s3 = group_sum<G>(s3);
-      }
+      s2 = group_sum<G>(s2);
+      s3 = group_sum<G>(s3);
       if constexpr (WPR > 1) {
         // two buffers: a wave may write the next row's sums while another still
         // reads this row's
@@ -204,8 +198,7 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdArgs a, int parts) 
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float xh = now.r[c].get(k) * now.rho;
-          float d = now.rho * (now.g[c].get(k, a.g_bf16) * w[c][k] - xh * c1);
-          if (has_stream) d += now.s[c].get(k);
+          const float d = fmaf(now.rho, now.g[c].get(k, a.g_bf16) * w[c][k] - xh * c1, now.s[c].get(k));
           dr[k] = a.alpha * d;
           const float yh = now.y[c].get(k) * now.rho_y;  // y itself without the norm: rho_y is 1 then
           const bool kept = keep[c] >> k & 1;
@@ -216,12 +209,8 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdArgs a, int parts) 
           } else {
             if (here) dgate[c][k] = fmaf(dm, u, dgate[c][k]);
           }
-          if (has_post) {
-            if (here) dpost[c][k] = fmaf(dv, yh, dpost[c][k]);
-            dy[k] = now.rho_y * (dv * post[c][k] - yh * c2);
-          } else {
-            dy[k] = dv;
-          }
+          if (here) dpost[c][k] = fmaf(dv, yh, dpost[c][k]);
+          dy[k] = now.rho_y * (dv * post[c][k] - (has_post ? yh * c2 : 0.f));  // dv without the norm, whatever y holds
         }
         if (here) {
           store8<KIND>(static_cast<TR*>(a.dr) + row * cols, t + T * c, cols, dr);
@@ -229,11 +218,141 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdArgs a, int parts) 
           if constexpr (EACH) store8<KIND>(a.dgate + row * cols, t + T * c, cols, dgate[c]);
         }
       }
-      if constexpr (AHEAD) now = next;
+      now = next;
     }
     if (!EACH && has_gate) {
       const bool part = parts > 1;
       put(dgate, part ? a.part + ((int64_t)gridDim.x * (has_post ? 2 : 1) + b) * cols : a.dgate + gr * cols);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dgate[c][k] = 0.f;
+    }
+  }
+  const bool alone = gridDim.x == 1;
+  put(dw, alone ? a.dw : a.part + (int64_t)b * cols);
+  if (has_post) put(dpost, alone ? a.dpost : a.part + ((int64_t)gridDim.x + b) * cols);
+}
+
+// Rows of more than 4096 elements: 512 threads a row, C chunks each, one chunk at a
+// time. Only the sums stay in registers; a chunk's operands and weights are read
+// for the row's sums, and again, from L2 then, for what follows them (kept in
+// registers they went to scratch memory: 2000 x 8192 122 us, 1000 x 16384 352).
+template <typename TR, typename TY, int C, int KIND>
+__global__ __launch_bounds__(512) void join_bwd_wide_kernel(JoinBwdArgs a, int parts, int each) {
+  constexpr int T = 512, WAVES = T / 64;
+  const int wave = threadIdx.x >> 6, t = threadIdx.x, cols = a.cols, b = blockIdx.x;
+  const bool has_stream = a.d_residual != nullptr, has_post = a.post_w != nullptr, has_gate = a.gate != nullptr;
+  const bool drops = a.drop != 0;
+  float dw[C][8], dpost[C][8], dgate[C][8];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dw[c][k] = dpost[c][k] = dgate[c][k] = 0.f;
+  auto put = [&](float (&sum)[C][8], float* to) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) store8<KIND>(to, t + T * c, cols, sum[c]);
+  };
+  const DropArgs drop_args{a.rng, a.site, a.drop, a.drop_scale};
+  const DropBits bits = drops ? DropBits(drop_args) : DropBits();
+  __shared__ float red[2][3][WAVES];
+  int flip = 0;
+  // rows of the gate of this workgroup, as in join_bwd_kernel
+  const int64_t per = each ? a.rows : a.rows / a.gates, gates = each ? 1 : a.gates;
+  const bool shared = each || parts > 1;
+  const int n = each ? (int)gridDim.x : parts;
+  const int64_t first_gate = shared ? b / n : b * gates / gridDim.x;
+  const int64_t end_gate = shared ? first_gate + 1 : (b + 1) * gates / gridDim.x;
+  const int64_t slice = shared ? b % n : 0, slices = shared ? n : 1;
+  for (int64_t gr = first_gate; gr < end_gate; ++gr) {
+    const int64_t r0 = gr * per + slice * per / slices, r1 = gr * per + (slice + 1) * per / slices;
+    for (int64_t row = r0; row < r1; ++row) {
+      const int64_t off = row * cols, gate_off = (each ? row : gr) * cols;
+      const float rho = a.rstd[row], rho_y = has_post ? a.post_rstd[row] : 1.f;
+      struct Operands {
+        Raw8<TR> r, s;
+        Raw8<TY> y;
+        RawAny g, w, post, gate;
+        uint32_t keep;
+      };
+      auto fetch = [&](int c, Operands& x) {
+        const int i = t + T * c;
+        x.r.template load<KIND>(static_cast<const TR*>(a.residual) + off, i, cols);
+        x.y.template load<KIND>(static_cast<const TY*>(a.y) + off, i, cols);
+        x.g.template load<KIND>(a.d_out, a.g_bf16, off, i, cols);
+        if (has_stream) x.s.template load<KIND>(static_cast<const TR*>(a.d_residual) + off, i, cols);
+        else x.s = {};
+        x.w.template load<KIND>(a.w, a.w_bf16, 0, i, cols);
+        if (has_post) x.post.template load<KIND>(a.post_w, a.post_bf16, 0, i, cols);
+        if (has_gate) x.gate.template load<KIND>(a.gate, a.gate_bf16, gate_off, i, cols);
+        x.keep = drops ? bits.template chunk<KIND>((uint32_t)row, i, cols) : 0xFFu;
+      };
+      float s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        Operands x;
+        fetch(c, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float xh = x.r.get(k) * rho, g = x.g.get(k, a.g_bf16), u = g * x.w.get(k, a.w_bf16);
+          const float post = has_post ? x.post.get(k, a.post_bf16) : 1.f, gate = has_gate ? x.gate.get(k, a.gate_bf16) : 1.f;
+          dw[c][k] = fmaf(g, xh, dw[c][k]);
+          const float base = fmaf(rho, u, x.s.get(k));
+          const float kyh = x.keep >> k & 1 ? gate * a.drop_scale * post * (x.y.get(k) * rho_y) : 0.f;
+          if (chunk_counts<KIND>(t + T * c, k, cols)) {
+            s1 = fmaf(u, xh, s1);
+            s2 = fmaf(base, kyh, s2);
+            s3 = fmaf(xh, kyh, s3);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);  // one chunk at a time
+      }
+      s1 = group_sum<64>(s1);
+      s2 = group_sum<64>(s2);
+      s3 = group_sum<64>(s3);
+      if ((t & 63) == 0) {
+        red[flip][0][wave] = s1;
+        red[flip][1][wave] = s2;
+        red[flip][2][wave] = s3;
+      }
+      lds_barrier();
+      s1 = s2 = s3 = 0.f;
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) {
+        s1 += red[flip][0][i];
+        s2 += red[flip][1][i];
+        s3 += red[flip][2][i];
+      }
+      flip ^= 1;
+      const float c1 = s1 / (float)cols, c2 = (s2 - rho * c1 * s3) / (float)cols;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        asm volatile("" ::: "memory");  // read again
+        Operands x;
+        fetch(c, x);
+        float dr[8], dy[8], dg[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float post = has_post ? x.post.get(k, a.post_bf16) : 1.f, gate = has_gate ? x.gate.get(k, a.gate_bf16) : 1.f;
+          const float xh = x.r.get(k) * rho;
+          const float d = fmaf(rho, x.g.get(k, a.g_bf16) * x.w.get(k, a.w_bf16) - xh * c1, x.s.get(k));
+          dr[k] = a.alpha * d;
+          const float yh = x.y.get(k) * rho_y;
+          const bool kept = x.keep >> k & 1;
+          const float dm = kept ? d * a.drop_scale : 0.f, dv = dm * gate, u = kept ? yh * post : 0.f;
+          dg[k] = dm * u;
+          dgate[c][k] += dg[k];
+          dpost[c][k] = fmaf(dv, yh, dpost[c][k]);
+          dy[k] = rho_y * (dv * post - (has_post ? yh * c2 : 0.f));
+        }
+        store8<KIND>(static_cast<TR*>(a.dr) + off, t + T * c, cols, dr);
+        store8<KIND>(static_cast<TY*>(a.dy) + off, t + T * c, cols, dy);
+        if (each) store8<KIND>(a.dgate + off, t + T * c, cols, dg);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (!each && has_gate) {
+      put(dgate, parts > 1 ? a.part + ((int64_t)gridDim.x * (has_post ? 2 : 1) + b) * cols : a.dgate + gr * cols);
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -274,11 +393,14 @@ hipError_t launch_cfg(const JoinBwdArgs& a, hipStream_t s) {
   const bool each = a.gate != nullptr && a.gates == a.rows && a.rows > 1;
   row_kind(a.cols, [&](auto kind) {
     constexpr int KIND = decltype(kind)::value;
-    if constexpr (KIND != ROWS_SHORT || T == 16) {
+    if constexpr (C > 1) {
+      if constexpr (KIND != ROWS_SHORT)
+        TWELL_LAUNCH("join_rms_norm_bwd", (join_bwd_wide_kernel<TR, TY, C, KIND>), dim3(p.groups), NT, 0, s, a, p.parts, each);
+    } else if constexpr (KIND != ROWS_SHORT || T == 16) {
       if (each)
-        TWELL_LAUNCH("join_rms_norm_bwd", (join_bwd_kernel<TR, TY, NT, T, C, KIND, true>), dim3(p.groups), NT, 0, s, a, p.parts);
+        TWELL_LAUNCH("join_rms_norm_bwd", (join_bwd_kernel<TR, TY, NT, T, KIND, true>), dim3(p.groups), NT, 0, s, a, p.parts);
       else
-        TWELL_LAUNCH("join_rms_norm_bwd", (join_bwd_kernel<TR, TY, NT, T, C, KIND, false>), dim3(p.groups), NT, 0, s, a, p.parts);
+        TWELL_LAUNCH("join_rms_norm_bwd", (join_bwd_kernel<TR, TY, NT, T, KIND, false>), dim3(p.groups), NT, 0, s, a, p.parts);
     }
   });
   hipError_t e = hipGetLastError();

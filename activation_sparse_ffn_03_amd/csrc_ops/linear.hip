@@ -50,43 +50,68 @@ __global__ __launch_bounds__(256) void linear_pad_kernel(const uint16_t* __restr
   store_some<8>(out, 1, row * ld + col, 8, v);
 }
 
-// dz = d_out * act'(pre), and the sums of its columns over a run of rows: 64
-// threads side by side take 8 units each, four rows at a time.
-template <int ACT>
-__global__ __launch_bounds__(256) void linear_dz_kernel(LinearDzArgs a) {
-  const int t = threadIdx.x & 63, side = threadIdx.x >> 6;
-  const int unit = 8 * (blockIdx.x * 64 + t), have = a.units - unit;
+// dz = d_out * act'(pre), and the sums of its columns over a run of rows: 16
+// threads side by side take 8 units each, 64 rows at a time, so that up to 1024
+// rows need no second launch for the sums (509 x 1021 6.2 + 3.9 -> DZ_SMALL us;
+// 8192 x 5632 72 -> DZ_LARGE).
+template <int ACT, typename TG>
+__global__ __launch_bounds__(1024) void linear_dz_kernel(LinearDzArgs a) {
+  constexpr int T = kLinearDzUnits / 8, SIDES = 1024 / T, BATCH = 4;
+  constexpr int G_BF16 = std::is_same_v<TG, uint16_t>;
+  const int t = threadIdx.x % T, side = threadIdx.x / T;
+  const int unit = 8 * (blockIdx.x * T + t), have = a.units - unit;
   const int64_t r0 = (int64_t)blockIdx.y * a.rows / gridDim.y, r1 = ((int64_t)blockIdx.y + 1) * a.rows / gridDim.y;
   float sum[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) sum[k] = 0.f;
-  if (have > 0) {
-#pragma unroll 2
-    for (int64_t row = r0 + side; row < r1; row += 4) {
-      const int64_t at = row * a.units + unit;
-      float g[8];
-      load_some<8>(a.d_out, a.g_bf16, at, have, g);
-      if constexpr (ACT != TWELL_ACT_NONE) {
-        float z[8];
-        load_some<8>(a.pre, 1, at, have, z);
+  auto finish = [&](int64_t row, float (&g)[8], const float (&z)[8]) {
+    if constexpr (ACT != TWELL_ACT_NONE) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] *= activate_slope<ACT>(z[k]);
+      for (int k = 0; k < 8; ++k) g[k] *= activate_slope<ACT>(z[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] += g[k];
+    if (a.dz != nullptr) store_some<8>(a.dz, 1, row * a.ld + unit, 8, g);  // zeros behind the last unit
+  };
+  if (have >= 8) {
+    int64_t row = r0 + side;
+    for (; row + (BATCH - 1) * SIDES < r1; row += BATCH * SIDES) {
+      float g[BATCH][8], z[BATCH][8];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int64_t at = (row + i * SIDES) * a.units + unit;
+        load_some<8>(a.d_out, G_BF16, at, 8, g[i]);
+        if constexpr (ACT != TWELL_ACT_NONE) load_some<8>(a.pre, 1, at, 8, z[i]);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum[k] += g[k];
-      if (a.dz != nullptr) store_some<8>(a.dz, 1, row * a.ld + unit, 8, g);  // zeros behind the last unit
+      for (int i = 0; i < BATCH; ++i) finish(row + i * SIDES, g[i], z[i]);
+    }
+    for (; row < r1; row += SIDES) {
+      float g[8], z[8];
+      load_some<8>(a.d_out, G_BF16, row * a.units + unit, 8, g);
+      if constexpr (ACT != TWELL_ACT_NONE) load_some<8>(a.pre, 1, row * a.units + unit, 8, z);
+      finish(row, g, z);
+    }
+  } else if (have > 0) {
+    for (int64_t row = r0 + side; row < r1; row += SIDES) {
+      float g[8], z[8];
+      load_some<8>(a.d_out, G_BF16, row * a.units + unit, have, g);
+      if constexpr (ACT != TWELL_ACT_NONE) load_some<8>(a.pre, 1, row * a.units + unit, have, z);
+      finish(row, g, z);
     }
   }
   if (a.db == nullptr) return;
-  __shared__ float acc[4][8][64];
+  // the rows side by side: 8 T threads add a unit each, in the sides' order
+  __shared__ float acc[SIDES][8][T];
 #pragma unroll
   for (int k = 0; k < 8; ++k) acc[side][k][t] = sum[k];
   __syncthreads();
-  if (side > 0 || have <= 0) return;
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    for (int i = 1; i < 4; ++i) sum[k] += acc[i][k][t];
-  store_some<8>(gridDim.y == 1 ? a.db : a.part + (int64_t)blockIdx.y * a.units, 0, unit, have, sum);
+  if (threadIdx.x >= 8 * T) return;
+  const int k = threadIdx.x / T, u = 8 * (blockIdx.x * T + t) + k;
+  if (u >= a.units) return;
+  float s = 0.f;
+  for (int i = 0; i < SIDES; ++i) s += acc[i][k][t];
+  (gridDim.y == 1 ? a.db : a.part + (int64_t)blockIdx.y * a.units)[u] = s;
 }
 
 // db[u] = sum over the partial rows, in their order.
@@ -103,7 +128,11 @@ __global__ __launch_bounds__(256) void linear_db_sum(const float* __restrict__ p
 template <int ACT>
 hipError_t launch_dz(const LinearDzArgs& a, hipStream_t s) {
   const int parts = linear_db_parts(a.rows);
-  TWELL_LAUNCH("linear_dz", linear_dz_kernel<ACT>, dim3((a.units + 511) / 512, parts), 256, 0, s, a);
+  const dim3 grid((a.units + kLinearDzUnits - 1) / kLinearDzUnits, parts);
+  if (a.g_bf16)
+    TWELL_LAUNCH("linear_dz", (linear_dz_kernel<ACT, uint16_t>), grid, 1024, 0, s, a);
+  else
+    TWELL_LAUNCH("linear_dz", (linear_dz_kernel<ACT, float>), grid, 1024, 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.db == nullptr || parts == 1) return e;
   TWELL_LAUNCH("linear_db_sum", linear_db_sum, dim3((a.units + 255) / 256), 256, 0, s, a.part, parts, a.units, a.db);

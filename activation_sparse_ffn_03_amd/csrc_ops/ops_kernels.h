@@ -427,7 +427,8 @@ struct LinearDzArgs {
   float* db;          // [units] or null
   float* part;        // [linear_db_parts][units] when there are several
 };
-inline int linear_db_parts(int64_t rows) { return (int)(rows < 16 ? 1 : rows < 1024 ? (rows + 15) / 16 : 64); }
+constexpr int kLinearDzUnits = 128;  // of a workgroup
+inline int linear_db_parts(int64_t rows) { return (int)(rows <= 1024 ? 1 : rows <= 65536 ? (rows + 1023) / 1024 : 64); }
 hipError_t launch_linear_dz(const LinearDzArgs& a, hipStream_t s);
 
 }  // namespace twell
