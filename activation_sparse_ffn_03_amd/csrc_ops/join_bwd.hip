@@ -235,24 +235,32 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdArgs a, int parts) 
 }
 
 // Rows of more than 4096 elements: 512 threads a row, C chunks each, one chunk at a
-// time. Only the sums stay in registers; a chunk's operands and weights are read
-// for the row's sums, and again, from L2 then, for what follows them (kept in
-// registers they went to scratch memory: 2000 x 8192 122 us, 1000 x 16384 352).
+// time. Only the sums are kept; a chunk's operands and weights are read for the
+// row's sums, and again, from L2 then, for what follows them (kept in registers
+// they went to scratch memory: 2000 x 8192 122 us, 1000 x 16384 352). A chunk's
+// loads wait for the chunk before by a dependence of their addresses, without
+// which the compiler still hoists them all into scratch memory; with four chunks
+// two of the sums lie in LDS. 2000 x 8192 114 -> 80 us, 1000 x 16384 278 -> 89.
 template <typename TR, typename TY, int C, int KIND>
 __global__ __launch_bounds__(512) void join_bwd_wide_kernel(JoinBwdArgs a, int parts, int each) {
   constexpr int T = 512, WAVES = T / 64;
   const int wave = threadIdx.x >> 6, t = threadIdx.x, cols = a.cols, b = blockIdx.x;
   const bool has_stream = a.d_residual != nullptr, has_post = a.post_w != nullptr, has_gate = a.gate != nullptr;
   const bool drops = a.drop != 0;
-  float dw[C][8], dpost[C][8], dgate[C][8];
+  float dgate[C][8];
+  // two of the three sums: registers, or LDS where they would not fit; a thread
+  // touches only its own
+  constexpr bool LDS = C > 2;
+  __shared__ float lds_sum[LDS ? 2 : 1][LDS ? C * 8 : 1][LDS ? T : 1];
+  float reg_sum[2][LDS ? 1 : C][8];
+  auto sum_at = [&](int which, int c, int k) -> float& {
+    if constexpr (LDS) return lds_sum[which][c * 8 + k][t];
+    else return reg_sum[which][c][k];
+  };
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dw[c][k] = dpost[c][k] = dgate[c][k] = 0.f;
-  auto put = [&](float (&sum)[C][8], float* to) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) store8<KIND>(to, t + T * c, cols, sum[c]);
-  };
+    for (int k = 0; k < 8; ++k) sum_at(0, c, k) = sum_at(1, c, k) = dgate[c][k] = 0.f;
   const DropArgs drop_args{a.rng, a.site, a.drop, a.drop_scale};
   const DropBits bits = drops ? DropBits(drop_args) : DropBits();
   __shared__ float red[2][3][WAVES];
@@ -275,8 +283,11 @@ __global__ __launch_bounds__(512) void join_bwd_wide_kernel(JoinBwdArgs a, int p
         RawAny g, w, post, gate;
         uint32_t keep;
       };
-      auto fetch = [&](int c, Operands& x) {
-        const int i = t + T * c;
+      // `after`: a result of the chunk before, without which this one's loads do
+      // not begin
+      auto fetch = [&](int c, Operands& x, float after) {
+        int i = t + T * c;
+        asm volatile("" : "+v"(i) : "v"(after));
         x.r.template load<KIND>(static_cast<const TR*>(a.residual) + off, i, cols);
         x.y.template load<KIND>(static_cast<const TY*>(a.y) + off, i, cols);
         x.g.template load<KIND>(a.d_out, a.g_bf16, off, i, cols);
@@ -291,12 +302,12 @@ __global__ __launch_bounds__(512) void join_bwd_wide_kernel(JoinBwdArgs a, int p
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         Operands x;
-        fetch(c, x);
+        fetch(c, x, s3);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float xh = x.r.get(k) * rho, g = x.g.get(k, a.g_bf16), u = g * x.w.get(k, a.w_bf16);
           const float post = has_post ? x.post.get(k, a.post_bf16) : 1.f, gate = has_gate ? x.gate.get(k, a.gate_bf16) : 1.f;
-          dw[c][k] = fmaf(g, xh, dw[c][k]);
+          sum_at(0, c, k) = fmaf(g, xh, sum_at(0, c, k));
           const float base = fmaf(rho, u, x.s.get(k));
           const float kyh = x.keep >> k & 1 ? gate * a.drop_scale * post * (x.y.get(k) * rho_y) : 0.f;
           if (chunk_counts<KIND>(t + T * c, k, cols)) {
@@ -327,9 +338,8 @@ __global__ __launch_bounds__(512) void join_bwd_wide_kernel(JoinBwdArgs a, int p
       const float c1 = s1 / (float)cols, c2 = (s2 - rho * c1 * s3) / (float)cols;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        asm volatile("" ::: "memory");  // read again
         Operands x;
-        fetch(c, x);
+        fetch(c, x, c == 0 ? c2 : dgate[c - 1][7]);
         float dr[8], dy[8], dg[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -342,7 +352,7 @@ __global__ __launch_bounds__(512) void join_bwd_wide_kernel(JoinBwdArgs a, int p
           const float dm = kept ? d * a.drop_scale : 0.f, dv = dm * gate, u = kept ? yh * post : 0.f;
           dg[k] = dm * u;
           dgate[c][k] += dg[k];
-          dpost[c][k] = fmaf(dv, yh, dpost[c][k]);
+          sum_at(1, c, k) = fmaf(dv, yh, sum_at(1, c, k));
           dy[k] = rho_y * (dv * post - (has_post ? yh * c2 : 0.f));
         }
         store8<KIND>(static_cast<TR*>(a.dr) + off, t + T * c, cols, dr);
@@ -352,16 +362,28 @@ __global__ __launch_bounds__(512) void join_bwd_wide_kernel(JoinBwdArgs a, int p
       }
     }
     if (!each && has_gate) {
-      put(dgate, parts > 1 ? a.part + ((int64_t)gridDim.x * (has_post ? 2 : 1) + b) * cols : a.dgate + gr * cols);
+      float* to = parts > 1 ? a.part + ((int64_t)gridDim.x * (has_post ? 2 : 1) + b) * cols : a.dgate + gr * cols;
 #pragma unroll
-      for (int c = 0; c < C; ++c)
+      for (int c = 0; c < C; ++c) {
+        store8<KIND>(to, t + T * c, cols, dgate[c]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) dgate[c][k] = 0.f;
+      }
     }
   }
   const bool alone = gridDim.x == 1;
-  put(dw, alone ? a.dw : a.part + (int64_t)b * cols);
-  if (has_post) put(dpost, alone ? a.dpost : a.part + ((int64_t)gridDim.x + b) * cols);
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    if (which == 1 && !has_post) break;
+    float* to = which == 0 ? (alone ? a.dw : a.part + (int64_t)b * cols) : alone ? a.dpost : a.part + ((int64_t)gridDim.x + b) * cols;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = sum_at(which, c, k);
+      store8<KIND>(to, t + T * c, cols, v);
+    }
+  }
 }
 
 // Sums of partial rows: a workgroup takes 64 columns of one of them, each of its
