@@ -32,7 +32,8 @@ SOURCES = ["twell_host.cpp", "twell_api.hip", "trace.hip", "side_stream.hip", "s
 # operators around the block
 OPS_SOURCES = ["ops_api.hip", "norm.hip", "norm_bwd.hip", "mx4_quant.hip", "mx4_product.hip", "join_api.hip",
                "join.hip", "join_bwd.hip", "dropout.hip", "linear_api.hip", "linear.hip", "linear_rows_big.hip",
-               "linear_rows_wide.hip", "linear_rows_mid.hip", "linear_rows_few.hip", "linear_mixed.hip", "linear_cols.hip", "linear_direct.hip"]
+               "linear_rows_wide.hip", "linear_rows_mid.hip", "linear_rows_few.hip", "linear_mixed.hip", "linear_cols.hip",
+               "linear_pair.hip", "linear_direct.hip"]
 
 
 def _hipcc() -> str:

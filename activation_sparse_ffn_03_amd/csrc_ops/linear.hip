@@ -50,13 +50,14 @@ __global__ __launch_bounds__(256) void linear_pad_kernel(const uint16_t* __restr
   store_some<8>(out, 1, row * ld + col, 8, v);
 }
 
-// dz = d_out * act'(pre), and the sums of its columns over a run of rows: 16
-// threads side by side take 8 units each, 64 rows at a time, so that up to 1024
-// rows need no second launch for the sums (509 x 1021 6.2 + 3.9 -> DZ_SMALL us;
-// 8192 x 5632 72 -> DZ_LARGE).
-template <int ACT, typename TG>
+// dz = d_out * act'(pre), and the sums of its columns over a run of rows. T
+// threads side by side take 8 units each, 1024 / T rows at a time: 16, whole
+// lines of 256 bytes, or 4 up to 1024 rows, which then need no second launch for
+// the sums and still spread over the chip (509 x 1021 7.4 us, with 16 threads and
+// a second launch 10.1; 8192 x 5632 62, with 256 threads a workgroup 72).
+template <int ACT, typename TG, int T>
 __global__ __launch_bounds__(1024) void linear_dz_kernel(LinearDzArgs a) {
-  constexpr int T = kLinearDzUnits / 8, SIDES = 1024 / T, BATCH = 4;
+  constexpr int SIDES = 1024 / T, BATCH = T == 16 ? 4 : 2;
   constexpr int G_BF16 = std::is_same_v<TG, uint16_t>;
   const int t = threadIdx.x % T, side = threadIdx.x / T;
   const int unit = 8 * (blockIdx.x * T + t), have = a.units - unit;
@@ -101,16 +102,22 @@ __global__ __launch_bounds__(1024) void linear_dz_kernel(LinearDzArgs a) {
     }
   }
   if (a.db == nullptr) return;
-  // the rows side by side: 8 T threads add a unit each, in the sides' order
-  __shared__ float acc[SIDES][8][T];
+  // the rows side by side: those of a wave, then 8 T threads add the waves' sums
+  // of a unit each, in their order
+  constexpr int WAVES = 1024 / 64;
+  __shared__ float acc[WAVES][8][T];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) acc[side][k][t] = sum[k];
+  for (int k = 0; k < 8; ++k) {
+#pragma unroll
+    for (int o = T; o < 64; o *= 2) sum[k] += __shfl_xor(sum[k], o, 64);
+    if ((threadIdx.x & 63) < T) acc[threadIdx.x >> 6][k][t] = sum[k];
+  }
   __syncthreads();
   if (threadIdx.x >= 8 * T) return;
   const int k = threadIdx.x / T, u = 8 * (blockIdx.x * T + t) + k;
   if (u >= a.units) return;
   float s = 0.f;
-  for (int i = 0; i < SIDES; ++i) s += acc[i][k][t];
+  for (int i = 0; i < WAVES; ++i) s += acc[i][k][t];
   (gridDim.y == 1 ? a.db : a.part + (int64_t)blockIdx.y * a.units)[u] = s;
 }
 
@@ -128,11 +135,16 @@ __global__ __launch_bounds__(256) void linear_db_sum(const float* __restrict__ p
 template <int ACT>
 hipError_t launch_dz(const LinearDzArgs& a, hipStream_t s) {
   const int parts = linear_db_parts(a.rows);
-  const dim3 grid((a.units + kLinearDzUnits - 1) / kLinearDzUnits, parts);
-  if (a.g_bf16)
-    TWELL_LAUNCH("linear_dz", (linear_dz_kernel<ACT, uint16_t>), grid, 1024, 0, s, a);
-  else
-    TWELL_LAUNCH("linear_dz", (linear_dz_kernel<ACT, float>), grid, 1024, 0, s, a);
+  auto go = [&](auto kernel, int t) {
+    TWELL_LAUNCH("linear_dz", kernel, dim3((a.units + 8 * t - 1) / (8 * t), parts), 1024, 0, s, a);
+  };
+  if (parts == 1) {
+    if (a.g_bf16) go(linear_dz_kernel<ACT, uint16_t, 4>, 4);
+    else go(linear_dz_kernel<ACT, float, 4>, 4);
+  } else {
+    if (a.g_bf16) go(linear_dz_kernel<ACT, uint16_t, 16>, 16);
+    else go(linear_dz_kernel<ACT, float, 16>, 16);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.db == nullptr || parts == 1) return e;
   TWELL_LAUNCH("linear_db_sum", linear_db_sum, dim3((a.units + 255) / 256), 256, 0, s, a.part, parts, a.units, a.db);

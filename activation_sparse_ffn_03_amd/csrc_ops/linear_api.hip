@@ -57,7 +57,7 @@ ForwardLayout forward_layout(int64_t n, int32_t cols, int32_t units) {
 // other in the same place.
 struct BackwardLayout {
   LinearPlan dx, dw;
-  bool dz, pad_x, pad_w;
+  bool dz, pad_x, pad_w, pair;
   size_t dz_at, x, w, db, part, total;
 };
 BackwardLayout backward_layout(int64_t n, int32_t cols, int32_t units, bool d_out_bf16, int32_t act, uint32_t wanted) {
@@ -65,6 +65,8 @@ BackwardLayout backward_layout(int64_t n, int32_t cols, int32_t units, bool d_ou
   const bool dx = wanted & TWELL_LINEAR_DX, dw = wanted & TWELL_LINEAR_DW;
   L.dx = twell::linear_plan(twell::LINEAR_MIXED, n, units, cols, cols % 8 != 0);
   L.dw = twell::linear_plan(twell::LINEAR_COLS, units, n, cols, cols % 8 != 0);
+  L.pair = dx && dw && twell::linear_paired(n, units, cols, cols % 8 != 0, L.dx, L.dw);
+  if (L.pair) L.dx = L.dw = {twell::LINEAR_FEW, 1, false, 0};
   L.dz = (dx || dw) && (act != TWELL_ACT_NONE || !d_out_bf16 || units % 8 != 0);
   L.pad_x = dw && L.dw.pad;
   L.pad_w = dx && L.dx.pad;
@@ -195,32 +197,33 @@ twell_status twell_linear_bwd(int64_t n, int32_t cols, int32_t units, twell_dtyp
     if (e != hipSuccess) return hip_status(e, "twell_linear_bwd");
   }
   const int64_t ld = twell::linear_pad(cols);
-  twell::LinearArgs a{};
-  a.part = reinterpret_cast<float*>(base + L.part);
-  if (dx != nullptr && n > 0) {
-    a.p = {static_cast<const uint16_t*>(w), cols};
+  twell::LinearArgs gx{}, gw{};
+  gx.q = gw.q = dz;
+  gx.part = gw.part = reinterpret_cast<float*>(base + L.part);
+  gx.out = {n, cols, nullptr, nullptr, nullptr, dx, 0, 0, dx_dtype == TWELL_BF16, TWELL_ACT_NONE};
+  gw.out = {units, cols, nullptr, nullptr, nullptr, dw, 0, 0, dw_dtype == TWELL_BF16, TWELL_ACT_NONE};
+  if (n == 0) return dw == nullptr ? ok() : hip_status(twell::launch_linear_zero(gw.out, s), "twell_linear_bwd");
+  if (dx != nullptr) {
+    gx.p = {static_cast<const uint16_t*>(w), cols};
     if (L.pad_w) {
       if ((e = twell::launch_linear_pad(w, units, cols, base + L.w, ld, s)) != hipSuccess) return hip_status(e, "twell_linear_bwd");
-      a.p = {reinterpret_cast<const uint16_t*>(base + L.w), ld};
+      gx.p = {reinterpret_cast<const uint16_t*>(base + L.w), ld};
     }
-    a.any = cols % 8 != 0 && !L.pad_w;
-    a.q = dz;
-    a.k = units;
-    a.out = {n, cols, nullptr, nullptr, nullptr, dx, 0, 0, dx_dtype == TWELL_BF16, TWELL_ACT_NONE};
-    if ((e = twell::launch_linear(twell::LINEAR_MIXED, L.dx, a, s)) != hipSuccess) return hip_status(e, "twell_linear_bwd");
+    gx.any = cols % 8 != 0 && !L.pad_w;
+    gx.k = units;
+    gx.splits = 1;
+    if (!L.pair && (e = twell::launch_linear(twell::LINEAR_MIXED, L.dx, gx, s)) != hipSuccess) return hip_status(e, "twell_linear_bwd");
   }
   if (dw != nullptr) {
-    a.out = {units, cols, nullptr, nullptr, nullptr, dw, 0, 0, dw_dtype == TWELL_BF16, TWELL_ACT_NONE};
-    if (n == 0) return hip_status(twell::launch_linear_zero(a.out, s), "twell_linear_bwd");
-    a.p = {static_cast<const uint16_t*>(x), cols};
+    gw.p = {static_cast<const uint16_t*>(x), cols};
     if (L.pad_x) {
       if ((e = twell::launch_linear_pad(x, n, cols, base + L.x, ld, s)) != hipSuccess) return hip_status(e, "twell_linear_bwd");
-      a.p = {reinterpret_cast<const uint16_t*>(base + L.x), ld};
+      gw.p = {reinterpret_cast<const uint16_t*>(base + L.x), ld};
     }
-    a.any = cols % 8 != 0 && !L.pad_x;
-    a.q = dz;
-    a.k = n;
-    e = twell::launch_linear(twell::LINEAR_COLS, L.dw, a, s);
+    gw.any = cols % 8 != 0 && !L.pad_x;
+    gw.k = n;
+    gw.splits = 1;
+    e = L.pair ? twell::launch_linear_pair(gx, gw, s) : twell::launch_linear(twell::LINEAR_COLS, L.dw, gw, s);
   }
   return hip_status(e, "twell_linear_bwd");
 }

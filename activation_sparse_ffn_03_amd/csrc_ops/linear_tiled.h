@@ -295,10 +295,11 @@ __device__ __forceinline__ void linear_tile_of(uint32_t L, uint32_t tb, uint32_t
   t = group * kGroup + in - u * g;
 }
 
-// PA, QA: the operand's lines begin at any element (and hold 8 or more).
+// Workgroup `block` of `blocks` at a product. PA, QA: the operand's lines begin at
+// any element (and hold 8 or more).
 template <class C, bool PK, bool QK, bool PA, bool QA, int ACT, bool RES>
-__global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32_t tb, uint32_t ub) {
-  __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
+__device__ __forceinline__ void linear_items(const LinearArgs& a, uint32_t tb, uint32_t ub, uint32_t block, uint32_t blocks,
+                                             char* smem) {
   constexpr int FU = C::FU, FT = C::FT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wu = wave >> 1, wt = wave & 1;
@@ -309,9 +310,9 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32
   // This workgroup's items (tiles, for each split): every n-th (n workgroups on
   // the XCD) of its XCD's run. There are less than 2^24 of them.
   const uint32_t tiles = tb * ub, items = tiles * a.splits;
-  const uint32_t xcd = blockIdx.x % 8, run = items / 8, extra = items % 8;
-  const uint32_t end = (xcd + 1) * run + min(xcd + 1, extra), stride = (gridDim.x + 7 - xcd) / 8;
-  uint32_t L = xcd * run + min(xcd, extra) + blockIdx.x / 8;
+  const uint32_t xcd = block % 8, run = items / 8, extra = items % 8;
+  const uint32_t end = (xcd + 1) * run + min(xcd + 1, extra), stride = (blocks + 7 - xcd) / 8;
+  uint32_t L = xcd * run + min(xcd, extra) + block / 8;
   if (L >= end) return;
 
   struct Item {
@@ -518,6 +519,12 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32
     L += stride;
   }
   wait_vmcnt<0>();  // no load may write to LDS behind the workgroup's end
+}
+
+template <class C, bool PK, bool QK, bool PA, bool QA, int ACT, bool RES>
+__global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32_t tb, uint32_t ub) {
+  __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
+  linear_items<C, PK, QK, PA, QA, ACT, RES>(a, tb, ub, blockIdx.x, gridDim.x, smem);
 }
 
 using LinearBig = LinearTile<4, 4, 1>;

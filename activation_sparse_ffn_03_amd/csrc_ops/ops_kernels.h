@@ -329,7 +329,13 @@ struct LinearPlan {
   LinearTileSize tile;
   int splits;  // of k; 1 straight from memory
   bool pad;    // lines at any element are copied to lines of whole 16 bytes first
+  double us;   // what it is thought to take
 };
+inline int64_t linear_tiles(LinearTileSize tile, int64_t rows, int units) {
+  const int64_t br = tile == LINEAR_BIG ? 256 : tile == LINEAR_FEW ? 64 : 128;
+  const int64_t bu = tile == LINEAR_BIG || tile == LINEAR_WIDE ? 256 : 128;
+  return ((rows + br - 1) / br) * ((units + bu - 1) / bu);
+}
 // Estimates (us). Tiles: 3.5 a launch, for each item of the busiest compute unit
 // its stages and an end, and where k is split another launch and the partial sums
 // written and read. A stage takes longer when all compute units are at it.
@@ -351,9 +357,7 @@ struct LinearPlan {
 //   512 x 8192 x 512     6: 16.9           6: 19.0      10: 22.4       12: 28.7
 //   5632 x 8192 x 2048   1: 284            1: 173       1: 188 2: 182  1: 151
 inline double linear_tile_us(LinearTileSize tile, int64_t rows, int64_t k, int units, int splits) {
-  const int64_t br = tile == LINEAR_BIG ? 256 : tile == LINEAR_FEW ? 64 : 128;
-  const int64_t bu = tile == LINEAR_BIG || tile == LINEAR_WIDE ? 256 : 128;
-  const int64_t items = ((rows + br - 1) / br) * ((units + bu - 1) / bu) * splits, n = (items + 255) / 256;
+  const int64_t items = linear_tiles(tile, rows, units) * splits, n = (items + 255) / 256;
   const double load = items < 256 ? items / 256.0 : 1.0;
   const double stage = tile == LINEAR_BIG    ? 1.0 + 0.32 * load
                        : tile == LINEAR_WIDE ? 0.57 + 0.15 * load
@@ -377,9 +381,9 @@ inline double linear_direct_us(int64_t rows, int64_t k, int units) {
 // operands) go through registers on their way to LDS, or are copied first, which
 // lines of less than 8 elements need, and the tiles of 256 x 256.
 inline LinearPlan linear_plan(LinearLayout layout, int64_t rows, int64_t k, int units, bool any) {
-  if (rows == 0 || k == 0) return {LINEAR_FEW, 1, false};  // nothing is launched
+  if (rows == 0 || k == 0) return {LINEAR_FEW, 1, false, 0};  // nothing is launched
   const int64_t stages = (k + kLinearStage - 1) / kLinearStage;
-  LinearPlan best{LINEAR_DIRECT, 1, false};
+  LinearPlan best{LINEAR_DIRECT, 1, false, 0};
   double least = layout == LINEAR_ROWS && rows <= 32 ? linear_direct_us(rows, k, units) : 1e30;
   const double copied = layout == LINEAR_ROWS ? (double)k * (rows + units) : (double)k * units;
   const double pad_us = any ? (layout == LINEAR_ROWS ? 5 : 2.5) + 4 * copied / 5e6 : 0;
@@ -388,15 +392,30 @@ inline LinearPlan linear_plan(LinearLayout layout, int64_t rows, int64_t k, int 
     for (int pad = any ? 0 : 1; pad < 2; ++pad) {
       if (pad == 0 && (short_lines || t == LINEAR_BIG)) continue;
       const int fewest = pad == 0 ? 3 : 2;  // stages of a split
+      const int64_t tiles = linear_tiles((LinearTileSize)t, rows, units);
       for (int s = 1; s <= 16 && (s == 1 || fewest * s <= stages); ++s) {
+        if (tiles * s >= kLinearMaxItems) break;  // never with the largest tiles and one split
         const double us = linear_tile_us((LinearTileSize)t, rows, k, units, s) * (pad ? 1 : 1.1) + (pad ? pad_us : 0);
         if (us < least) {
           least = us;
-          best = {(LinearTileSize)t, s, any && pad == 1};
+          best = {(LinearTileSize)t, s, any && pad == 1, us};
         }
       }
     }
   return best;
+}
+// dx = dz w (rows x k x units) and dw = dz^T x (k x rows x units) in one launch of
+// tiles of few rows, all of which run at a time, where that is thought to take
+// less than one product after the other (whole call, bf16, rows x units x cols:
+// 509 x 1021 x 1000 25.5 -> 17.2 us, 1024 x 1024 x 1024 23.2 -> 15.3, 1500 x 700 x
+// 700 46.9 -> 37.1, 33 x 100 x 100 20.5 -> 12.5).
+inline bool linear_paired(int64_t rows, int64_t k, int units, bool any, const LinearPlan& dx, const LinearPlan& dw) {
+  if (rows == 0 || units < 8) return false;
+  const int64_t of_dx = linear_tiles(LINEAR_FEW, rows, units), of_dw = linear_tiles(LINEAR_FEW, k, units);
+  if (of_dx + of_dw > 512) return false;
+  const int64_t longest = (rows > k ? rows : k) + kLinearStage - 1;
+  const double body = (of_dx + of_dw > 256 ? 2 * 0.28 : 0.35) * (double)(longest / kLinearStage);
+  return (5.9 + body) * (any ? 1.1 : 1) < dx.us + dw.us;
 }
 inline size_t linear_part_bytes(const LinearPlan& p, int64_t rows, int units) {
   return p.splits > 1 ? (size_t)p.splits * rows * units * 4 : 0;
@@ -409,6 +428,8 @@ hipError_t launch_linear_rows_mid(const LinearArgs& a, hipStream_t s);
 hipError_t launch_linear_rows_few(const LinearArgs& a, hipStream_t s);
 hipError_t launch_linear_mixed(LinearTileSize tile, const LinearArgs& a, hipStream_t s);
 hipError_t launch_linear_cols(LinearTileSize tile, const LinearArgs& a, hipStream_t s);
+// MIXED and COLS at a time.
+hipError_t launch_linear_pair(const LinearArgs& dx, const LinearArgs& dw, hipStream_t s);
 hipError_t launch_linear_direct(const LinearArgs& a, hipStream_t s);
 hipError_t launch_linear_zero(const LinearOut& o, hipStream_t s);  // y = 0
 // Adds the splits' sums in their order and finishes them.
@@ -427,7 +448,6 @@ struct LinearDzArgs {
   float* db;          // [units] or null
   float* part;        // [linear_db_parts][units] when there are several
 };
-constexpr int kLinearDzUnits = 128;  // of a workgroup
 inline int linear_db_parts(int64_t rows) { return (int)(rows <= 1024 ? 1 : rows <= 65536 ? (rows + 1023) / 1024 : 64); }
 hipError_t launch_linear_dz(const LinearDzArgs& a, hipStream_t s);
 

@@ -100,6 +100,15 @@ hipError_t launch_linear(LinearLayout layout, const LinearPlan& plan, const Line
   ++g_launches;
   return hipSuccess;
 }
+static int g_pairs;
+hipError_t launch_linear_pair(const LinearArgs& dx, const LinearArgs& dw, hipStream_t s) {
+  const int64_t tiles = (dx.out.units + 127) / 128 * ((dx.out.rows + 63) / 64 + (dw.out.rows + 63) / 64);
+  CHECK(tiles <= 512 && dx.out.units == dw.out.units && dx.any == dw.any && dx.splits == 1 && dw.splits == 1, "pair");
+  const LinearPlan few{LINEAR_FEW, 1, false, 0};
+  ++g_pairs;
+  launch_linear(LINEAR_MIXED, few, dx, s);
+  return launch_linear(LINEAR_COLS, few, dw, s);
+}
 hipError_t launch_linear_zero(const LinearOut& o, hipStream_t) {
   extent(o.y, (size_t)o.rows * o.units * (o.y_bf16 ? 2 : 4), "dw");
   ++g_launches;
@@ -234,6 +243,27 @@ int main() {
   g_where = "plans";
   for (int p = 0; p < 5; ++p) CHECK(twell::g_tiles[p] > 0, "tile %d was not reached", p);
   CHECK(twell::g_splits > 0 && twell::g_any > 0 && twell::g_pads > 0, "splits, lines at any element, copies");
+
+  g_where = "pairs";  // tokens, columns, units of test_gpu_linear_variants.py's
+  const int pairs[][3] = {{1, 8, 1}, {33, 100, 100}, {64, 128, 64}, {65, 129, 63}, {1, 4096, 500}, {500, 1000, 9},
+                          {509, 1000, 1021}, {509, 1021, 1000}, {2049, 264, 500}, {2000, 1001, 2000}, {2048, 1024, 2048}};
+  for (const auto& p : pairs) {
+    const int before = twell::g_pairs;
+    linear_case(p[0], p[1], p[2], TWELL_ACT_NONE, TWELL_BF16, TWELL_BF16);
+    CHECK(twell::g_pairs > before, "%d x %d x %d in two launches", p[0], p[1], p[2]);
+  }
+
+  g_where = "tiles of a launch";
+  for (int64_t n : {0x7FFFFFFFll, (1ll << 30) + 1, 1ll << 24, 1ll << 20})
+    for (int units : {1, 8, 15, 100, 129, 2304, 1 << 20})
+      for (int64_t k : {8ll, 64ll, 100000ll})
+        for (bool any : {false, true})
+          for (int layout = 0; layout < 3; ++layout) {
+            if (n * ((units + 7) / 8) >= (1ll << 32) - 256) continue;
+            const twell::LinearPlan p = twell::linear_plan((twell::LinearLayout)layout, n, k, units, any);
+            CHECK(p.tile != twell::LINEAR_DIRECT && twell::linear_tiles(p.tile, n, units) * p.splits < twell::kLinearMaxItems,
+                  "%lld x %lld x %d", (long long)n, (long long)k, units);
+          }
 
   g_where = "limits";
   size_t b = 0;

@@ -75,6 +75,29 @@ def test_weight_gradient_products(rows, k, units):
         assert torch.equal(out, want.to(t))
 
 
+# tokens, columns, units whose two products run in one launch (host_check_sublayer.cpp asks that they do), the last ones
+# nearly as many tiles as run at a time
+PAIRS = [(1, 8, 1), (33, 100, 100), (64, 128, 64), (65, 129, 63), (1, 4096, 500), (500, 1000, 9), (509, 1000, 1021), (509, 1021, 1000),
+         (2049, 264, 500), (2000, 1001, 2000), (2048, 1024, 2048)]
+
+
+@pytest.mark.parametrize("n,cols,units", PAIRS)
+@pytest.mark.parametrize("dx_type,dw_type", [(BF, F32), (F32, BF)])
+def test_both_gradient_products_at_a_time(n, cols, units, dx_type, dw_type):
+    require_gpu()
+    gen = _gen(n + cols)
+    g, x, w = _whole(gen, n, units), _whole(gen, n, cols), _whole(gen, units, cols)
+    (dx, a), (dw, b), (db, c) = _guarded((n, cols), dx_type), _guarded((units, cols), dw_type), _guarded((units,), F32)
+    ws, d = _ws(tw.linear_bwd_ws(n, cols, units, BF, "none"))
+    print(f"[linear bwd] {n}x{cols}x{units} {dx_type} {dw_type}", flush=True)
+    tw.linear_bwd(g, x, w, out=(dx, dw, db), ws=ws)
+    torch.cuda.synchronize()
+    _check_guards(a, b, c, d)
+    assert torch.equal(dx, (g.double() @ w.double()).to(dx_type))
+    assert torch.equal(dw, (g.double().t() @ x.double()).to(dw_type))
+    assert torch.equal(db, g.double().sum(0).float())
+
+
 # one size for each tile, of aligned lines and of lines at any element
 EPILOGUES = [(33, 72, 200), (100, 73, 203), (1000, 72, 2056), (1000, 73, 2059), (1500, 200, 4104), (1500, 129, 4103), (4100, 200, 3000)]
 

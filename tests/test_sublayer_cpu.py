@@ -359,10 +359,10 @@ def test_every_epilogue_is_reached(plans):
     assert seen >= {(t, k) for t in TILES for k in ("aligned", "any")} - {("big", "any")}, seen
 
 
-TILED = sorted(s for s in b.OPS_SOURCES if s.startswith(("linear_rows", "linear_mixed", "linear_cols")))
+TILED = sorted(s for s in b.OPS_SOURCES if s.startswith(("linear_rows", "linear_mixed", "linear_cols", "linear_pair")))
 
 
-@pytest.mark.parametrize("source", ["linear_rows_few.hip", "linear_mixed.hip", "linear_cols.hip"])
+@pytest.mark.parametrize("source", ["linear_rows_few.hip", "linear_mixed.hip", "linear_cols.hip", "linear_pair.hip"])
 def test_waits_in_front_of_loads_into_lds(source):
     """As test_lds_load_wait_cpu.py, of which the tiles' header is the same in every source."""
     loads, m0, base = hazards(_listing(os.path.join(CSRC_OPS, source)))
