@@ -439,6 +439,11 @@ def _addr(t: Optional[torch.Tensor], what: str, shape, dtype=None, device=None):
     return t.data_ptr() or None
 
 
+def _made(t: Optional[torch.Tensor], *_):
+    """_addr of a tensor that the call itself has just allocated, of which there is nothing to check."""
+    return None if t is None else t.data_ptr() or None
+
+
 def _on_gpu(t: torch.Tensor, what: str, device) -> None:
     if not t.is_cuda:
         raise ValueError(f"{what} must be on the GPU")
@@ -733,9 +738,10 @@ def linear(x, w, bias=None, act: str = "none", residual=None, dtype=torch.bfloat
     args = (_addr(x, "x", x.shape, bf), _addr(w, "w", (units, cols), bf, dev), BF16 if bias is None else _code(bias, "bias"),
             _addr(bias, "bias", (units,), None, dev), code, BF16 if residual is None else _code(residual, "residual"),
             _addr(residual, "residual", shape, None, dev), _addr(pre, "pre", shape, bf, dev))
+    to = _addr if out is not None else _made
     if out is None:
         out = _new(stream, lambda: torch.empty(shape, dtype=dtype, device=x.device))
-    yc, y = _code(out, "out"), _addr(out, "out", shape, None, dev)
+    yc, y = _code(out, "out"), to(out, "out", shape, None, dev)
     at, nbytes, _keep = _workspace(ws, ws is None and linear_ws(n, cols, units), x, stream)
     _call(lib().twell_linear, dev, stream, n, cols, units, *args, yc, y, at, nbytes)
     return out
@@ -780,6 +786,7 @@ def linear_bwd(d_out, x, w, act: str = "none", pre=None, bias: bool = True, dx_d
     args = (_code(d_out, "d_out"), _addr(d_out, "d_out", shape, None, dev), code,
             _addr(pre, "pre", shape, bf, dev) if code else None, _addr(x, "x", x.shape, bf),
             _addr(w, "w", (units, cols), bf, dev))
+    to = _addr if out is not None else _made
     if out is None:
         def make():
             e = dict(device=x.device)
@@ -789,9 +796,9 @@ def linear_bwd(d_out, x, w, act: str = "none", pre=None, bias: bool = True, dx_d
     elif not isinstance(out, LinearGrads):
         out = LinearGrads(*out)
     dx, dw, db = out
-    outs = (BF16 if dx is None else _code(dx, "dx"), _addr(dx, "dx", (n, cols), None, dev),
-            BF16 if dw is None else _code(dw, "dw"), _addr(dw, "dw", (units, cols), None, dev),
-            _addr(db, "db", (units,), torch.float32, dev))
+    outs = (BF16 if dx is None else _code(dx, "dx"), to(dx, "dx", (n, cols), None, dev),
+            BF16 if dw is None else _code(dw, "dw"), to(dw, "dw", (units, cols), None, dev),
+            to(db, "db", (units,), torch.float32, dev))
     wanted = (LINEAR_DX if dx is not None else 0) | (LINEAR_DW if dw is not None else 0) | (LINEAR_DB if db is not None else 0)
     need = ws is None and linear_bwd_ws(n, cols, units, d_out.dtype, act, wanted)
     at, nbytes, _keep = _workspace(ws, need, x, stream)
@@ -827,10 +834,11 @@ def dropout(x, rng, p: float, site: int = 0, out=None, stream=None):
         _too_large("twell_dropout", cols)
     dt, dev = _code(x, "x"), x.get_device()
     src = _addr(x, "x", shape)
+    to = _addr if out is not None else _made
     if out is None:
         out = _new(stream, lambda: torch.empty_like(x))
     _call(lib().twell_dropout, dev, stream, rows, cols, dt, src, p, _addr(rng, "rng", (2,), torch.int64, dev), _site(site),
-          _addr(out, "out", shape, x.dtype, dev))
+          to(out, "out", shape, x.dtype, dev))
     return out
 
 
@@ -891,6 +899,7 @@ def join_rms_norm(residual, y, weight, post_weight=None, gate=None, alpha: float
     if cols > _INT32:
         _too_large("twell_join_rms_norm", cols)
     rc, dev = _code(residual, "residual"), residual.get_device()
+    to = _addr if out is not None else _made
     if out is None:
         out = _new(stream, lambda: alloc_join(residual, out_dtype, codes, stats, post_weight is not None))
     elif not isinstance(out, JoinOut):
@@ -903,10 +912,10 @@ def join_rms_norm(residual, y, weight, post_weight=None, gate=None, alpha: float
     _call(
         lib().twell_join_rms_norm, dev, stream, rows, cols, rc, r,
         _code(y, "y"), _addr(y, "y", shape, None, dev), _code(weight, "weight"), _addr(weight, "weight", shape[1:], None, dev),
-        j, eps, _addr(out.residual, "out.residual", shape, residual.dtype, dev),
-        F32 if out.out is None else _code(out.out, "out.out"), _addr(out.out, "out.out", shape, None, dev),
-        _addr(out.codes, "out.codes", shape, torch.uint8, dev), _addr(out.scale, "out.scale", row, torch.float32, dev),
-        _addr(out.rstd, "out.rstd", row, torch.float32, dev), _addr(out.post_rstd, "out.post_rstd", row, torch.float32, dev))
+        j, eps, to(out.residual, "out.residual", shape, residual.dtype, dev),
+        F32 if out.out is None else _code(out.out, "out.out"), to(out.out, "out.out", shape, None, dev),
+        to(out.codes, "out.codes", shape, torch.uint8, dev), to(out.scale, "out.scale", row, torch.float32, dev),
+        to(out.rstd, "out.rstd", row, torch.float32, dev), to(out.post_rstd, "out.post_rstd", row, torch.float32, dev))
     return out
 
 
@@ -946,6 +955,7 @@ def join_rms_norm_bwd(d_out, residual, rstd, y, weight, post_weight=None, post_r
     j = _join(shape, dev, post_weight, gate, alpha, p, rng, site)
     if post_weight is not None and post_rstd is None:
         raise ValueError("post_weight needs post_rstd")
+    to = _addr if out is not None else _made
     if out is None:
         def make():
             e = dict(dtype=torch.float32, device=residual.device)
@@ -959,10 +969,10 @@ def join_rms_norm_bwd(d_out, residual, rstd, y, weight, post_weight=None, post_r
     args = (rows, cols, gc, _addr(d_out, "d_out", shape, None, dev), rc,
             _addr(d_residual, "d_residual", shape, residual.dtype, dev), res, _addr(rstd, "rstd", row, f32, dev), yc,
             _addr(y, "y", shape, None, dev), None if post_weight is None else _addr(post_rstd, "post_rstd", row, f32, dev),
-            wc, _addr(weight, "weight", col, None, dev), j, _addr(out.dr, "dr", shape, residual.dtype, dev),
-            _addr(out.dy, "dy", shape, y.dtype, dev), _addr(out.dw, "dw", col, f32, dev),
-            _addr(out.dpost, "dpost", col, f32, dev),
-            None if gate is None else _addr(out.dgate, "dgate", gate.shape, f32, dev))
+            wc, _addr(weight, "weight", col, None, dev), j, to(out.dr, "dr", shape, residual.dtype, dev),
+            to(out.dy, "dy", shape, y.dtype, dev), to(out.dw, "dw", col, f32, dev),
+            to(out.dpost, "dpost", col, f32, dev),
+            None if gate is None else to(out.dgate, "dgate", gate.shape, f32, dev))
     need = ws is None and join_rms_norm_bwd_ws(rows, cols, post_weight is not None, j.gate_rows)
     at, n, _keep = _workspace(ws, need, residual, stream)
     _call(lib().twell_join_rms_norm_bwd, dev, stream, *args, at, n)
