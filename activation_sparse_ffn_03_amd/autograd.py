@@ -324,6 +324,8 @@ class DropoutFunction(torch.autograd.Function):
 def dropout(x, rng, p: float, site: int = 0):
     """Functional form for any leading dimensions (rows of the mask are those of x as [rows, cols]). rng: see
     twell.make_rng."""
+    if rng is None:
+        raise ValueError("dropout needs rng")
     return DropoutFunction.apply(x.reshape(-1, x.shape[-1]), rng, p, site).reshape(x.shape)
 
 

@@ -312,6 +312,13 @@ def test_shapes_and_types(which, library):  # noqa: F811
     assert not library.calls
 
 
+def test_dropout_needs_its_generator():
+    from activation_sparse_ffn_03_amd import autograd
+    for p in (0.0, 0.5):
+        with pytest.raises(ValueError, match="rng"):
+            autograd.dropout(torch.zeros(2, 8, requires_grad=True), None, p)
+
+
 def test_sizes_beyond_32_bits_are_refused(library):  # noqa: F811
     far = (1 << 32) + 64
     t = lambda *shape, dtype=F32: _OnGpu(shape, dtype)  # noqa: E731
