@@ -6,6 +6,7 @@ namespace twell {
 hipError_t launch_linear_cols(LinearTileSize tile, const LinearArgs& a, hipStream_t s) {
   switch (tile) {
     case LINEAR_BIG: return launch_linear_tile<LinearBig, true, true, TWELL_ACT_NONE, false>(a, s);
+    case LINEAR_TALL: return launch_linear_tile<LinearTall, true, true, TWELL_ACT_NONE, false>(a, s);
     case LINEAR_WIDE: return launch_linear_tile<LinearWide, true, true, TWELL_ACT_NONE, false>(a, s);
     case LINEAR_MID: return launch_linear_tile<LinearMid, true, true, TWELL_ACT_NONE, false>(a, s);
     default: return launch_linear_tile<LinearFew, true, true, TWELL_ACT_NONE, false>(a, s);

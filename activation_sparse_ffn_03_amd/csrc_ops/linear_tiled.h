@@ -98,13 +98,25 @@ struct LinearSide {
   // Four neighbouring k meet four parts of 64 bytes of the banks: k & 3, or with
   // two groups a line, which reach half of the banks, k / 2 & 1.
   static __device__ __forceinline__ int turn(int k) { return B >= 128 ? k & 3 : k >> 1 & 1; }
-  int line, col;     // this lane's line in a load of g = 0, and its bytes in the line
+  // 192 elements a line are no whole share of a load: piece 256 g + first of the
+  // stage's is what this lane loads, and the fragments' groups go round by k / 2 & 1
+  // (eight k are 96 four-byte banks apart: again every bank twice).
+  static constexpr bool ODD = KROWS && B == 192;
+  static constexpr int PIECES = B / 8;  // of a k line
+  int line, col;     // this lane's line in a load of g = 0 (ODD: first), and its bytes in the line
   uint32_t at[KROWS ? F : 4];  // LDS bytes of this lane's operands (fragments, or steps)
   uint32_t ld2;      // bytes of a line
   uint32_t off[LOADS];  // bytes from a stage's first line and k to what this lane loads
 
   __device__ __forceinline__ LinearSide(const LinearOperand& o, int lane, int wave, int w) : ld2((uint32_t)(2 * o.ld)) {
-    if constexpr (KROWS) {
+    if constexpr (ODD) {
+      line = 64 * wave + lane;
+      col = 0;
+      const int i16 = lane & 15, k = 8 * (lane >> 5) + (i16 >> 2);
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+        at[i] = k * (2 * B) + ((w * F + i + (k >> 1 & 1)) % (B / 32) << 6) + 32 * ((lane >> 4) & 1) + 8 * (i16 & 3);
+    } else if constexpr (KROWS) {
       constexpr int SLOTS = 64 / PER;
       line = wave * PER + lane / SLOTS;
       const int slot = lane % SLOTS;
@@ -121,13 +133,22 @@ struct LinearSide {
       for (int ks = 0; ks < 4; ++ks) at[ks] = w * F * 4096 + row * 128 + ((2 * ks + (lane >> 5)) ^ key) * 16;
     }
   }
+  // The line of load g, and the bytes in it.
+  __device__ __forceinline__ int line_at(int g) const {
+    return ODD ? (line + 256 * g) / PIECES : line + (KROWS ? 4 * PER : 32) * g;
+  }
+  __device__ __forceinline__ int col_at(int g) const {
+    if constexpr (!ODD) return col;
+    const int slot = (line + 256 * g) % PIECES, groups = B / 32;
+    return 64 * (((slot >> 2) + groups - (line_at(g) >> 1 & 1)) % groups) + 16 * (slot & 3);
+  }
   // Lines, or elements of a line, behind `last` read that one. 16 bytes of a
   // line that begin before its end may reach into the next line: there they are
   // the result's columns that are not stored.
-  __device__ __forceinline__ int reach(int last) const { return min(col, last / 8 * 16); }
+  __device__ __forceinline__ int reach(int g, int last) const { return min(col_at(g), last / 8 * 16); }
   __device__ __forceinline__ uint32_t offset(int g, int last) const {
-    if constexpr (KROWS) return (uint32_t)(line + 4 * PER * g) * ld2 + (uint32_t)reach(last);
-    else return (uint32_t)min(line + 32 * g, last) * ld2 + (uint32_t)col;
+    if constexpr (KROWS) return (uint32_t)line_at(g) * ld2 + (uint32_t)reach(g, last);
+    else return (uint32_t)min(line_at(g), last) * ld2 + (uint32_t)col;
   }
   __device__ __forceinline__ void offsets(int last) {
 #pragma unroll
@@ -139,7 +160,7 @@ struct LinearSide {
   }
   // ... and of any stage: k from `k_left` on are zeros.
   __device__ __forceinline__ void issue_any(const char* base, int last, int k_left, int g, uint32_t lds, int wave) const {
-    const bool in = KROWS ? line + 4 * PER * g < k_left : col < 2 * k_left;
+    const bool in = KROWS ? line_at(g) < k_left : col < 2 * k_left;
     linear_dma_at(in ? base + offset(g, last) : reinterpret_cast<const char*>(&linear_zeros), lds + (wave + 4 * g) * 1024);
   }
   // Operands whose lines begin at any element go through registers: load g of a
@@ -153,8 +174,8 @@ struct LinearSide {
   // zeros then.
   __device__ __forceinline__ u32x4_t fetch_any(const char* base, int last, int k_left, int g) const {
     int64_t at;
-    if constexpr (KROWS) at = (int64_t)min(line + 4 * PER * g, k_left - 1) * ld2 + (k_left > 64 ? reach(last) : min(col, 2 * last - 14));
-    else at = (int64_t)min(line + 32 * g, last) * ld2 + min(col, 2 * k_left - 16);
+    if constexpr (KROWS) at = (int64_t)min(line_at(g), k_left - 1) * ld2 + (k_left > 64 ? reach(g, last) : min(col, 2 * last - 14));
+    else at = (int64_t)min(line_at(g), last) * ld2 + min(col, 2 * k_left - 16);
     return *reinterpret_cast<const u32x4_a2_t*>(base + at);
   }
   __device__ __forceinline__ u32x4_t fix(u32x4_t v, int last, int k_left, int g) const {
@@ -164,7 +185,7 @@ struct LinearSide {
       if (s & 2) v = u32x4_t{v[1], v[2], v[3], 0u};
       if (s & 1) v = u32x4_t{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
     }
-    const bool none = KROWS ? line + 4 * PER * g >= k_left : s >= 8;
+    const bool none = KROWS ? line_at(g) >= k_left : s >= 8;
     return none ? u32x4_t{0u, 0u, 0u, 0u} : v;
   }
   __device__ __forceinline__ void put(const u32x4_t& v, char* side, int g, int wave, int lane) const {
@@ -529,6 +550,7 @@ __global__ __launch_bounds__(256, C::OCC) void linear_tiled(LinearArgs a, uint32
 
 using LinearBig = LinearTile<4, 4, 1>;
 using LinearMid = LinearTile<2, 2, 2>;
+using LinearTall = LinearTile<4, 3, 1>;
 using LinearWide = LinearTile<4, 2, 1>;
 using LinearFew = LinearTile<2, 1, 2>;
 
@@ -544,8 +566,8 @@ hipError_t launch_linear_tile(const LinearArgs& a, hipStream_t s) {
     return hipGetLastError();
   };
   if (a.any) {
-    // in tiles of 256 x 256 there are no registers for it
-    if constexpr (C::FU * C::FT < 16) return go(std::true_type{}, std::bool_constant<!PK>{});
+    // in the largest tiles there are no registers for it
+    if constexpr (C::FU * C::FT < 12) return go(std::true_type{}, std::bool_constant<!PK>{});
     else return hipErrorInvalidValue;
   }
   return go(std::false_type{}, std::false_type{});

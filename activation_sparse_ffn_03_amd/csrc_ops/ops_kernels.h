@@ -323,6 +323,7 @@ enum LinearTileSize {
   LINEAR_FEW,   // 64 rows x 128 units, two workgroups a compute unit
   LINEAR_MID,   // 128 x 128, two workgroups a compute unit
   LINEAR_WIDE,  // 128 rows x 256 units
+  LINEAR_TALL,  // 192 rows x 256 units, for LINEAR_COLS, whose results are a weight's and few: whole rounds of tiles
   LINEAR_BIG    // 256 x 256
 };
 struct LinearPlan {
@@ -332,8 +333,8 @@ struct LinearPlan {
   double us;   // what it is thought to take
 };
 inline int64_t linear_tiles(LinearTileSize tile, int64_t rows, int units) {
-  const int64_t br = tile == LINEAR_BIG ? 256 : tile == LINEAR_FEW ? 64 : 128;
-  const int64_t bu = tile == LINEAR_BIG || tile == LINEAR_WIDE ? 256 : 128;
+  const int64_t br = tile == LINEAR_BIG ? 256 : tile == LINEAR_TALL ? 192 : tile == LINEAR_FEW ? 64 : 128;
+  const int64_t bu = tile >= LINEAR_WIDE ? 256 : 128;
   return ((rows + br - 1) / br) * ((units + bu - 1) / bu);
 }
 // Estimates (us). Tiles: 3.5 a launch, for each item of the busiest compute unit
@@ -355,16 +356,19 @@ inline int64_t linear_tiles(LinearTileSize tile, int64_t rows, int units) {
 //   1000 x 8192 x 1024   1: 48.8 4: 30.1   4: 31.7      6: 41.3        10: 64.1
 //   1021 x 509 x 1000    1: 8.2 2: 13.0    1: 10.0      1: 14.4        1: 22.5
 //   512 x 8192 x 512     6: 16.9           6: 19.0      10: 22.4       12: 28.7
-//   5632 x 8192 x 2048   1: 284            1: 173       1: 188 2: 182  1: 151
+//   5632 x 8192 x 2048   1: 284            1: 173       1: 188 2: 182  1: 145 (TALL 135: 240 tiles for 256
+//     compute units, not 176)
+//   1500 x 8192 x 3000   3: 131            4: 101       1: 92          3: 92 (TALL 2: 83)
 inline double linear_tile_us(LinearTileSize tile, int64_t rows, int64_t k, int units, int splits) {
   const int64_t items = linear_tiles(tile, rows, units) * splits, n = (items + 255) / 256;
   const double load = items < 256 ? items / 256.0 : 1.0;
   const double stage = tile == LINEAR_BIG    ? 1.0 + 0.32 * load
+                       : tile == LINEAR_TALL ? 0.75 + 0.23 * load
                        : tile == LINEAR_WIDE ? 0.57 + 0.15 * load
                        : tile == LINEAR_MID  ? 0.38 + 0.05 * load
                        : n == 1              ? 0.35
                                              : 0.28;
-  const double end = tile == LINEAR_BIG ? 9.0 : tile == LINEAR_WIDE ? 4.5 : tile == LINEAR_MID ? 2.0 : 1.2;
+  const double end = tile == LINEAR_BIG ? 9.0 : tile == LINEAR_TALL ? 7.0 : tile == LINEAR_WIDE ? 4.5 : tile == LINEAR_MID ? 2.0 : 1.2;
   const int64_t stages = ((k + kLinearStage - 1) / kLinearStage + splits - 1) / splits;
   const double body = n * stages * stage, reads = 2.0 * k * (rows + units) / 6.5e6;
   const double join = splits > 1 ? 2.5 + 8.0 * splits * rows * units / 5.5e6 : 0;
@@ -390,7 +394,8 @@ inline LinearPlan linear_plan(LinearLayout layout, int64_t rows, int64_t k, int 
   const bool short_lines = (layout == LINEAR_ROWS ? k : units) < 8;
   for (int t = LINEAR_FEW; t <= LINEAR_BIG; ++t)
     for (int pad = any ? 0 : 1; pad < 2; ++pad) {
-      if (pad == 0 && (short_lines || t == LINEAR_BIG)) continue;
+      if (t == LINEAR_TALL && layout != LINEAR_COLS) continue;
+      if (pad == 0 && (short_lines || t >= LINEAR_TALL)) continue;
       const int fewest = pad == 0 ? 3 : 2;  // stages of a split
       const int64_t tiles = linear_tiles((LinearTileSize)t, rows, units);
       for (int s = 1; s <= 16 && (s == 1 || fewest * s <= stages); ++s) {

@@ -67,7 +67,7 @@ hipError_t launch_dropout(const DropoutArgs& a, hipStream_t) {
   return hipSuccess;
 }
 
-static int g_tiles[5], g_splits, g_any, g_pads;
+static int g_tiles[6], g_splits, g_any, g_pads;
 hipError_t launch_linear(LinearLayout layout, const LinearPlan& plan, const LinearArgs& a, hipStream_t) {
   const LinearOut& o = a.out;
   ++g_tiles[plan.tile];
@@ -75,7 +75,8 @@ hipError_t launch_linear(LinearLayout layout, const LinearPlan& plan, const Line
   g_any += a.any;
   const bool direct = plan.tile == LINEAR_DIRECT;
   CHECK(!direct || (layout == LINEAR_ROWS && plan.splits == 1), "straight from memory");
-  CHECK(!(a.any && plan.tile == LINEAR_BIG), "no registers");
+  CHECK(!(a.any && plan.tile >= LINEAR_TALL), "no registers");
+  CHECK(plan.tile != LINEAR_TALL || layout == LINEAR_COLS, "a tile of one layout");
   // lines: of the side (p: units, q: rows) with k neighbouring, or k lines; read in whole 16 bytes unless at any element
   auto operand = [&](const LinearOperand& p, bool k_lines, bool any, int64_t side, const char* what) {
     const int64_t lines = k_lines ? a.k : side, line = k_lines ? side : a.k;
@@ -241,7 +242,7 @@ int main() {
   linear_case(300, 8192, 4000, TWELL_ACT_SILU, TWELL_F32, TWELL_BF16);
   linear_case(3000, 2001, 4105, TWELL_ACT_RELU, TWELL_BF16, TWELL_F32);
   g_where = "plans";
-  for (int p = 0; p < 5; ++p) CHECK(twell::g_tiles[p] > 0, "tile %d was not reached", p);
+  for (int p = 0; p < 6; ++p) CHECK(twell::g_tiles[p] > 0, "tile %d was not reached", p);
   CHECK(twell::g_splits > 0 && twell::g_any > 0 && twell::g_pads > 0, "splits, lines at any element, copies");
 
   g_where = "pairs";  // tokens, columns, units of test_gpu_linear_variants.py's

@@ -6,7 +6,7 @@
 #include "ops_kernels.h"
 
 int main() {
-  const char* names[] = {"direct", "few", "mid", "wide", "big"};
+  const char* names[] = {"direct", "few", "mid", "wide", "tall", "big"};
   int layout, units;
   long long rows, k;
   while (std::scanf("%d %lld %lld %d", &layout, &rows, &k, &units) == 4) {

@@ -23,6 +23,7 @@ ROWS = [(33, 7, 64), (33, 8, 64), (33, 73, 64), (33, 1000, 64), (33, 1001, 64), 
 OTHERS = [(33, 8, 64), (33, 8, 7), (33, 8, 100), (33, 1000, 64), (33, 1000, 100), (1000, 8, 2056), (4100, 8, 500), (4100, 4001, 64),
           (3000, 2000, 129), (1500, 129, 4104), (1500, 129, 4105), (4100, 129, 3000), (3000, 520, 4105), (8000, 8, 4105),
           (300, 8192, 4000), (3000, 32768, 129), (1500, 8192, 3000)]
+COLS = OTHERS + [(5632, 512, 2048), (5600, 513, 2056), (5000, 200, 2048), (1000, 32768, 3704)]
 
 
 @pytest.mark.parametrize("rows,k,units", ROWS)
@@ -58,7 +59,7 @@ def test_input_gradient_products(rows, k, units):
         assert torch.equal(out, want.to(t))
 
 
-@pytest.mark.parametrize("rows,k,units", OTHERS)
+@pytest.mark.parametrize("rows,k,units", COLS)
 def test_weight_gradient_products(rows, k, units):
     """dw of `rows` units, `units` columns and k tokens."""
     require_gpu()

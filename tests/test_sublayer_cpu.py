@@ -354,10 +354,12 @@ TILES = ("few", "mid", "wide", "big")
 
 
 def test_every_product_is_reached(plans):
-    for layout, sizes in ((0, variants.ROWS), (1, variants.OTHERS), (2, variants.OTHERS)):
+    for layout, sizes in ((0, variants.ROWS), (1, variants.OTHERS), (2, variants.COLS)):
         seen = set(plans(layout, sizes))
         want = {(t, s, k) for t in TILES for s in ("whole", "split") for k in ("aligned", "any")} - {("big", s, "any") for s in ("whole", "split")}
         want |= {("few", "whole", "copied"), ("big", "whole", "copied")}
+        if layout == 2:
+            want |= {("tall", "whole", "aligned"), ("tall", "split", "aligned")}
         assert want <= seen, (layout, want - seen)
 
 
