@@ -41,7 +41,7 @@ hipError_t launch_join(const LinearArgs& a, hipStream_t s) {
 
 __global__ __launch_bounds__(256) void linear_pad_kernel(const uint16_t* __restrict__ in, int64_t rows, int cols,
                                                          uint16_t* __restrict__ out, int64_t ld) {
-  const int chunks = (int)(ld / 8);
+  const int chunks = (cols + 7) / 8;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / chunks;
   if (row >= rows) return;
   const int col = 8 * (int)(i - row * chunks);
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(256) void linear_db_sum(const float* __restrict__ p
 
 template <int ACT>
 hipError_t launch_dz(const LinearDzArgs& a, hipStream_t s) {
-  const int parts = linear_db_parts(a.rows);
+  const int parts = linear_db_parts(a.rows, a.units);
   auto go = [&](auto kernel, int t) {
     TWELL_LAUNCH("linear_dz", kernel, dim3((a.units + 8 * t - 1) / (8 * t), parts), 1024, 0, s, a);
   };
@@ -177,7 +177,7 @@ hipError_t launch_linear_join(const LinearArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_linear_pad(const void* in, int64_t rows, int cols, void* out, int64_t ld, hipStream_t s) {
-  const dim3 grid((unsigned)((rows * (ld / 8) + 255) / 256));
+  const dim3 grid((unsigned)((rows * ((cols + 7) / 8) + 255) / 256));
   TWELL_LAUNCH("linear_pad", linear_pad_kernel, grid, 256, 0, s, static_cast<const uint16_t*>(in), rows, cols,
                static_cast<uint16_t*>(out), ld);
   return hipGetLastError();

@@ -43,7 +43,7 @@ ForwardLayout forward_layout(int64_t n, int32_t cols, int32_t units) {
   ForwardLayout L{};
   L.plan = twell::linear_plan(twell::LINEAR_ROWS, n, cols, units, cols % 8 != 0);
   L.pad = L.plan.pad;
-  const size_t ld = (size_t)twell::linear_pad(cols);
+  const size_t ld = (size_t)twell::linear_line(cols);
   Pieces p;
   L.x = p.take(L.pad ? (size_t)n * ld * 2 : 0);
   L.w = p.take(L.pad ? (size_t)units * ld * 2 : 0);
@@ -70,12 +70,12 @@ BackwardLayout backward_layout(int64_t n, int32_t cols, int32_t units, bool d_ou
   L.dz = (dx || dw) && (act != TWELL_ACT_NONE || !d_out_bf16 || units % 8 != 0);
   L.pad_x = dw && L.dw.pad;
   L.pad_w = dx && L.dx.pad;
-  const size_t ld = (size_t)twell::linear_pad(cols);
+  const size_t ld = (size_t)twell::linear_line(cols);
   Pieces p;
-  L.dz_at = p.take(L.dz ? (size_t)n * twell::linear_pad(units) * 2 : 0);
+  L.dz_at = p.take(L.dz ? (size_t)n * twell::linear_line(units) * 2 : 0);
   L.x = p.take(L.pad_x ? (size_t)n * ld * 2 : 0);
   L.w = p.take(L.pad_w ? (size_t)units * ld * 2 : 0);
-  const int parts = twell::linear_db_parts(n);
+  const int parts = twell::linear_db_parts(n, units);
   L.db = p.take(wanted & TWELL_LINEAR_DB && parts > 1 ? (size_t)parts * units * 4 : 0);
   const size_t part_dx = dx ? twell::linear_part_bytes(L.dx, n, cols) : 0, part_dw = dw ? twell::linear_part_bytes(L.dw, units, cols) : 0;
   L.part = p.take(part_dx > part_dw ? part_dx : part_dw);
@@ -126,13 +126,13 @@ twell_status twell_linear(int64_t n, int32_t cols, int32_t units, const void* x,
   a.out = {n, units, bias, residual, pre, y, bias_dtype == TWELL_BF16, res_dtype == TWELL_BF16, y_dtype == TWELL_BF16, act};
   a.any = cols % 8 != 0 && !L.pad && L.plan.tile != twell::LINEAR_DIRECT;
   if (L.pad) {
-    const int64_t ld = twell::linear_pad(cols);
+    const int64_t ld = twell::linear_line(cols);
     hipError_t e = twell::launch_linear_pad(x, n, cols, base + L.x, ld, s);
     if (e == hipSuccess) e = twell::launch_linear_pad(w, units, cols, base + L.w, ld, s);
     if (e != hipSuccess) return hip_status(e, "twell_linear");
     a.p = {reinterpret_cast<const uint16_t*>(base + L.w), ld};
     a.q = {reinterpret_cast<const uint16_t*>(base + L.x), ld};
-    a.k = ld;  // zeros behind the last column
+    a.k = twell::linear_pad(cols);  // zeros behind the last column
   }
   a.part = reinterpret_cast<float*>(base + L.part);
   return hip_status(twell::launch_linear(twell::LINEAR_ROWS, L.plan, a, s), "twell_linear");
@@ -188,7 +188,7 @@ twell_status twell_linear_bwd(int64_t n, int32_t cols, int32_t units, twell_dtyp
     z.pre = pre;
     if (L.dz && n > 0) {
       z.dz = reinterpret_cast<uint16_t*>(base + L.dz_at);
-      z.ld = twell::linear_pad(units);
+      z.ld = twell::linear_line(units);
       dz = {z.dz, z.ld};
     }
     z.db = db;
@@ -196,7 +196,7 @@ twell_status twell_linear_bwd(int64_t n, int32_t cols, int32_t units, twell_dtyp
     if (n > 0 || db != nullptr) e = twell::launch_linear_dz(z, s);
     if (e != hipSuccess) return hip_status(e, "twell_linear_bwd");
   }
-  const int64_t ld = twell::linear_pad(cols);
+  const int64_t ld = twell::linear_line(cols);
   twell::LinearArgs gx{}, gw{};
   gx.q = gw.q = dz;
   gx.part = gw.part = reinterpret_cast<float*>(base + L.part);

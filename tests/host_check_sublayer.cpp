@@ -130,7 +130,7 @@ hipError_t launch_linear_dz(const LinearDzArgs& a, hipStream_t) {
   if (a.dz) CHECK(a.ld % 8 == 0 && a.ld >= a.units, "lines of dz");
   if (a.dz) extent(a.dz, (size_t)a.rows * a.ld * 2, "dz");
   if (a.db) extent(a.db, (size_t)a.units * 4, "db");
-  const int parts = linear_db_parts(a.rows);
+  const int parts = linear_db_parts(a.rows, a.units);
   CHECK(parts >= 1 && parts <= 64, "%d parts", parts);
   if (a.db && parts > 1) extent(a.part, (size_t)parts * a.units * 4, "ws.db");
   ++g_launches;
