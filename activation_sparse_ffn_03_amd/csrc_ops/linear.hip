@@ -53,8 +53,9 @@ __global__ __launch_bounds__(256) void linear_pad_kernel(const uint16_t* __restr
 // dz = d_out * act'(pre), and the sums of its columns over a run of rows. T
 // threads side by side take 8 units each, 1024 / T rows at a time: 16, whole
 // lines of 256 bytes, or 4 up to 1024 rows, which then need no second launch for
-// the sums and still spread over the chip (509 x 1021 7.4 us, with 16 threads and
-// a second launch 10.1; 8192 x 5632 62, with 256 threads a workgroup 72).
+// the sums and still spread over the chip (509 x 1021 5.7 us, with 16 threads and
+// a second launch 10.1). Bound by memory: 8192 x 5632 59 us, 4.7 TB/s (with 256
+// threads a workgroup 72).
 template <int ACT, typename TG, int T>
 __global__ __launch_bounds__(1024) void linear_dz_kernel(LinearDzArgs a) {
   constexpr int SIDES = 1024 / T, BATCH = T == 16 ? 4 : 2;
@@ -74,23 +75,46 @@ __global__ __launch_bounds__(1024) void linear_dz_kernel(LinearDzArgs a) {
     for (int k = 0; k < 8; ++k) sum[k] += g[k];
     if (a.dz != nullptr) store_some<8>(a.dz, 1, row * a.ld + unit, 8, g);  // zeros behind the last unit
   };
-  if (have >= 8) {
+  // The last units of a row that is no whole number of 8 are read with those in
+  // front of them, as 8, and moved down.
+  const int back = have < 8 ? 8 - have : 0;
+  auto fetch = [&](const void* p, int is_bf16, int64_t row, float (&v)[8]) {
+    load_some<8>(p, is_bf16, row * a.units + unit - back, 8, v);
+  };
+  auto settle = [&](float (&v)[8]) {  // when all loads are on their way
+#pragma unroll
+    for (int s = 4; s > 0; s /= 2) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = back & s ? (k + s < 8 ? v[k + s] : 0.f) : v[k];
+    }
+  };
+  if (have > 0 && a.units >= 8) {
     int64_t row = r0 + side;
     for (; row + (BATCH - 1) * SIDES < r1; row += BATCH * SIDES) {
       float g[BATCH][8], z[BATCH][8];
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        const int64_t at = (row + i * SIDES) * a.units + unit;
-        load_some<8>(a.d_out, G_BF16, at, 8, g[i]);
-        if constexpr (ACT != TWELL_ACT_NONE) load_some<8>(a.pre, 1, at, 8, z[i]);
+        fetch(a.d_out, G_BF16, row + i * SIDES, g[i]);
+        if constexpr (ACT != TWELL_ACT_NONE) fetch(a.pre, 1, row + i * SIDES, z[i]);
+      }
+      if (back > 0) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          settle(g[i]);
+          if constexpr (ACT != TWELL_ACT_NONE) settle(z[i]);
+        }
       }
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) finish(row + i * SIDES, g[i], z[i]);
     }
     for (; row < r1; row += SIDES) {
       float g[8], z[8];
-      load_some<8>(a.d_out, G_BF16, row * a.units + unit, 8, g);
-      if constexpr (ACT != TWELL_ACT_NONE) load_some<8>(a.pre, 1, row * a.units + unit, 8, z);
+      fetch(a.d_out, G_BF16, row, g);
+      if constexpr (ACT != TWELL_ACT_NONE) fetch(a.pre, 1, row, z);
+      if (back > 0) {
+        settle(g);
+        if constexpr (ACT != TWELL_ACT_NONE) settle(z);
+      }
       finish(row, g, z);
     }
   } else if (have > 0) {
