@@ -12,7 +12,8 @@
 //   sum(dv post_w yh) = sum((d_residual + rho d_out w) k yh) - rho c sum(xh k yh),  k = gate m post_w,
 // so that a row is reduced once, three sums at a time.
 //
-// Bound by memory: one pass over d_out, d_residual, r' and y. A workgroup takes
+// Bound by memory: one pass over d_out, d_residual, r' and y (8192 x 2048 52 us,
+// 5.1 TB/s, 5 of them the second launch; 131 x 1000 8). A workgroup takes
 // rows that share one row of the gate, or all rows of several rows of it, keeps
 // its sums in registers (thread t owns the same columns in every row) and leaves
 // partial rows; a second launch adds them in a fixed order.

@@ -9,7 +9,8 @@
 // 24 x 5632 x 2048 15.1, however many loads are in flight). So a load takes 8
 // whole lines of 128 bytes, lane l piece l & 7 of line l >> 3, and the wave turns
 // them in LDS of its own, without barriers: piece p of line r lies at piece
-// p ^ (r & 7), which keeps both sides' accesses on different banks.
+// p ^ (r & 7), which keeps both sides' accesses on different banks: 14.6 us (6.2
+// TB/s, most of w from the 256 MB cache) and 8.2.
 //
 // A wave has DEPTH steps' loads on their way all the time; loads lie in no branch,
 // since the compiler waits for all of them where branches meet.
