@@ -229,6 +229,12 @@ def _grad(t: torch.Tensor) -> torch.Tensor:
     return _packed(t if t.dtype in (torch.bfloat16, torch.float32) else t.float())
 
 
+def _recorded(*tensors):
+    """The tensors, detached where no gradient is recorded (torch.no_grad): a function's needs_input_grad goes by the
+    tensors alone, and its forward would write what only a backward reads."""
+    return tensors if torch.is_grad_enabled() else tuple(None if t is None else t.detach() for t in tensors)
+
+
 class LinearFunction(torch.autograd.Function):
     """y = residual + act(x · w^T + bias) through libtwell's kernels both ways. x [rows, cols] and w [units, cols] bf16,
     bias [units] and residual [rows, units] bf16, fp32 or None."""
@@ -272,6 +278,7 @@ def linear(x, w, bias=None, act: str = "none", residual=None, out_dtype=None):
         if residual.shape != shape:
             raise ValueError(f"residual must have shape {tuple(shape)}, got {tuple(residual.shape)}")
         residual = residual.reshape(-1, shape[-1])
+    x, w, bias, residual = _recorded(x, w, bias, residual)
     return LinearFunction.apply(x.reshape(-1, x.shape[-1]), w, bias, residual, act, out_dtype).reshape(shape)
 
 
@@ -326,6 +333,7 @@ def dropout(x, rng, p: float, site: int = 0):
     twell.make_rng."""
     if rng is None:
         raise ValueError("dropout needs rng")
+    x, = _recorded(x)
     return DropoutFunction.apply(x.reshape(-1, x.shape[-1]), rng, p, site).reshape(x.shape)
 
 
@@ -371,6 +379,7 @@ def join_rms_norm(residual, y, weight, post_weight=None, gate=None, alpha: float
     shape = residual.shape
     if y.shape != shape:
         raise ValueError("y must have the shape of the residual")
+    residual, y, weight, post_weight, gate = _recorded(residual, y, weight, post_weight, gate)
     r, out = JoinRmsNormFunction.apply(residual.reshape(-1, shape[-1]), y.reshape(-1, shape[-1]), weight, post_weight, gate,
                                        alpha, eps, p, rng, site, out_dtype)
     return r.reshape(shape), out.reshape(shape)

@@ -319,6 +319,36 @@ def test_dropout_needs_its_generator():
             autograd.dropout(torch.zeros(2, 8, requires_grad=True), None, p)
 
 
+@pytest.mark.parametrize("grad", [True, False])
+def test_nothing_is_kept_where_no_gradient_is_recorded(grad, monkeypatch):
+    """Under no_grad the layers' parameters ask for a gradient all the same: the forward keeps no pre-activation, statistics
+    or generator's state."""
+    from activation_sparse_ffn_03_amd import autograd
+    kept = []
+
+    def linear(x, w, pre=None, **kw):
+        kept.append(pre is not None)
+        return torch.zeros(x.shape[0], w.shape[0], dtype=BF)
+
+    def join(residual, y, weight, stats=False, **kw):
+        kept.append(stats)
+        rows = torch.zeros(residual.shape[0])
+        return tw.JoinOut(residual.clone(), residual.clone(), None, None, rows, None)
+
+    monkeypatch.setattr(tw, "linear", linear)
+    monkeypatch.setattr(tw, "join_rms_norm", join)
+    monkeypatch.setattr(tw, "dropout", lambda x, *a, **kw: x.clone())
+    layer = autograd.TwellLinear(8, 16, act="silu", device="cpu")
+    norm = autograd.TwellJoin(16, post_norm=False, dtype=F32, device="cpu")
+    with torch.set_grad_enabled(grad):
+        y = layer(torch.zeros(2, 3, 8, dtype=BF))
+        r, out = norm(torch.zeros(2, 3, 16), y.float())
+        d = autograd.dropout(layer.bias, tw.make_rng(1, device="cpu"), 0.5)
+    assert kept == [grad, grad]
+    assert all((t.grad_fn is not None) == grad for t in (y, r, out, d))
+    assert y.shape == (2, 3, 16) and out.shape == (2, 3, 16) and d.shape == (16,)
+
+
 def test_sizes_beyond_32_bits_are_refused(library):  # noqa: F811
     far = (1 << 32) + 64
     t = lambda *shape, dtype=F32: _OnGpu(shape, dtype)  # noqa: E731
