@@ -183,12 +183,24 @@ __global__ __launch_bounds__(256) void linear_zero(LinearOut o, int chunks) {
   store_some<8>(o.y, o.y_bf16, row * o.units + unit, o.units - unit, z);
 }
 
+// A launch holds less than 2^32 threads, one for each 8 elements here, and a
+// weight may have more of them.
+int64_t rows_of_a_launch(int chunks) { return ((1ll << 32) - 256) / chunks; }
+
 }  // namespace
 
-hipError_t launch_linear_zero(const LinearOut& o, hipStream_t s) {
-  const int chunks = (o.units + 7) / 8;
-  TWELL_LAUNCH("linear_zero", linear_zero, dim3((unsigned)((o.rows * chunks + 255) / 256)), 256, 0, s, o, chunks);
-  return hipGetLastError();
+hipError_t launch_linear_zero(const LinearOut& all, hipStream_t s) {
+  const int chunks = (all.units + 7) / 8;
+  LinearOut o = all;
+  const int64_t most = rows_of_a_launch(chunks);
+  for (int64_t left = all.rows; left > 0; left -= most) {
+    o.rows = left < most ? left : most;
+    TWELL_LAUNCH("linear_zero", linear_zero, dim3((unsigned)((o.rows * chunks + 255) / 256)), 256, 0, s, o, chunks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    o.y = static_cast<char*>(o.y) + most * o.units * (o.y_bf16 ? 2 : 4);
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_linear_join(const LinearArgs& a, hipStream_t s) {
@@ -201,10 +213,17 @@ hipError_t launch_linear_join(const LinearArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_linear_pad(const void* in, int64_t rows, int cols, void* out, int64_t ld, hipStream_t s) {
-  const dim3 grid((unsigned)((rows * ((cols + 7) / 8) + 255) / 256));
-  TWELL_LAUNCH("linear_pad", linear_pad_kernel, grid, 256, 0, s, static_cast<const uint16_t*>(in), rows, cols,
-               static_cast<uint16_t*>(out), ld);
-  return hipGetLastError();
+  const int chunks = (cols + 7) / 8;
+  const uint16_t* from = static_cast<const uint16_t*>(in);
+  uint16_t* to = static_cast<uint16_t*>(out);
+  const int64_t most = rows_of_a_launch(chunks);
+  for (int64_t left = rows; left > 0; left -= most, from += most * cols, to += most * ld) {
+    const int64_t here = left < most ? left : most;
+    TWELL_LAUNCH("linear_pad", linear_pad_kernel, dim3((unsigned)((here * chunks + 255) / 256)), 256, 0, s, from, here, cols, to, ld);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_linear_dz(const LinearDzArgs& a, hipStream_t s) {

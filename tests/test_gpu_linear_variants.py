@@ -141,3 +141,22 @@ def test_results_beyond_32_bits_of_elements():
         got, want = dx[part].double(), y[part].double() @ w.double()
         tol = (y[part].double().abs() @ w.double().abs()) * units * lr.U
         assert bool(((got - want).abs() <= lr.rounded(tol, want, BF)).all())
+
+
+def test_weights_of_more_elements_than_a_launch_writes():
+    """A weight's gradient of no rows, of more than 2^32 pieces of 8: zeros in its first and last rows and around the border
+    of two launches."""
+    require_gpu()
+    units, cols = (1 << 18) + 3, (1 << 17) + 4
+    pieces = (cols + 7) // 8
+    assert units * pieces > 1 << 32
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 150 GB of free device memory")
+    e = lambda *s: torch.empty(*s, dtype=BF, device="cuda")  # noqa: E731
+    x, w, dw = e(0, cols), e(units, cols), e(units, cols).fill_(3)
+    tw.linear_bwd(e(0, units), x, w, out=(None, dw, None))
+    border = ((1 << 32) - 256) // pieces
+    for part in (slice(0, 9), slice(border - 9, border + 9), slice(units - 9, units)):
+        assert not dw[part].any()
+    del w, dw
+    torch.cuda.empty_cache()
