@@ -61,7 +61,7 @@ twell_status twell_join_rms_norm(int64_t rows, int32_t cols, twell_dtype res_dty
                                  const twell_join* join, float eps, void* residual_out, twell_dtype out_dtype,
                                  void* out, uint8_t* q, float* q_scale, float* rstd, float* post_rstd, void* stream) {
   Drop drop;
-  const twell_status st = check_join(rows, cols, join, &drop);
+  twell_status st = check_join(rows, cols, join, &drop);
   if (st != TWELL_OK) return st;
   if (bad_dtype(res_dtype) || bad_dtype(y_dtype) || bad_dtype(weight_dtype) || bad_dtype(out_dtype))
     return fail(TWELL_ERR_INVALID_ARG, "dtypes must be bf16 or fp32");
@@ -81,6 +81,13 @@ twell_status twell_join_rms_norm(int64_t rows, int32_t cols, twell_dtype res_dty
   if (residual_out == nullptr && out == nullptr && q == nullptr && rstd == nullptr && post_rstd == nullptr && rows > 0)
     return fail(TWELL_ERR_INVALID_ARG, "no output is given");
   if (rows == 0) return ok();
+  st = check_apart({{residual_out, n * size_of(res_dtype)}, {out, n * size_of(out_dtype)}, {q, n},
+                    {q != nullptr ? q_scale : nullptr, (size_t)rows * 4}, {rstd, (size_t)rows * 4}, {post_rstd, (size_t)rows * 4}},
+                   {{residual == residual_out ? nullptr : residual, n * size_of(res_dtype)}, {y, n * size_of(y_dtype)},
+                    {weight, (size_t)cols * size_of(weight_dtype)},
+                    {join->post_weight, (size_t)cols * size_of(join->post_weight_dtype)},
+                    {join->gate, (size_t)join->gate_rows * cols * size_of(join->gate_dtype)}, {drop.drop != 0 ? join->rng : nullptr, 16}});
+  if (st != TWELL_OK) return st;
   twell::JoinArgs a{};
   a.rows = rows;
   a.cols = cols;
@@ -149,6 +156,14 @@ twell_status twell_join_rms_norm_bwd(int64_t rows, int32_t cols, twell_dtype d_o
   if (gate) OPS_CHECK_PTR(dgate, (size_t)gates * cols * 4, "dgate");
   const size_t need = 4 * twell::join_bwd_ws_floats(rows, cols, gates, post, gate);
   if ((st = check_ws(ws, ws_bytes, need, "workspace smaller than twell_join_rms_norm_bwd_ws says")) != TWELL_OK) return st;
+  st = check_apart({{dr, n * size_of(res_dtype)}, {dy, n * size_of(y_dtype)}, {dw, (size_t)cols * 4},
+                    {post ? dpost : nullptr, (size_t)cols * 4}, {gate ? dgate : nullptr, (size_t)gates * cols * 4}, {ws, need}},
+                   {{d_out, n * size_of(d_out_dtype)}, {d_residual, n * size_of(res_dtype)}, {residual, n * size_of(res_dtype)},
+                    {rstd, (size_t)rows * 4}, {y, n * size_of(y_dtype)}, {post ? post_rstd : nullptr, (size_t)rows * 4},
+                    {weight, (size_t)cols * size_of(weight_dtype)},
+                    {join->post_weight, (size_t)cols * size_of(join->post_weight_dtype)},
+                    {join->gate, (size_t)gates * cols * size_of(join->gate_dtype)}, {drop.drop != 0 ? join->rng : nullptr, 16}});
+  if (st != TWELL_OK) return st;
   twell::JoinBwdArgs a{};
   a.rows = rows;
   a.cols = cols;
@@ -196,6 +211,8 @@ twell_status twell_dropout(int64_t rows, int32_t cols, twell_dtype dtype, const 
   OPS_CHECK_PTR(x, bytes, "x");
   OPS_CHECK_PTR(out, bytes, "out");
   if (rows == 0) return ok();
+  st = check_apart({{out, bytes}}, {{x == out ? nullptr : x, bytes}, {rng, 16}});
+  if (st != TWELL_OK) return st;
   twell::DropoutArgs a{};
   a.rows = rows;
   a.cols = cols;

@@ -116,6 +116,10 @@ twell_status twell_linear(int64_t n, int32_t cols, int32_t units, const void* x,
   if (n == 0) return ok();
   const ForwardLayout L = forward_layout(n, cols, units);
   if ((st = check_ws(ws, ws_bytes, L.total, "workspace smaller than twell_linear_ws says")) != TWELL_OK) return st;
+  st = check_apart({{y, results * size_of(y_dtype)}, {pre, results * 2}, {ws, L.total}},
+                   {{x, (size_t)n * cols * 2}, {w, (size_t)units * cols * 2}, {bias, (size_t)units * size_of(bias_dtype)},
+                    {residual == y ? nullptr : residual, results * size_of(res_dtype)}});
+  if (st != TWELL_OK) return st;
   ok();
   char* base = static_cast<char*>(ws);
   const hipStream_t s = (hipStream_t)stream;
@@ -173,6 +177,12 @@ twell_status twell_linear_bwd(int64_t n, int32_t cols, int32_t units, twell_dtyp
   const bool d_out_bf16 = d_out_dtype == TWELL_BF16;
   const BackwardLayout L = backward_layout(n, cols, units, d_out_bf16, act, wanted);
   if ((st = check_ws(ws, ws_bytes, L.total, "workspace smaller than twell_linear_bwd_ws says")) != TWELL_OK) return st;
+  st = check_apart({{dx, (size_t)n * cols * size_of(dx_dtype)}, {dw, (size_t)units * cols * size_of(dw_dtype)}, {db, (size_t)units * 4},
+                    {ws, L.total}},
+                   {{d_out, results * size_of(d_out_dtype)}, {act != TWELL_ACT_NONE ? pre : nullptr, results * 2},
+                    {dw != nullptr ? x : nullptr, (size_t)n * cols * 2},
+                    {dx != nullptr && n > 0 ? w : nullptr, (size_t)units * cols * 2}});
+  if (st != TWELL_OK) return st;
   ok();
   char* base = static_cast<char*>(ws);
   const hipStream_t s = (hipStream_t)stream;

@@ -2,7 +2,9 @@
 // around the block. Host code.
 #pragma once
 
+#include <cstdint>
 #include <cstdio>
+#include <initializer_list>
 
 #include <hip/hip_runtime.h>
 
@@ -41,6 +43,26 @@ inline size_t size_of(twell_dtype t) { return t == TWELL_BF16 ? 2 : 4; }
 inline twell_status check_ws(void* ws, size_t have, size_t need, const char* small) {
   if (have < need) return fail(TWELL_ERR_WORKSPACE, small);
   if (twell::bad_ptr(ws, need)) return fail(TWELL_ERR_WORKSPACE, "workspace is NULL or not 16-byte aligned");
+  return TWELL_OK;
+}
+
+// Memory of an array that a call reads or writes; null: none.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+inline bool meet(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x != 0 && y != 0 && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+}
+// Refuses outputs that share memory with an input or with each other.
+inline twell_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& in : ins)
+      if (meet(*o, in)) return fail(TWELL_ERR_INVALID_ARG, "an output overlaps an input");
+    for (const Span* p = o + 1; p != outs.end(); ++p)
+      if (meet(*o, *p)) return fail(TWELL_ERR_INVALID_ARG, "outputs overlap each other");
+  }
   return TWELL_OK;
 }
 

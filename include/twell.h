@@ -453,8 +453,8 @@ twell_status twell_linear_ws(int64_t n, int32_t cols, int32_t units, size_t* ws_
  * y is rounded once to y_dtype. bias [units] of bias_dtype or NULL; residual
  * [n][units] of res_dtype or NULL; pre: NULL, or bf16 [n][units] for z, which
  * twell_linear_bwd takes. residual may be y itself when both have one type (the
- * stream updated in place); otherwise outputs may not overlap inputs or each
- * other. Any cols and units from 1 to 2^20; n == 0 is a no-op. ws: at least the
+ * stream updated in place); otherwise outputs that overlap inputs or each other
+ * are refused. Any cols and units from 1 to 2^20; n == 0 is a no-op. ws: at least the
  * queried bytes (NULL allowed when that is 0). */
 twell_status twell_linear(int64_t n, int32_t cols, int32_t units, const void* x, const void* w,
                           twell_dtype bias_dtype, const void* bias, int32_t act, twell_dtype res_dtype,
@@ -479,8 +479,8 @@ twell_status twell_linear_bwd_ws(int64_t n, int32_t cols, int32_t units, twell_d
  * db sums it unrounded. dx [n][cols] of dx_dtype, dw [units][cols] of dw_dtype, db
  * [units] fp32, each NULL when it is not wanted; sums are fp32, in a fixed order.
  * x and w may be NULL when the gradient that reads them is not wanted. Outputs
- * are fully overwritten (n == 0: dw and db are 0) and may not overlap inputs or
- * each other; dx and dw may be written at the same time. */
+ * are fully overwritten (n == 0: dw and db are 0); those that overlap inputs or
+ * each other are refused; dx and dw may be written at the same time. */
 twell_status twell_linear_bwd(int64_t n, int32_t cols, int32_t units, twell_dtype d_out_dtype, const void* d_out,
                               int32_t act, const void* pre, const void* x, const void* w, twell_dtype dx_dtype,
                               void* dx, twell_dtype dw_dtype, void* dw, float* db, void* ws, size_t ws_bytes,
@@ -502,8 +502,8 @@ twell_status twell_linear_bwd(int64_t n, int32_t cols, int32_t units, twell_dtyp
  * runs: a call recorded into a graph draws anew when the caller advances the
  * step between replays. site tells apart the places of one network. The gradient
  * is this call on the gradient, with the same p, rng and site.
- * x, out: [rows][cols] bf16 or fp32; out may be x, otherwise they may not
- * overlap. 0 <= p <= 1. Any cols from 1 to 2^30; rows == 0 is a no-op. */
+ * x, out: [rows][cols] bf16 or fp32; out may be x, any other overlap is
+ * refused. 0 <= p <= 1. Any cols from 1 to 2^30; rows == 0 is a no-op. */
 twell_status twell_dropout(int64_t rows, int32_t cols, twell_dtype dtype, const void* x, float p, const uint64_t* rng,
                            uint32_t site, void* out, void* stream);
 
@@ -533,7 +533,7 @@ typedef struct twell_join {
  * beyond fp32 has rho = 0 there, too. residual, y [rows][cols]; weight [cols].
  * residual_out, out, q (with q_scale [rows]), rstd and post_rstd (with
  * post_weight) may each be NULL, not all of them; residual_out may be
- * `residual` itself, no other output may overlap an input or another output. Any
+ * `residual` itself, any other overlap of outputs and inputs is refused. Any
  * cols from 1 to 16384; rows == 0 is a no-op. */
 twell_status twell_join_rms_norm(int64_t rows, int32_t cols, twell_dtype res_dtype, const void* residual,
                                  twell_dtype y_dtype, const void* y, twell_dtype weight_dtype, const void* weight,
@@ -555,8 +555,8 @@ twell_status twell_join_rms_norm_bwd_ws(int64_t rows, int32_t cols, int32_t post
  * dr is of res_dtype, dy of y_dtype; dw, dpost (with post_weight) [cols] and
  * dgate (with gate) [gate_rows][cols] are fp32, summed in a fixed order. The
  * codes have no gradient. d_residual may be NULL when nothing else reads the
- * stream. All outputs are fully overwritten (rows == 0: the sums are 0); none may
- * overlap an input or another output. ws: at least the queried bytes. */
+ * stream. All outputs are fully overwritten (rows == 0: the sums are 0); those
+ * that overlap an input or another output are refused. ws: at least the queried bytes. */
 twell_status twell_join_rms_norm_bwd(int64_t rows, int32_t cols, twell_dtype d_out_dtype, const void* d_out,
                                      twell_dtype res_dtype, const void* d_residual, const void* residual,
                                      const float* rstd, twell_dtype y_dtype, const void* y, const float* post_rstd,

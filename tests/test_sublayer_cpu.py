@@ -210,6 +210,30 @@ def test_linear_backward_refusals(kw, code, word):
     assert word in tw.lib().twell_last_error()
 
 
+def _apart(call, outputs, inputs, may=(), **given):
+    """Each output that begins where an input or an output before it does, or 16 bytes behind, is refused; `may` are pairs that
+    may be one and the same array."""
+    at = {name: 0x1000000 * (i + 1) for i, name in enumerate((*outputs, *inputs))}
+    address = lambda **moved: {n: ctypes.c_void_p(moved.get(n, a)) for n, a in at.items()}  # noqa: E731
+    for i, out in enumerate(outputs):
+        for other in (*inputs, *outputs[:i]):
+            for shift in (0, 16):
+                if shift == 0 and (out, other) in may:
+                    continue
+                assert call(**{**given, **address(**{out: at[other] + shift})}) == 1, (out, other, shift)
+                assert b"overlap" in tw.lib().twell_last_error(), (out, other, shift)
+
+
+def test_outputs_that_overlap_are_refused():
+    _apart(_dropout, ["out"], ["x"], [("out", "x")])
+    assert _dropout(rng=ctypes.c_void_p(0x2000000), out=ctypes.c_void_p(0x2000000)) == 1
+    _apart(_join, ["ro", "o", "q", "rstd", "prstd"], ["r", "y", "w", "post_weight", "gate"], [("ro", "r")], rows=64,
+           qs=ctypes.c_void_p(0xF0000000))
+    _apart(_join_bwd, ["dr", "dy", "dw", "dp", "dg", "ws"], ["g", "ds", "r", "rstd", "y", "prstd", "w", "post_weight", "gate"])
+    _apart(_linear, ["y", "pre", "ws"], ["x", "w", "bias", "res"], [("y", "res")], n=100, cols=1 << 10)
+    _apart(_linear_bwd, ["dx", "dw", "db", "ws"], ["g", "pre", "x", "w"])
+
+
 def test_calls_of_no_rows_need_no_device():
     for st in (_dropout(rows=0, x=None, out=None), _join(rows=0, r=None, y=None, ro=None, o=None, gate_rows=5),
                _linear(n=0, x=None, res=None, y=None, ws=None, nb=0), _linear_bwd(n=0, g=None, pre=None, x=None, dx=None, dw=None, db=None)):
