@@ -156,10 +156,12 @@ hipError_t launch_cfg(const LinearArgs& a, hipStream_t s) {
 
 template <int ACT>
 hipError_t launch_act(const LinearArgs& a, hipStream_t s) {
-  if (a.out.rows <= 8) return launch_cfg<1, 1, 8, 4, ACT>(a, s);
-  if (a.out.rows <= 16) return launch_cfg<1, 2, 8, 4, ACT>(a, s);
-  if (a.out.rows <= 24) return launch_cfg<1, 3, 8, 2, ACT>(a, s);
-  return launch_cfg<1, 4, 8, 3, ACT>(a, s);
+  switch (linear_direct_groups(a.out.rows, a.k, a.out.units)) {
+    case 1: return launch_cfg<1, 1, 8, 4, ACT>(a, s);
+    case 2: return launch_cfg<1, 2, 8, 4, ACT>(a, s);
+    case 3: return launch_cfg<1, 3, 8, 2, ACT>(a, s);
+    default: return launch_cfg<1, 4, 8, 3, ACT>(a, s);
+  }
 }
 
 }  // namespace

@@ -378,12 +378,41 @@ inline double linear_tile_us(LinearTileSize tile, int64_t rows, int64_t k, int u
   const double join = splits > 1 ? 2.5 + 8.0 * splits * rows * units / 5.5e6 : 0;
   return 3.5 + (body > reads ? body : reads) + n * end + join;
 }
-// Straight from memory: w once, and 8 lines of x for every 8 rows and 16 units
-// (measured: 8, 16, 24, 32 x 4096 x 11008 16.6, 20.5, 23.3, 26.8; x 5632 x 2048
-// 6.1, 7.6, 8.7, 9.8; the tiles of few rows take 22 and 13).
-inline double linear_direct_us(int64_t rows, int64_t k, int units) {
-  const double groups = (units + 15) / 16 / 256.0, steps = (double)((k + 63) / 64);
-  return 2.5 + 2.0 * k * units / 8.6e6 + (groups > 1 ? groups : 1) * steps * 8 * ((rows + 7) / 8) * 0.0022;
+// Straight from memory a workgroup takes 16 units by 8, 16, 24 or 32 rows and loads
+// the lines of both (of 64 columns each): what counts is how many the busiest
+// compute unit loads, and how often it begins anew, which costs as much as 800
+// of them (200 x 512 x 2048 in four rounds of workgroups 9.2 us, in tiles 7.3).
+// Lines that begin at any element touch two cache lines, and with 32 rows of them
+// the loads in flight no longer cover it.
+inline int64_t linear_direct_lines(int64_t rows, int64_t k, int units, bool any, int groups) {
+  const int64_t tiles = ((rows + 8 * groups - 1) / (8 * groups)) * ((units + 15) / 16);
+  const int64_t lines = 8 * (2 + groups), cost = any ? groups == 4 ? lines * 5 / 2 : lines * 7 / 4 : lines;
+  return (tiles + 255) / 256 * (cost * ((k + 63) / 64) + 800);
+}
+// Groups of 8 rows of a workgroup: those with the fewest lines on the busiest
+// compute unit, and among them the most (24 x 5632 x 2048 in 128 workgroups of 24
+// rows 9.0 us, in 256 of 16 8.0; 32 x 2048 x 1000 in 63 of 32 6.4, in 252 of 8 4.0).
+inline int linear_direct_groups(int64_t rows, int64_t k, int units) {
+  const int all = rows < 32 ? (int)((rows + 7) / 8) : 4;
+  int best = all;
+  for (int g = all - 1; g >= 1; --g)
+    if (linear_direct_lines(rows, k, units, k % 8 != 0, g) < linear_direct_lines(rows, k, units, k % 8 != 0, best)) best = g;
+  return best;
+}
+// Estimate (us): w from memory and the lines, one mostly behind the other.
+// Measured, best tiles : straight from memory (k x units, rows):
+//                  24           32           64           96
+//   2048 x 1000                              11.8 : 4.4   11.6 : 4.9
+//   5632 x 2048                 13.5 : 8.2   15.3 : 10.4  15.7 : 13.8
+//   4096 x 4096                              16.0 : 13.7  16.3 : 18.3
+//   8192 x 700     15.2 : 6.8   15.3 : 6.9   15.8 : 8.6   15.9 : 10.0
+//   4096 x 11008   24.2 : 18.5  24.5 : 21.3  25.5 : 33.4  28.0 : 44.8
+//   11008 x 4096   28.3 : 19.5  29.6 : 22.1  30.4 : 30.3  31.1 : 41.0
+constexpr int64_t kLinearDirectRows = 512;  // beyond, tiles of 64 rows and more read w less often
+inline double linear_direct_us(int64_t rows, int64_t k, int units, bool any) {
+  const double lines = 0.00144 * linear_direct_lines(rows, k, units, any, linear_direct_groups(rows, k, units));
+  const double weights = 2.0 * k * units / 6e6;
+  return 1.1 + (lines > weights ? lines + 0.3 * weights : weights + 0.3 * lines);
 }
 // Lines that begin at any element (`any`; of p, with LINEAR_ROWS of both
 // operands) go through registers on their way to LDS, or are copied first, which
@@ -392,7 +421,7 @@ inline LinearPlan linear_plan(LinearLayout layout, int64_t rows, int64_t k, int 
   if (rows == 0 || k == 0) return {LINEAR_FEW, 1, false, 0};  // nothing is launched
   const int64_t stages = (k + kLinearStage - 1) / kLinearStage;
   LinearPlan best{LINEAR_DIRECT, 1, false, 0};
-  double least = layout == LINEAR_ROWS && rows <= 32 ? linear_direct_us(rows, k, units) : 1e30;
+  double least = layout == LINEAR_ROWS && rows <= kLinearDirectRows ? linear_direct_us(rows, k, units, any) : 1e30;
   const double copied = layout == LINEAR_ROWS ? (double)k * (rows + units) : (double)k * units;
   const double pad_us = any ? (layout == LINEAR_ROWS ? 5 : 2.5) + 4 * copied / 5e6 : 0;
   const bool short_lines = (layout == LINEAR_ROWS ? k : units) < 8;

@@ -40,6 +40,9 @@ FEW = [(1, 1, 1), (1, 8, 8), (1, 64, 16), (1, 4096, 1000), (2, 7, 5), (3, 100, 3
        (24, 1999, 130), (32, 1024, 256), (33, 640, 64), (47, 999, 257), (64, 520, 96)]
 TILES = [(65, 1, 1), (65, 8, 129), (100, 64, 100), (128, 128, 128), (129, 63, 127), (200, 72, 300), (256, 192, 256), (300, 1000, 77),
          (130, 130, 640), (500, 4096, 200), (1000, 200, 1001), (513, 1990, 515)]
+# of 64 rows
+LOW = [(513, 1, 1), (513, 8, 129), (600, 64, 100), (640, 128, 128), (577, 63, 127), (520, 72, 300), (768, 192, 256), (600, 1000, 77),
+       (514, 130, 640), (1000, 4096, 200), (600, 200, 1001)]
 BIG = [(4100, 64, 4200), (4096, 128, 4096), (4001, 137, 4111), (4353, 200, 4097)]
 
 
@@ -68,14 +71,14 @@ def _exact_case(rows, cols, units, bias, res, y, pre, act="relu"):
     assert torch.equal(out, want.to(y))
 
 
-@pytest.mark.parametrize("rows,cols,units", FEW + TILES + BIG)
+@pytest.mark.parametrize("rows,cols,units", FEW + TILES + LOW + BIG)
 def test_products_of_whole_numbers_are_exact(rows, cols, units):
     require_gpu()
     for k, (bias, res, y) in enumerate(((None, None, F32), (F32, BF, BF), (BF, F32, F32), (BF, None, BF))):
         _exact_case(rows, cols, units, bias, res, y, k % 2 == 1, act="none" if k == 2 else "relu")
 
 
-@pytest.mark.parametrize("rows,cols,units", [(1, 1000, 257), (24, 5632, 200), (50, 999, 130), (200, 1990, 260), (300, 4096, 129), (4100, 72, 4200)])
+@pytest.mark.parametrize("rows,cols,units", [(1, 1000, 257), (24, 5632, 200), (600, 1990, 260), (700, 4096, 129), (50, 999, 130), (200, 1990, 260), (300, 4096, 129), (4100, 72, 4200)])
 @pytest.mark.parametrize("act", list(tw.ACTS))
 def test_forward(rows, cols, units, act):
     require_gpu()
@@ -92,7 +95,7 @@ def test_forward(rows, cols, units, act):
         assert torch.equal(got, tw.linear(x, w, bias=b, act=act, residual=r, dtype=y))  # the same bits without pre, again
 
 
-@pytest.mark.parametrize("rows", [1, 40, 130])
+@pytest.mark.parametrize("rows", [1, 40, 130, 600])
 @pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
 def test_far_and_special_pre_activations(act, rows):
     """Values that leave exp's range, infinities and NaN."""
@@ -108,7 +111,7 @@ def test_far_and_special_pre_activations(act, rows):
     assert bool((got[:, -2] == float("inf")).all()) and bool(got[:, -1].isnan().all())
 
 
-@pytest.mark.parametrize("rows,cols,units", [(1, 512, 1000), (24, 999, 200), (300, 256, 300), (300, 4096, 129), (4100, 128, 4200)])
+@pytest.mark.parametrize("rows,cols,units", [(1, 512, 1000), (600, 256, 300), (600, 4096, 129), (24, 999, 200), (300, 256, 300), (300, 4096, 129), (4100, 128, 4200)])
 def test_residual_in_place(rows, cols, units):
     require_gpu()
     gen = _gen(3)
@@ -207,7 +210,7 @@ def test_no_rows(cols, units):
     assert bool((got.dw == 0).all()) and bool((got.db == 0).all())
 
 
-@pytest.mark.parametrize("rows,cols,units", [(9, 300, 40), (140, 300, 40), (140, 303, 41)])
+@pytest.mark.parametrize("rows,cols,units", [(9, 300, 40), (140, 300, 40), (140, 303, 41), (600, 300, 40), (600, 303, 41)])
 def test_non_finite_operands_stay_in_their_rows(rows, cols, units):
     """NaN and infinity in a row of x reach that row alone, in w that unit alone, k behind the last none."""
     require_gpu()
@@ -233,7 +236,7 @@ def test_streams_and_graphs():
     require_gpu()
     gen = _gen(8)
     sets = []
-    for rows, cols, units in ((300, 4096, 129), (24, 1000, 640)):
+    for rows, cols, units in ((600, 4096, 129), (300, 4096, 129), (24, 1000, 640)):
         x, w = _randn(gen, rows, cols, dtype=BF), _randn(gen, units, cols, scale=0.05, dtype=BF)
         sets.append((x, w, _randn(gen, units), _randn(gen, rows, units, dtype=BF)))
 
@@ -262,4 +265,4 @@ def test_streams_and_graphs():
         for t, out in zip(sets, outs):
             for a, c in zip(out, step(*t)):
                 assert torch.equal(a, c)
-    assert len(first) == 2
+    assert len(first) == len(sets)

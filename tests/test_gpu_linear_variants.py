@@ -16,8 +16,12 @@ pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
 
+# straight from memory: 8, 16, 24 and 32 rows a workgroup, one and several of them, lines of every kind
+DIRECT = [(9, 64, 40), (17, 1000, 2049), (30, 520, 1500), (39, 1001, 2100), (50, 999, 2048), (50, 1000, 2048), (70, 2047, 1999),
+          (96, 2048, 1000), (90, 5, 1000), (100, 7, 4000), (250, 72, 1100), (24, 5632, 2048), (40, 2048, 4096)]
 # rows, k, units of the product
-ROWS = [(33, 7, 64), (33, 8, 64), (33, 73, 64), (33, 1000, 64), (33, 1001, 64), (4100, 8, 500), (1000, 73, 2056), (3000, 2000, 129),
+ROWS = DIRECT + [(600, 7, 64), (600, 8, 64), (600, 73, 64), (600, 1000, 64), (600, 1001, 64),
+        (33, 7, 64), (33, 8, 64), (33, 73, 64), (33, 1000, 64), (33, 1001, 64), (4100, 8, 500), (1000, 73, 2056), (3000, 2000, 129),
         (2100, 4001, 129), (1500, 200, 4104), (1500, 129, 4104), (300, 8192, 4000), (2000, 131073, 129), (4100, 200, 3000),
         (4353, 1000, 4097), (1500, 8192, 3000), (3000, 2001, 4105), (8000, 513, 8000)]
 OTHERS = [(33, 8, 64), (33, 8, 7), (33, 8, 100), (33, 1000, 64), (33, 1000, 100), (1000, 8, 2056), (4100, 8, 500), (4100, 4001, 64),
@@ -100,7 +104,7 @@ def test_both_gradient_products_at_a_time(n, cols, units, dx_type, dw_type):
 
 
 # one size for each tile, of aligned lines and of lines at any element
-EPILOGUES = [(33, 72, 200), (100, 73, 203), (1000, 72, 2056), (1000, 73, 2059), (1500, 200, 4104), (1500, 129, 4103), (4100, 200, 3000)]
+EPILOGUES = [(50, 72, 2056), (70, 73, 2001), (600, 72, 200), (600, 73, 203), (33, 72, 200), (100, 73, 203), (1000, 72, 2056), (1000, 73, 2059), (1500, 200, 4104), (1500, 129, 4103), (4100, 200, 3000)]
 
 
 @pytest.mark.parametrize("rows,cols,units", EPILOGUES)

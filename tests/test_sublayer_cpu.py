@@ -230,7 +230,7 @@ def test_outputs_that_overlap_are_refused():
     _apart(_join, ["ro", "o", "q", "rstd", "prstd"], ["r", "y", "w", "post_weight", "gate"], [("ro", "r")], rows=64,
            qs=ctypes.c_void_p(0xF0000000))
     _apart(_join_bwd, ["dr", "dy", "dw", "dp", "dg", "ws"], ["g", "ds", "r", "rstd", "y", "prstd", "w", "post_weight", "gate"])
-    _apart(_linear, ["y", "pre", "ws"], ["x", "w", "bias", "res"], [("y", "res")], n=100, cols=1 << 10)
+    _apart(_linear, ["y", "pre", "ws"], ["x", "w", "bias", "res"], [("y", "res")], n=600, cols=1 << 10)
     _apart(_linear_bwd, ["dx", "dw", "db", "ws"], ["g", "pre", "x", "w"])
 
 
