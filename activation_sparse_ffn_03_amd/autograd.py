@@ -20,6 +20,12 @@ backward calls. Capacities for overflow rows (a tile count above S) and
 dense-backup rows (more than row_cap entries) are fractions of N; by
 default a call that exceeds one raises TwellError after a host sync of the
 status word (check=False skips the sync and leaves such rows uncomputed).
+
+A training step through these functions is captured into a HIP graph only
+where no autograd graph of the same parameters that was recorded eagerly is
+still alive (drop its loss and outputs first): torch adds their gradients on
+the stream of that graph, which the capture does not hold, and the process
+may end.
 """
 from __future__ import annotations
 
