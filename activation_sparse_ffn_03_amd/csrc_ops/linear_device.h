@@ -83,9 +83,11 @@ __device__ __forceinline__ void load_some(const void* base, int is_bf16, int64_t
     }
   }
 }
-// STREAM marks the store as one of data that is not read again soon: a large
+// STREAM marks a store of bf16 as one of data that is not read again soon: a large
 // product's results then leave the operands' lines in L2 (16384 x 4096 x 11008
-// 1071 -> 1007 us, 8192 x 8192 x 8192 815 -> 785).
+// 1071 -> 1007 us, 8192 x 8192 x 8192 815 -> 785). It is for whole cache lines:
+// parts of them, and the two halves that a lane's fp32 are stored in, have to be
+// brought together in L2.
 template <int N, bool STREAM = false>
 __device__ __forceinline__ void store_some(void* base, int is_bf16, int64_t at, int have, const float (&v)[N]) {
   if (is_bf16) {
@@ -108,8 +110,7 @@ __device__ __forceinline__ void store_some(void* base, int is_bf16, int64_t at, 
 #pragma unroll
       for (int k = 0; k < N; k += 4) {
         const f32x4_t q = {v[k], v[k + 1], v[k + 2], v[k + 3]};
-        if constexpr (STREAM) __builtin_nontemporal_store(q, reinterpret_cast<f32x4_a4_t*>(p + k));
-        else *reinterpret_cast<f32x4_a4_t*>(p + k) = q;
+        *reinterpret_cast<f32x4_a4_t*>(p + k) = q;
       }
     } else {
 #pragma unroll

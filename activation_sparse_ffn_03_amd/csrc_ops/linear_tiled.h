@@ -215,7 +215,7 @@ struct LinearSide {
 // lie in branches the compiler waits for everything, the stores too (61000
 // cycles a tile of 256 x 256, a fifth of 8192 x 8192 x 8192). At the result's
 // edges each lane looks at what there is.
-template <class C, int ACT, bool RES, bool WHOLE>
+template <class C, int ACT, bool RES, bool WHOLE, bool STREAM>
 __device__ __forceinline__ void linear_store(const LinearOut& o, const f32x16_t (&acc)[C::FU][C::FT], int64_t row0,
                                              int unit0, char* out) {
   const int lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5;
@@ -284,7 +284,7 @@ __device__ __forceinline__ void linear_store(const LinearOut& o, const f32x16_t 
             add[k] = __uint_as_float(o.res_bf16 ? b : raw[k >> 2][k & 3]);
           }
         }
-        finish_units<ACT, 8, true>(o, first + 8 * r + (lane >> 3), unit0 + 64 * i + col, 8, z, bias[i], add);
+        finish_units<ACT, 8, STREAM>(o, first + 8 * r + (lane >> 3), unit0 + 64 * i + col, 8, z, bias[i], add);
       }
     } else {
       const int unit = unit0 + 64 * i + col;
@@ -301,7 +301,7 @@ __device__ __forceinline__ void linear_store(const LinearOut& o, const f32x16_t 
           for (int e = 0; e < 4; ++e) z[k + e] = v[e], add[k + e] = 0.f;
         }
         if constexpr (RES) load_some<8>(o.residual, o.res_bf16, at * o.units + unit, o.units - unit, add);
-        finish_units<ACT, 8, true>(o, at, unit, o.units - unit, z, bias[i], add);
+        finish_units<ACT, 8, STREAM>(o, at, unit, o.units - unit, z, bias[i], add);
       }
     }
     asm volatile("" ::: "memory");
@@ -533,8 +533,10 @@ __device__ __forceinline__ void linear_items(const LinearArgs& a, uint32_t tb, u
     const int unit0 = cur.unit0 + wu * FU * 32;
     char* out = smem + 2 * C::STAGE + wave * C::OUT;
     const bool whole = row0 + FT * 32 <= a.out.rows && unit0 + FU * 32 <= a.out.units;
-    if (whole) linear_store<C, ACT, RES, true>(o, acc, row0, unit0, out);
-    else linear_store<C, ACT, RES, false>(o, acc, row0, unit0, out);
+    // rows of whole cache lines
+    if (whole && a.out.units % 64 == 0) linear_store<C, ACT, RES, true, true>(o, acc, row0, unit0, out);
+    else if (whole) linear_store<C, ACT, RES, true, false>(o, acc, row0, unit0, out);
+    else linear_store<C, ACT, RES, false, false>(o, acc, row0, unit0, out);
     if (!more) break;
     // at the result's edges some have nothing to store, and may not have been issued
     stores = whole;
